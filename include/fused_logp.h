@@ -563,6 +563,46 @@ flp_status logp_grpo_loss_counted(const float* logp, const float* old_logp, cons
                                   flp_stream_t stream);
 
 /*
+ * The norm in front of the LM head: layer norm, or RMS norm when center == 0.
+ * For each row x of width d (sums in FP32, one rounding to x's dtype):
+ *   mu = mean(x) (0 when center == 0), var = mean((x - mu)^2),
+ *   rstd = (var + eps)^(-1/2), xh = (x - mu) rstd, y = xh weight + bias.
+ * Forward:
+ *   x      [n, ld_x] of `dtype`, y [n, ld_y] of the same dtype (y may be x
+ *          itself with ld_y == ld_x; any other overlap is FLP_EINVAL)
+ *   weight, bias  [d] of weight_dtype (x's dtype or FP32), or NULL (1 and 0)
+ *   mean, rstd    [n] FP32 out for the backward, or NULL (mean is not written
+ *          when center == 0)
+ * Backward, with g = dy weight:
+ *   dx = rstd (g - mean(g) - xh mean(g xh))  (no mean(g) when center == 0)
+ *   dweight = sum over rows of dy xh, dbias = sum over rows of dy
+ *   dy     [n, ld_dy] of dy_dtype: x's dtype or FP32 (the dhidden of
+ *          fused_linear_logp_backward is FP32)
+ *   mean (NULL allowed when center == 0), rstd  from the forward
+ *   dx     [n, ld_dx] of x's dtype, not overlapping x or dy
+ *   dweight, dbias  [d] FP32 out, or NULL when not wanted; with `accumulate`
+ *          they are added to (gradient accumulation over micro-batches)
+ *   workspace  fused_layer_norm_backward_workspace_size(d) bytes, 16-byte
+ *          aligned, caller-owned, no initial contents needed (the partial
+ *          sums of dweight and dbias); may be NULL without both
+ * A row's y, mean, rstd and dx depend on that row (and the vectors) only;
+ * dweight and dbias are summed in an order fixed by n, d and the layout, so
+ * repeated calls give identical bits.  Rows may have any alignment and any
+ * stride >= d.  n == 0 writes empty sums (zeros, unless accumulating).
+ * Errors: FLP_EINVAL for a bad dtype, extent, stride, eps or overlap;
+ * FLP_EUNSUPPORTED for d >= 2^31.
+ */
+flp_status fused_layer_norm_forward(const void* x, int dtype, int64_t n, int64_t d, int64_t ld_x,
+                                    const void* weight, const void* bias, int weight_dtype, float eps, int center,
+                                    void* y, int64_t ld_y, float* mean, float* rstd, flp_stream_t stream);
+flp_status fused_layer_norm_backward_workspace_size(int64_t d, int64_t* bytes);
+flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy, const void* x, int dtype, int64_t n,
+                                     int64_t d, int64_t ld_x, const void* weight, int weight_dtype, const float* mean,
+                                     const float* rstd, int center, void* workspace, int64_t workspace_bytes, void* dx,
+                                     int64_t ld_dx, float* dweight, float* dbias, int accumulate,
+                                     flp_stream_t stream);
+
+/*
  * Health of the device side (no counterpart in the pages: a guard of this
  * library's own waits).  The bulk-copy forward waits on its own copies with a
  * bounded wait (about 2 s); if one runs out, the kernel records it in a

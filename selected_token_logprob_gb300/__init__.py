@@ -34,13 +34,16 @@ from __future__ import annotations
 import torch
 
 from . import _lib
+from ._args import _cuda, _dtype, _mask, _opt_ptr, _rows, _stream, _vec
 from ._lib import FusedLogpError
+from .norm import (FusedLayerNorm, fused_layer_norm, fused_layer_norm_backward,
+                   fused_layer_norm_backward_workspace_size, fused_layer_norm_forward)
 
 IGNORE_INDEX = -100
 NUM_TILES = 16
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 __all__ = [
+    "FusedLayerNorm",
     "FusedLinearLogp",
     "FusedLogp",
     "FusedLogpError",
@@ -50,6 +53,10 @@ __all__ = [
     "flp_selftest_ex2_bias",
     "flp_selftest_wait_timeout",
     "flp_tile_width",
+    "fused_layer_norm",
+    "fused_layer_norm_backward",
+    "fused_layer_norm_backward_workspace_size",
+    "fused_layer_norm_forward",
     "fused_logp",
     "fused_logp_backward",
     "fused_logp_forward",
@@ -75,51 +82,9 @@ __all__ = [
 GRPO_MODES = {"token_mean": 0, "seq_mean_token_mean": 1, "seq_mean_token_sum": 2}
 
 
-def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
-
-
-def _rows(x: torch.Tensor, name: str):
-    """(n, v, ld) of a 2-D tensor whose rows are contiguous."""
-    if x.dim() != 2:
-        raise ValueError(f"{name} must be 2-D [N, V], got shape {tuple(x.shape)}")
-    n, v = x.shape
-    if v > 1 and x.stride(1) != 1:
-        raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
-    ld = x.stride(0) if n > 1 else max(v, x.stride(0))
-    if ld < v:
-        raise ValueError(f"{name} row stride {ld} is smaller than its width {v}")
-    return n, v, ld
-
-
-def _vec(t: torch.Tensor, name: str, n: int, dtype: torch.dtype) -> None:
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name} must have shape [{n}], got {tuple(t.shape)}")
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _cuda(*ts) -> None:
-    for t in ts:
-        if not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors")
-
-
 def flp_tile_width(v: int) -> int:
     """Tile width W = 8 * ceil(v / 128) of a v-column vocabulary."""
     return int(_lib.load().flp_tile_width(int(v)))
-
-
-def _opt_ptr(t: torch.Tensor | None) -> int | None:
-    return None if t is None else t.data_ptr()
-
-
-def _dtype(x: torch.Tensor, name: str) -> int:
-    if x.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
-    return _DTYPES[x.dtype]
 
 
 def _inv_temperature(temperature: float) -> float:
@@ -127,17 +92,6 @@ def _inv_temperature(temperature: float) -> float:
     if not (t > 0.0) or t == float("inf"):
         raise ValueError(f"temperature must be finite and > 0, got {temperature}")
     return 1.0 / t   # rounded to binary32 at the C boundary
-
-
-def _mask(active_mask: torch.Tensor | None, n: int) -> int | None:
-    if active_mask is None:
-        return None
-    if active_mask.dtype not in (torch.bool, torch.uint8):
-        raise TypeError("active_mask must be bool or uint8")
-    if active_mask.dim() != 1 or active_mask.shape[0] != n or (n > 1 and active_mask.stride(0) != 1):
-        raise ValueError(f"active_mask must be a contiguous [{n}] tensor")
-    _cuda(active_mask)
-    return active_mask.data_ptr()
 
 
 def fused_logp_forward(logits: torch.Tensor, targets: torch.Tensor,

@@ -1,0 +1,60 @@
+"""Argument checks and marshalling shared by the binding's modules."""
+
+from __future__ import annotations
+
+import torch
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _stream(t: torch.Tensor) -> int:
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _rows(x: torch.Tensor, name: str):
+    """(n, v, ld) of a 2-D tensor whose rows are contiguous."""
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D [N, V], got shape {tuple(x.shape)}")
+    n, v = x.shape
+    if v > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
+    ld = x.stride(0) if n > 1 else max(v, x.stride(0))
+    if ld < v:
+        raise ValueError(f"{name} row stride {ld} is smaller than its width {v}")
+    return n, v, ld
+
+
+def _vec(t: torch.Tensor, name: str, n: int, dtype: torch.dtype) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must have shape [{n}], got {tuple(t.shape)}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _cuda(*ts) -> None:
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors")
+
+
+def _opt_ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _dtype(x: torch.Tensor, name: str) -> int:
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    return _DTYPES[x.dtype]
+
+
+def _mask(active_mask: torch.Tensor | None, n: int) -> int | None:
+    if active_mask is None:
+        return None
+    if active_mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("active_mask must be bool or uint8")
+    if active_mask.dim() != 1 or active_mask.shape[0] != n or (n > 1 and active_mask.stride(0) != 1):
+        raise ValueError(f"active_mask must be a contiguous [{n}] tensor")
+    _cuda(active_mask)
+    return active_mask.data_ptr()

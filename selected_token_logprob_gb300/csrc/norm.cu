@@ -1,0 +1,206 @@
+// Host side of the norm in front of the LM head (fused_layer_norm_forward,
+// fused_layer_norm_backward): argument checks and launches.
+#include <math.h>
+
+#include "host_common.h"
+#include "norm_kernels.cuh"
+
+using namespace flp_host;
+
+namespace {
+
+constexpr int64_t kNormMaxDim = ((int64_t)1 << 31) - 1;
+
+flp_status check_norm_shape(int64_t n, int64_t d, int dtype) {
+    flp_status st;
+    if ((st = check_dtype(dtype)) != FLP_OK) return st;
+    if (n < 0) return fail(FLP_EINVAL, "n must be >= 0 (got %lld)", (long long)n);
+    if (d < 1) return fail(FLP_EINVAL, "d must be >= 1 (got %lld)", (long long)d);
+    if (d > kNormMaxDim) return fail(FLP_EUNSUPPORTED, "d must be below 2^31 (got %lld)", (long long)d);
+    return FLP_OK;
+}
+
+// A vector's or gradient's dtype: the rows' own or FP32.
+flp_status check_side_dtype(const char* name, int side, int dtype) {
+    if (side != dtype && side != FLP_DTYPE_F32)
+        return fail(FLP_EINVAL, "%s dtype must be x's (%d) or FLP_DTYPE_F32 (got %d)", name, dtype, side);
+    return FLP_OK;
+}
+
+struct Extent {
+    const char* name;
+    const void* p;
+    int64_t bytes;
+};
+
+// The output `o` must not share bytes with the input `i`, unless it lies on
+// it exactly and `same` allows that.
+flp_status check_apart(const Extent& o, const Extent& i, bool same) {
+    if (o.p == nullptr || i.p == nullptr || (same && o.p == i.p)) return FLP_OK;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(o.p), b = reinterpret_cast<uintptr_t>(i.p);
+    if (a < b + (uintptr_t)i.bytes && b < a + (uintptr_t)o.bytes)
+        return fail(FLP_EINVAL, "%s overlaps %s", o.name, i.name);
+    return FLP_OK;
+}
+
+int norm_row_grid(int64_t n, int sms) {
+    const int64_t most = (int64_t)sms * 8;
+    return (int)(n < most ? n : most);
+}
+
+template <class T>
+void launch_norm_fwd(const flp::NormFwdArgs& a, bool center, int sms, cudaStream_t s) {
+    const int grid = norm_row_grid(a.n, sms);
+    if (center) flp::k_norm_fwd_any<T, true><<<grid, flp::kNormAnyThreads, 0, s>>>(a);
+    else flp::k_norm_fwd_any<T, false><<<grid, flp::kNormAnyThreads, 0, s>>>(a);
+}
+
+template <class T, class G, bool kCenter>
+flp_status launch_norm_bwd_c(const flp::NormBwdArgs& a, int sms, cudaStream_t s) {
+    flp_status st;
+    flp::k_norm_dx_any<T, G, kCenter><<<norm_row_grid(a.n, sms), flp::kNormAnyThreads, 0, s>>>(a);
+    if ((st = check_launch("norm dx")) != FLP_OK) return st;
+    if (a.part_w || a.part_b) {
+        const dim3 grid((unsigned)ceil_div(a.d, flp::kNormAnyThreads), flp::kNormParts);
+        flp::k_norm_dw_any<T, G, kCenter><<<grid, flp::kNormAnyThreads, 0, s>>>(a);
+        if ((st = check_launch("norm dw")) != FLP_OK) return st;
+    }
+    return FLP_OK;
+}
+
+template <class T, class G>
+flp_status launch_norm_bwd(const flp::NormBwdArgs& a, bool center, int sms, cudaStream_t s) {
+    return center ? launch_norm_bwd_c<T, G, true>(a, sms, s) : launch_norm_bwd_c<T, G, false>(a, sms, s);
+}
+
+bool norm_workspace_bytes(int64_t d, int64_t* out) {
+    int64_t b;
+    if (__builtin_mul_overflow(d, (int64_t)(2 * flp::kNormParts * 4), &b)) return false;
+    *out = ceil_div(b, 256) * 256;
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+flp_status fused_layer_norm_forward(const void* x, int dtype, int64_t n, int64_t d, int64_t ld_x,
+                                    const void* weight, const void* bias, int weight_dtype, float eps, int center,
+                                    void* y, int64_t ld_y, float* mean, float* rstd, flp_stream_t stream) {
+    flp_status st;
+    if ((st = check_norm_shape(n, d, dtype)) != FLP_OK) return st;
+    if ((st = check_side_dtype("weight", weight_dtype, dtype)) != FLP_OK) return st;
+    if (ld_x < d || ld_y < d)
+        return fail(FLP_EINVAL, "ld_x (%lld) and ld_y (%lld) must be >= d (%lld)", (long long)ld_x, (long long)ld_y,
+                    (long long)d);
+    if (!(eps >= 0.f) || !isfinite(eps)) return fail(FLP_EINVAL, "eps must be finite and >= 0 (got %g)", (double)eps);
+    if (n == 0) return ok();
+    const int eb = elem_bytes(dtype);
+    int64_t bx, by;
+    if (!span_bytes(n, d, ld_x, eb, &bx) || !span_bytes(n, d, ld_y, eb, &by))
+        return fail(FLP_EINVAL, "x or y extent overflows int64");
+    const Extent ey{"y", y, by};
+    if ((st = check_apart(ey, {"x", x, bx}, ld_x == ld_y)) != FLP_OK) return st;
+    const void* ptrs[] = {x, y, weight, bias, mean, rstd};
+    const char* names[] = {"x", "y", "weight", "bias", "mean", "rstd"};
+    const bool optional[] = {false, false, true, true, true, true};
+    int dev;
+    if ((st = common_device(6, ptrs, names, optional, &dev)) != FLP_OK) return st;
+    if (dev < 0 || dev >= kMaxDevices) return fail(FLP_ECUDA, "device index %d out of range", dev);
+    DeviceGuard guard;
+    if ((st = guard.enter(dev)) != FLP_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return fail(FLP_ECUDA, "could not read the SM count of device %d", dev);
+    const flp::NormFwdArgs a{x, n, d, ld_x, {weight, weight_dtype}, {bias, weight_dtype}, eps, 1.f / (float)d,
+                             y, ld_y, mean, rstd};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == FLP_DTYPE_BF16) launch_norm_fwd<__nv_bfloat16>(a, center != 0, sms, s);
+    else if (dtype == FLP_DTYPE_F16) launch_norm_fwd<__half>(a, center != 0, sms, s);
+    else launch_norm_fwd<float>(a, center != 0, sms, s);
+    return check_launch("norm forward");
+}
+
+flp_status fused_layer_norm_backward_workspace_size(int64_t d, int64_t* bytes) {
+    if (bytes == nullptr) return fail(FLP_EINVAL, "bytes is a null pointer");
+    if (d < 1) return fail(FLP_EINVAL, "d must be >= 1 (got %lld)", (long long)d);
+    if (!norm_workspace_bytes(d, bytes)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    return ok();
+}
+
+flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy, const void* x, int dtype, int64_t n,
+                                     int64_t d, int64_t ld_x, const void* weight, int weight_dtype, const float* mean,
+                                     const float* rstd, int center, void* workspace, int64_t workspace_bytes, void* dx,
+                                     int64_t ld_dx, float* dweight, float* dbias, int accumulate,
+                                     flp_stream_t stream) {
+    flp_status st;
+    if ((st = check_norm_shape(n, d, dtype)) != FLP_OK) return st;
+    if ((st = check_side_dtype("weight", weight_dtype, dtype)) != FLP_OK) return st;
+    if ((st = check_side_dtype("dy", dy_dtype, dtype)) != FLP_OK) return st;
+    if (ld_x < d || ld_dy < d || ld_dx < d)
+        return fail(FLP_EINVAL, "ld_x (%lld), ld_dy (%lld) and ld_dx (%lld) must be >= d (%lld)", (long long)ld_x,
+                    (long long)ld_dy, (long long)ld_dx, (long long)d);
+    const bool sums = dweight != nullptr || dbias != nullptr;
+    if (n == 0 && !sums) return ok();
+    int64_t need = 0;
+    if (!norm_workspace_bytes(d, &need)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    if (sums && n > 0) {
+        if (workspace_bytes < need)
+            return fail(FLP_EINVAL, "workspace_bytes (%lld) is below the %lld bytes needed",
+                        (long long)workspace_bytes, (long long)need);
+        if (!aligned16(workspace)) return fail(FLP_EINVAL, "workspace must start on a 16-byte boundary");
+    }
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int dev;
+    if (n == 0) {
+        // no rows: the sums are empty
+        const void* ptrs[] = {dweight, dbias};
+        const char* names[] = {"dweight", "dbias"};
+        const bool optional[] = {true, true};
+        if ((st = common_device(2, ptrs, names, optional, &dev)) != FLP_OK) return st;
+        DeviceGuard guard;
+        if ((st = guard.enter(dev)) != FLP_OK) return st;
+        cudaError_t e = cudaSuccess;
+        if (!accumulate && dweight) e = cudaMemsetAsync(dweight, 0, (size_t)d * 4, s);
+        if (e == cudaSuccess && !accumulate && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)d * 4, s);
+        if (e != cudaSuccess) return fail(FLP_ECUDA, "norm backward: %s", cudaGetErrorString(e));
+        return ok();
+    }
+    const int eb = elem_bytes(dtype), gb = elem_bytes(dy_dtype);
+    int64_t bx, bg, bd;
+    if (!span_bytes(n, d, ld_x, eb, &bx) || !span_bytes(n, d, ld_dy, gb, &bg) || !span_bytes(n, d, ld_dx, eb, &bd))
+        return fail(FLP_EINVAL, "x, dy or dx extent overflows int64");
+    const Extent ed{"dx", dx, bd};
+    if ((st = check_apart(ed, {"x", x, bx}, false)) != FLP_OK) return st;
+    if ((st = check_apart(ed, {"dy", dy, bg}, false)) != FLP_OK) return st;
+    const void* ptrs[] = {dy, x, rstd, dx, mean, weight, dweight, dbias, workspace};
+    const char* names[] = {"dy", "x", "rstd", "dx", "mean", "weight", "dweight", "dbias", "workspace"};
+    const bool optional[] = {false, false, false, false, center == 0, true, true, true, !sums};
+    if ((st = common_device(9, ptrs, names, optional, &dev)) != FLP_OK) return st;
+    if (dev < 0 || dev >= kMaxDevices) return fail(FLP_ECUDA, "device index %d out of range", dev);
+    DeviceGuard guard;
+    if ((st = guard.enter(dev)) != FLP_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return fail(FLP_ECUDA, "could not read the SM count of device %d", dev);
+    float* ws = static_cast<float*>(workspace);
+    flp::NormBwdArgs a{dy, ld_dy, x, n, d, ld_x, {weight, weight_dtype}, mean, rstd, 1.f / (float)d, dx, ld_dx,
+                       dweight ? ws : nullptr, dbias ? ws + (int64_t)flp::kNormParts * d : nullptr};
+    const bool c = center != 0, wide = dy_dtype == FLP_DTYPE_F32;
+    if (dtype == FLP_DTYPE_BF16)
+        st = wide ? launch_norm_bwd<__nv_bfloat16, float>(a, c, sms, s)
+                  : launch_norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, c, sms, s);
+    else if (dtype == FLP_DTYPE_F16)
+        st = wide ? launch_norm_bwd<__half, float>(a, c, sms, s) : launch_norm_bwd<__half, __half>(a, c, sms, s);
+    else
+        st = launch_norm_bwd<float, float>(a, c, sms, s);
+    if (st != FLP_OK) return st;
+    const int fold = (int)ceil_div(d, flp::kNormFoldCols);
+    if (dweight)
+        flp::k_norm_fold<<<fold, flp::kNormFoldCols * flp::kNormFoldRows, 0, s>>>(a.part_w, flp::kNormParts, d, dweight,
+                                                                                   accumulate != 0);
+    if (dbias)
+        flp::k_norm_fold<<<fold, flp::kNormFoldCols * flp::kNormFoldRows, 0, s>>>(a.part_b, flp::kNormParts, d, dbias,
+                                                                                   accumulate != 0);
+    return check_launch("norm backward");
+}
+
+}  // extern "C"

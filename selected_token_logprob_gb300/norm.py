@@ -1,0 +1,157 @@
+"""The norm in front of the LM head: layer norm or, with ``center=False``, RMS
+norm; forward, backward with the weight's and bias's gradients, autograd."""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._args import _cuda, _dtype, _opt_ptr, _rows, _stream, _vec
+
+
+def _affine(weight, bias, x, d: int) -> int:
+    """The C dtype of weight and bias (x's when neither is given)."""
+    given = [(name, t) for name, t in (("weight", weight), ("bias", bias)) if t is not None]
+    for name, t in given:
+        if t.dtype not in (x.dtype, torch.float32):
+            raise TypeError(f"{name} must be {x.dtype} or torch.float32, got {t.dtype}")
+        if t.dtype != given[0][1].dtype:
+            raise TypeError("weight and bias must have the same dtype")
+        _vec(t, name, d, t.dtype)
+        _cuda(t)
+    return _dtype(given[0][1] if given else x, "weight")
+
+
+def fused_layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None,
+                             bias: torch.Tensor | None = None, eps: float = 1e-5, center: bool = True,
+                             y: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                             rstd: torch.Tensor | None = None):
+    """(y [N, D] of x's dtype, mean FP32 [N] or None, rstd FP32 [N]) of the
+    rows of x [N, D]: y = (x - mean) * rstd * weight + bias.  With
+    ``center=False`` no mean is taken (RMS norm; mean is None).  weight and
+    bias [D] have x's dtype or FP32.  ``y`` may be ``x`` (in place)."""
+    n, d, ld = _rows(x, "x")
+    dt = _dtype(x, "x")
+    wdt = _affine(weight, bias, x, d)
+    if not 0.0 <= float(eps) < float("inf"):
+        raise ValueError(f"eps must be finite and >= 0, got {eps}")
+    dev = x.device
+    y = torch.empty((n, d), dtype=x.dtype, device=dev) if y is None else y
+    if y.dtype != x.dtype or tuple(y.shape) != (n, d):
+        raise ValueError("y must have x's dtype and shape")
+    _, _, ld_y = _rows(y, "y")
+    if center and mean is None:
+        mean = torch.empty(n, dtype=torch.float32, device=dev)
+    rstd = torch.empty(n, dtype=torch.float32, device=dev) if rstd is None else rstd
+    _cuda(x, y, rstd)
+    _vec(rstd, "rstd", n, torch.float32)
+    if center:
+        _vec(mean, "mean", n, torch.float32)
+        _cuda(mean)
+    if n > 0:
+        st = _lib.load().fused_layer_norm_forward(
+            x.data_ptr(), dt, n, d, ld, _opt_ptr(weight), _opt_ptr(bias), wdt, float(eps), int(bool(center)),
+            y.data_ptr(), ld_y, _opt_ptr(mean) if center else None, rstd.data_ptr(), _stream(x))
+        _lib.check("fused_layer_norm_forward", st)
+    return y, (mean if center else None), rstd
+
+
+def fused_layer_norm_backward_workspace_size(d: int) -> int:
+    """Bytes of device scratch that fused_layer_norm_backward needs for the
+    partial sums of the weight's and bias's gradients."""
+    b = ctypes.c_int64(0)
+    _lib.check("fused_layer_norm_backward_workspace_size",
+               _lib.load().fused_layer_norm_backward_workspace_size(int(d), ctypes.byref(b)))
+    return int(b.value)
+
+
+def fused_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None,
+                              mean: torch.Tensor | None, rstd: torch.Tensor, center: bool = True,
+                              with_dweight: bool = True, with_dbias: bool = True,
+                              dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                              dbias: torch.Tensor | None = None, accumulate: bool = False,
+                              workspace: torch.Tensor | None = None):
+    """(dx [N, D] of x's dtype, dweight FP32 [D], dbias FP32 [D]) of the norm
+    for the upstream gradient dy [N, D] (x's dtype, or FP32 as
+    ``fused_linear_logp_backward`` returns its dhidden), from the forward's
+    mean and rstd.  dweight / dbias are None when not wanted; with
+    ``accumulate`` the given ones are added to, not overwritten."""
+    n, d, ld = _rows(x, "x")
+    dt = _dtype(x, "x")
+    wdt = _affine(weight, None, x, d)
+    if dy.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"dy must be {x.dtype} or torch.float32, got {dy.dtype}")
+    if tuple(dy.shape) != (n, d):
+        raise ValueError(f"dy must have x's shape {(n, d)}, got {tuple(dy.shape)}")
+    _, _, ld_dy = _rows(dy, "dy")
+    _vec(rstd, "rstd", n, torch.float32)
+    if center:
+        if mean is None:
+            raise ValueError("center=True needs the forward's mean")
+        _vec(mean, "mean", n, torch.float32)
+        _cuda(mean)
+    dev = x.device
+    dx = torch.empty((n, d), dtype=x.dtype, device=dev) if dx is None else dx
+    if dx.dtype != x.dtype or tuple(dx.shape) != (n, d):
+        raise ValueError("dx must have x's dtype and shape")
+    _, _, ld_dx = _rows(dx, "dx")
+    if accumulate and ((with_dweight and dweight is None) or (with_dbias and dbias is None)):
+        raise ValueError("accumulate needs the dweight and dbias tensors to add to")
+    if with_dweight and dweight is None:
+        dweight = torch.empty(d, dtype=torch.float32, device=dev)
+    if with_dbias and dbias is None:
+        dbias = torch.empty(d, dtype=torch.float32, device=dev)
+    dweight, dbias = (dweight if with_dweight else None), (dbias if with_dbias else None)
+    for name, t in (("dweight", dweight), ("dbias", dbias)):
+        if t is not None:
+            _vec(t, name, d, torch.float32)
+            _cuda(t)
+    _cuda(dy, x, rstd, dx)
+    if workspace is None and n > 0 and (with_dweight or with_dbias):
+        workspace = torch.empty(fused_layer_norm_backward_workspace_size(d), dtype=torch.uint8, device=dev)
+    wptr, wbytes = None, 0
+    if workspace is not None:
+        _cuda(workspace)
+        wptr, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = _lib.load().fused_layer_norm_backward(
+        dy.data_ptr(), _dtype(dy, "dy"), ld_dy, x.data_ptr(), dt, n, d, ld, _opt_ptr(weight), wdt,
+        _opt_ptr(mean) if center else None, rstd.data_ptr(), int(bool(center)), wptr, wbytes, dx.data_ptr(), ld_dx,
+        _opt_ptr(dweight), _opt_ptr(dbias), int(bool(accumulate)), _stream(x))
+    _lib.check("fused_layer_norm_backward", st)
+    return dx, dweight, dbias
+
+
+class FusedLayerNorm(torch.autograd.Function):
+    """y = FusedLayerNorm.apply(x, weight, bias, eps, center); saves x, the
+    weight and the rows' FP32 statistics."""
+
+    @staticmethod
+    def forward(ctx, x, weight=None, bias=None, eps=1e-5, center=True):
+        y, mean, rstd = fused_layer_norm_forward(x, weight, bias, eps=eps, center=center)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.center = center
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        n, d = dy.shape
+        if (d > 1 and dy.stride(1) != 1) or (n > 1 and dy.stride(0) < d):
+            dy = dy.contiguous()   # a broadcast or transposed gradient
+        dx, dw, db = fused_layer_norm_backward(
+            dy, x, weight, mean, rstd, center=ctx.center,
+            with_dweight=weight is not None and ctx.needs_input_grad[1],
+            with_dbias=ctx.bias_dtype is not None and ctx.needs_input_grad[2])
+        dw = dw if dw is None else dw.to(weight.dtype)
+        db = db if db is None else db.to(ctx.bias_dtype)
+        return dx, dw, db, None, None
+
+
+def fused_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                     eps: float = 1e-5, center: bool = True) -> torch.Tensor:
+    """Autograd-aware layer norm (RMS norm with ``center=False``) of the rows
+    of x [N, D]."""
+    return FusedLayerNorm.apply(x, weight, bias, eps, center)

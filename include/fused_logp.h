@@ -603,6 +603,54 @@ flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy
                                      flp_stream_t stream);
 
 /*
+ * Preference loss of pairs of packed sequences on the logp path.  Sequence s
+ * is tokens [cu_seqlens[s], cu_seqlens[s + 1]) (int64 on the device, num_seqs
+ * + 1 of them, num_seqs = 2 P even); pair p is (chosen, rejected) =
+ * (2 p, 2 p + 1) with FLP_PREF_INTERLEAVED, (p, p + P) with FLP_PREF_HALVES.
+ * Over the active tokens (active_mask byte nonzero, or all when NULL) of s,
+ *   r_s = sum of logp - ref_logp (ref_logp NULL: of logp), divided by their
+ *         number n_s with `average`;
+ *   h = r_chosen - r_rejected, u = beta h - margin, and the pair's loss
+ * kind FLP_PREF_SIGMOID: -(1 - e) log sigma(u) - e log sigma(-u), e =
+ *                        label_smoothing
+ *      FLP_PREF_HINGE:   max(0, 1 - u)
+ *      FLP_PREF_IPO:     (h - 1 / (2 beta))^2 (no margin)
+ * A pair is live when both its sequences have an active token; other pairs
+ * (padding) count nowhere.  D = the number of live pairs, or normalizer when
+ * that is > 0 (e.g. a count global to all micro-batches).
+ *   loss     [1] FP32 out: the live pairs' sum / D (0 without live pairs)
+ *   grad     [n] FP32 out: d loss / d logp, the upstream gradient for the
+ *            logp backward (+-(dl/dh) / D, / n_s with `average`); 0 for
+ *            tokens that are inactive, outside every sequence or in a pair
+ *            that is not live
+ *   rewards  [P, 2] FP32 out: beta r_chosen, beta r_rejected (0 for a
+ *            sequence without active tokens)
+ *   workspace  logp_preference_loss_workspace_size(n, num_seqs) bytes,
+ *            16-byte aligned, caller-owned, no initial contents needed; one
+ *            workspace serves one call at a time.
+ * logp and ref_logp are never used where the mask is 0 (they may hold NaN or
+ * infinities there).  Sums are FP32 within 256-token chunks and FP64 over
+ * them, in an order fixed by the layout: repeated calls give identical bits.
+ * Bounds in cu_seqlens are clamped to [0, n]; when they decrease, the result
+ * is unspecified, but every access stays inside the arrays.
+ * Errors: FLP_EINVAL for an odd or too large num_seqs, a bad kind or layout,
+ * beta not finite and positive, label_smoothing outside [0, 1] or nonzero
+ * without the sigmoid, a margin not finite or nonzero with ipo, or a bad
+ * normalizer or workspace.
+ */
+#define FLP_PREF_SIGMOID 0
+#define FLP_PREF_HINGE 1
+#define FLP_PREF_IPO 2
+#define FLP_PREF_INTERLEAVED 0
+#define FLP_PREF_HALVES 1
+flp_status logp_preference_loss_workspace_size(int64_t n, int64_t num_seqs, int64_t* bytes);
+flp_status logp_preference_loss(const float* logp, const float* ref_logp, const uint8_t* active_mask,
+                                const int64_t* cu_seqlens, int64_t num_seqs, int64_t n, int kind, int layout,
+                                int average, float beta, float label_smoothing, float margin, float normalizer,
+                                void* workspace, int64_t workspace_bytes, float* loss, float* grad, float* rewards,
+                                flp_stream_t stream);
+
+/*
  * Health of the device side (no counterpart in the pages: a guard of this
  * library's own waits).  The bulk-copy forward waits on its own copies with a
  * bounded wait (about 2 s); if one runs out, the kernel records it in a

@@ -38,6 +38,8 @@ from ._args import _cuda, _dtype, _mask, _opt_ptr, _rows, _stream, _vec
 from ._lib import FusedLogpError
 from .norm import (FusedLayerNorm, fused_layer_norm, fused_layer_norm_backward,
                    fused_layer_norm_backward_workspace_size, fused_layer_norm_forward)
+from .preference import (PREFERENCE_KINDS, PREFERENCE_LAYOUTS, logp_preference_loss,
+                         logp_preference_loss_workspace_size)
 
 IGNORE_INDEX = -100
 NUM_TILES = 16
@@ -49,6 +51,8 @@ __all__ = [
     "FusedLogpError",
     "IGNORE_INDEX",
     "NUM_TILES",
+    "PREFERENCE_KINDS",
+    "PREFERENCE_LAYOUTS",
     "flp_device_error",
     "flp_selftest_ex2_bias",
     "flp_selftest_wait_timeout",
@@ -76,6 +80,8 @@ __all__ = [
     "logp_grpo_loss_workspace_size",
     "logp_merge_gathered_partials",
     "logp_merge_partials",
+    "logp_preference_loss",
+    "logp_preference_loss_workspace_size",
     "logp_shard_backward",
     "logp_shard_partials",
 ]

@@ -1,0 +1,133 @@
+// Host side of the preference loss (logp_preference_loss): argument checks,
+// workspace layout and launches.
+#include <math.h>
+
+#include "host_common.h"
+#include "preference_kernels.cuh"
+
+using namespace flp_host;
+
+namespace {
+
+// Byte offsets of the workspace's parts; false when they overflow.
+struct PrefLayout {
+    int64_t part_loss, part_live, slots, first_seq, coef, total;
+};
+
+bool pref_layout(int64_t n, int64_t nseq, PrefLayout* l) {
+    const int64_t nchunks = n / flp::kPrefChunk + (n % flp::kPrefChunk != 0);
+    int64_t slots, b;
+    if (__builtin_add_overflow(nchunks, nseq, &slots) || slots > INT64_MAX / 32) return false;
+    l->part_loss = 256;   // the ticket and 1 / D
+    l->part_live = l->part_loss + 8 * flp::kPrefPairCtas;
+    l->slots = l->part_live + 8 * flp::kPrefPairCtas;
+    l->first_seq = l->slots + 8 * slots;
+    l->coef = l->first_seq + 4 * nchunks;
+    if (__builtin_add_overflow(l->coef, 4 * nseq + 255, &b)) return false;
+    l->total = b / 256 * 256;
+    return true;
+}
+
+flp_status check_pref_counts(int64_t n, int64_t num_seqs) {
+    if (n < 0) return fail(FLP_EINVAL, "n must be >= 0 (got %lld)", (long long)n);
+    if (num_seqs < 0 || num_seqs >= INT32_MAX || num_seqs % 2 != 0)
+        return fail(FLP_EINVAL, "num_seqs must be even and in [0, 2^31 - 1) (got %lld)", (long long)num_seqs);
+    return FLP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+flp_status logp_preference_loss_workspace_size(int64_t n, int64_t num_seqs, int64_t* bytes) {
+    if (bytes == nullptr) return fail(FLP_EINVAL, "bytes is a null pointer");
+    flp_status st;
+    if ((st = check_pref_counts(n, num_seqs)) != FLP_OK) return st;
+    PrefLayout l;
+    if (!pref_layout(n, num_seqs, &l)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    *bytes = l.total;
+    return ok();
+}
+
+flp_status logp_preference_loss(const float* logp, const float* ref_logp, const uint8_t* active_mask,
+                                const int64_t* cu_seqlens, int64_t num_seqs, int64_t n, int kind, int layout,
+                                int average, float beta, float label_smoothing, float margin, float normalizer,
+                                void* workspace, int64_t workspace_bytes, float* loss, float* grad, float* rewards,
+                                flp_stream_t stream) {
+    flp_status st;
+    if ((st = check_pref_counts(n, num_seqs)) != FLP_OK) return st;
+    if (kind < FLP_PREF_SIGMOID || kind > FLP_PREF_IPO) return fail(FLP_EINVAL, "kind must be 0, 1 or 2 (got %d)", kind);
+    if (layout != FLP_PREF_INTERLEAVED && layout != FLP_PREF_HALVES)
+        return fail(FLP_EINVAL, "layout must be 0 or 1 (got %d)", layout);
+    if (!(beta > 0.f) || !isfinite(beta)) return fail(FLP_EINVAL, "beta must be finite and > 0 (got %g)", (double)beta);
+    if (!(label_smoothing >= 0.f && label_smoothing <= 1.f) || (kind != FLP_PREF_SIGMOID && label_smoothing != 0.f))
+        return fail(FLP_EINVAL, "label_smoothing must be in [0, 1], and 0 unless the kind is sigmoid (got %g)",
+                    (double)label_smoothing);
+    if (!isfinite(margin) || (kind == FLP_PREF_IPO && margin != 0.f))
+        return fail(FLP_EINVAL, "margin must be finite, and 0 for the ipo kind (got %g)", (double)margin);
+    if (!(normalizer >= 0.f) || !isfinite(normalizer))
+        return fail(FLP_EINVAL, "normalizer must be finite and >= 0 (got %g)", (double)normalizer);
+    PrefLayout l;
+    if (!pref_layout(n, num_seqs, &l)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    if (workspace_bytes < l.total)
+        return fail(FLP_EINVAL, "workspace_bytes (%lld) is below the %lld bytes needed", (long long)workspace_bytes,
+                    (long long)l.total);
+    if (!aligned16(workspace)) return fail(FLP_EINVAL, "workspace must start on a 16-byte boundary");
+    const bool tokens = n > 0, seqs = num_seqs > 0;
+    const void* ptrs[] = {loss, workspace, tokens ? logp : nullptr, tokens ? grad : nullptr,
+                          seqs ? cu_seqlens : nullptr, seqs ? rewards : nullptr, tokens ? ref_logp : nullptr,
+                          tokens ? active_mask : nullptr};
+    const char* names[] = {"loss", "workspace", "logp", "grad", "cu_seqlens", "rewards", "ref_logp", "active_mask"};
+    const bool optional[] = {false, false, !tokens, !tokens, !seqs, !seqs, true, true};
+    int dev;
+    if ((st = common_device(8, ptrs, names, optional, &dev)) != FLP_OK) return st;
+    if (dev < 0 || dev >= kMaxDevices) return fail(FLP_ECUDA, "device index %d out of range", dev);
+    DeviceGuard guard;
+    if ((st = guard.enter(dev)) != FLP_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return fail(FLP_ECUDA, "could not read the SM count of device %d", dev);
+    flp::PrefArgs a;
+    a.logp = logp;
+    a.ref = ref_logp;
+    a.mask = active_mask;
+    a.cu = cu_seqlens;
+    a.n = n;
+    a.nseq = num_seqs;
+    a.nchunks = ceil_div(n, flp::kPrefChunk);
+    a.kind = kind;
+    a.average = average != 0;
+    a.halves = layout == FLP_PREF_HALVES;
+    a.beta = beta;
+    a.smooth = label_smoothing;
+    a.margin = margin;
+    a.normalizer = normalizer;
+    a.loss = loss;
+    a.grad = grad;
+    a.rewards = rewards;
+    char* base = static_cast<char*>(workspace);
+    a.ticket = reinterpret_cast<unsigned*>(base);
+    a.inv_den = reinterpret_cast<float*>(base + 16);
+    a.part_loss = reinterpret_cast<double*>(base + l.part_loss);
+    a.part_live = reinterpret_cast<int64_t*>(base + l.part_live);
+    a.slots = reinterpret_cast<flp::PrefSlot*>(base + l.slots);
+    a.first_seq = reinterpret_cast<int32_t*>(base + l.first_seq);
+    a.coef = reinterpret_cast<float*>(base + l.coef);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool vec = aligned16(logp) && aligned16(ref_logp) && aligned16(grad) &&
+                     (reinterpret_cast<uintptr_t>(active_mask) & 3u) == 0;
+    constexpr int kWarps = flp::kPrefThreads / 32;
+    const int64_t most = (int64_t)sms * 8;
+    const int64_t ctas = a.nchunks <= kWarps ? 1 : ceil_div(a.nchunks, kWarps);
+    const int grid = (int)(ctas < most ? ctas : most);
+    (vec ? flp::k_pref_sums<true> : flp::k_pref_sums<false>)<<<grid, flp::kPrefThreads, 0, s>>>(a);
+    if ((st = check_launch("preference sums")) != FLP_OK) return st;
+    int64_t pgrid = ceil_div(num_seqs / 2, kWarps);
+    pgrid = pgrid < 1 ? 1 : (pgrid > flp::kPrefPairCtas ? flp::kPrefPairCtas : pgrid);
+    if ((st = launch_dependent("preference pairs", flp::k_pref_pairs, (int)pgrid, flp::kPrefThreads, s, a)) != FLP_OK)
+        return st;
+    if (n == 0) return ok();
+    return launch_dependent("preference grad", vec ? flp::k_pref_grad<true> : flp::k_pref_grad<false>, grid,
+                            flp::kPrefThreads, s, a);
+}
+
+}  // extern "C"

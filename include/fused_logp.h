@@ -651,6 +651,43 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
                                 flp_stream_t stream);
 
 /*
+ * Orthogonalised update: Newton-Schulz products on the tensor cores.  For each
+ * matrix G [rows, cols] of a batch (e.g. the momentum of a weight, or of a
+ * stack of equal weights),
+ *   X = G / (|G|_F + eps);  `steps` times, with the step's (a, b, c):
+ *   A = X X^T,  X <- a X + (b A + c A^2) X      (A on the smaller side)
+ *   out = scale X
+ * which brings every singular value of G near 1 (with the usual quintic
+ * coefficients (3.4445, -4.7750, 2.0315) and 5 steps into about 0.7 .. 1.2)
+ * and keeps its singular vectors.
+ *   x        `dtype` (BF16, FP16 or FP32) [batch] matrices stride_x elements
+ *            apart, rows ld_x elements apart (stride_x is not read for one
+ *            matrix)
+ *   coefficients  HOST pointer to steps x 3 floats; they should keep singular
+ *            values in [0, 1] below 2 (FP16 overflows where an entry of X,
+ *            X X^T or b A + c A^2 passes 255)
+ *   out      out_dtype BF16 or FP32, ld_out, stride_out; may be x itself or
+ *            overlap it (x is read before out is written)
+ *   workspace  flp_orthogonalize_workspace_size(batch, rows, cols) bytes,
+ *            128-byte aligned, caller-owned, no initial contents needed
+ * The products run on FP16 operands with FP32 accumulators; X is carried as
+ * two FP16 numbers (22 bits) and the diagonals of A and b A + c A^2 in FP32, so
+ * that out is within about 1e-3 (of its norm) of the result in 64 bits also
+ * where G has few large singular values over a small floor.  The sum of squares
+ * is FP32 within a row (entries between about 1e-19 and 1e17 in size).  A zero
+ * matrix gives zeros; an infinity or NaN makes its matrix NaN.  Deterministic;
+ * a matrix's bits do not depend on the rest of the batch.
+ * Errors: FLP_EINVAL for a bad dtype, extent, stride, steps, coefficient, eps,
+ * scale or workspace; FLP_EUNSUPPORTED for a smaller side above 65536 or sizes
+ * beyond the 32-bit coordinates of the tensor maps.
+ */
+flp_status flp_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols, int64_t* bytes);
+flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t rows, int64_t cols, int64_t ld_x,
+                             int64_t stride_x, int steps, const float* coefficients, float eps, float scale,
+                             void* workspace, int64_t workspace_bytes, void* out, int out_dtype, int64_t ld_out,
+                             int64_t stride_out, flp_stream_t stream);
+
+/*
  * Health of the device side (no counterpart in the pages: a guard of this
  * library's own waits).  The bulk-copy forward waits on its own copies with a
  * bounded wait (about 2 s); if one runs out, the kernel records it in a

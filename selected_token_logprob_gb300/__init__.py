@@ -38,6 +38,7 @@ from ._args import _cuda, _dtype, _mask, _opt_ptr, _rows, _stream, _vec
 from ._lib import FusedLogpError
 from .norm import (FusedLayerNorm, fused_layer_norm, fused_layer_norm_backward,
                    fused_layer_norm_backward_workspace_size, fused_layer_norm_forward)
+from .newton_schulz import ORTHOGONALIZE_COEFFICIENTS, orthogonalize, orthogonalize_workspace_size
 from .preference import (PREFERENCE_KINDS, PREFERENCE_LAYOUTS, logp_preference_loss,
                          logp_preference_loss_workspace_size)
 
@@ -51,6 +52,7 @@ __all__ = [
     "FusedLogpError",
     "IGNORE_INDEX",
     "NUM_TILES",
+    "ORTHOGONALIZE_COEFFICIENTS",
     "PREFERENCE_KINDS",
     "PREFERENCE_LAYOUTS",
     "flp_device_error",
@@ -84,6 +86,8 @@ __all__ = [
     "logp_preference_loss_workspace_size",
     "logp_shard_backward",
     "logp_shard_partials",
+    "orthogonalize",
+    "orthogonalize_workspace_size",
 ]
 GRPO_MODES = {"token_mean": 0, "seq_mean_token_mean": 1, "seq_mean_token_sum": 2}
 

@@ -82,6 +82,10 @@ SIGNATURES = {
     "logp_preference_loss": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                             ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float, _P, _I64,
                                             _P, _P, _P, _P]),
+    "flp_orthogonalize_workspace_size": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_I64)]),
+    "flp_orthogonalize": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, ctypes.c_int,
+                                         ctypes.POINTER(ctypes.c_float), ctypes.c_float, ctypes.c_float, _P, _I64, _P,
+                                         ctypes.c_int, _I64, _I64, _P]),
     "flp_device_error": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_int)]),
     "flp_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int, _I64, ctypes.POINTER(ctypes.c_int)]),
     "flp_selftest_ex2_bias": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_double),

@@ -1314,7 +1314,7 @@ static flp_status grpo_impl(GrpoStage stage, const float* logp, const float* old
         //    count on the device when that ran before it
         auto fix = al(active_mask, 16) ? flp::k_grpo_fix<true> : flp::k_grpo_fix<false>;
         if (nranges > 0) {
-            if ((st = launch_dependent("grpo counts", fix, (int)nfix, flp::kGrpoFixThreads, s, a, wk, range,
+            if ((st = launch_dependent("grpo counts", fix, (int)nfix, flp::kGrpoFixThreads, (size_t)0, s, a, wk, range,
                                        nranges)) != FLP_OK)
                 return st;
         } else {
@@ -1337,7 +1337,7 @@ static flp_status grpo_impl(GrpoStage stage, const float* logp, const float* old
         if (reuse) {
             kern<<<(int)grid, flp::kGrpoPassThreads, 0, s>>>(a, wk, (int)nfix);
             if ((st = check_launch("grpo pass")) != FLP_OK) return st;
-        } else if ((st = launch_dependent("grpo pass", kern, (int)grid, flp::kGrpoPassThreads, s, a, wk,
+        } else if ((st = launch_dependent("grpo pass", kern, (int)grid, flp::kGrpoPassThreads, (size_t)0, s, a, wk,
                                           (int)nfix)) != FLP_OK) {
             return st;
         }
@@ -1384,8 +1384,10 @@ flp_status flp_device_error(int device, int* code) {
     int v = 0, zero = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, flp::g_device_error, sizeof v);
     if (e == cudaSuccess) e = cudaMemcpyToSymbol(flp::g_device_error, &zero, sizeof zero);
+    int orth = 0;   // the orthogonalisation's kernels, in a source of their own, have a word of their own
+    if (e == cudaSuccess) e = flp_take_orthogonalize_error(&orth);
     if (e != cudaSuccess) return fail(FLP_ECUDA, "device error word: %s", cudaGetErrorString(e));
-    *code = v;
+    *code = v | orth;
     return ok();
 }
 

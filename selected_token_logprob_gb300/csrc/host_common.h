@@ -13,6 +13,10 @@
 
 #include "fused_logp.h"
 
+// Reads and clears the error word of the orthogonalisation's bounded waits on
+// the current device (orthogonalize.cu).
+cudaError_t flp_take_orthogonalize_error(int* code);
+
 namespace flp_host {
 
 inline thread_local char g_msg[512] = "";
@@ -157,16 +161,16 @@ inline EncodeTiledFn encode_tiled() {
     return fn;
 }
 
-// Launches kern<<<grid, block, 0, s>>>(args...) with programmatic stream
+// Launches kern<<<grid, block, smem, s>>>(args...) with programmatic stream
 // serialization: the kernel may start while the previous work on s runs and
 // waits for it with griddepcontrol.wait.
 template <class... Args>
-inline flp_status launch_dependent(const char* what, void (*kern)(Args...), int grid, int block, cudaStream_t s,
-                            Args... args) {
+inline flp_status launch_dependent(const char* what, void (*kern)(Args...), int grid, int block, size_t smem,
+                                   cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)block);
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,0 +1,230 @@
+// Host side of the Newton-Schulz orthogonalisation (flp_orthogonalize):
+// argument checks, workspace layout, tensor maps and launches.
+#include <math.h>
+
+#include "host_common.h"
+#include "ortho_kernels.cuh"
+
+using namespace flp_host;
+
+namespace {
+
+struct OrthLayout {
+    int64_t m, n, mp, np;              // of X: the matrix or its transpose, m <= n
+    int64_t parts, d, e, hi0, hi1, lo, a0, b0, total;   // byte offsets
+};
+
+bool orth_layout(int64_t batch, int64_t rows, int64_t cols, OrthLayout* l) {
+    l->m = rows < cols ? rows : cols;
+    l->n = rows < cols ? cols : rows;
+    l->mp = ceil_div(l->m, 64) * 64;
+    l->np = ceil_div(l->n, 64) * 64;
+    int64_t all_rows, x, a;
+    if (__builtin_mul_overflow(batch, l->mp, &all_rows) || __builtin_mul_overflow(all_rows, l->np * 2, &x) ||
+        __builtin_mul_overflow(all_rows, l->mp * 2, &a))
+        return false;
+    if (x > INT64_MAX / 16 || a > INT64_MAX / 16) return false;
+    auto up = [](int64_t v) { return ceil_div(v, 1024) * 1024; };
+    l->parts = 0;
+    l->d = up(batch * flp::kOrthParts * 8);
+    l->e = l->d + up(all_rows * 4);
+    l->hi0 = l->e + up(all_rows * 4);
+    l->hi1 = l->hi0 + up(x);
+    l->lo = l->hi1 + up(x);
+    l->a0 = l->lo + up(x);
+    l->b0 = l->a0 + up(a);
+    l->total = l->b0 + up(a);
+    return true;
+}
+
+flp_status check_orth_shape(int64_t batch, int64_t rows, int64_t cols) {
+    if (batch < 0 || rows < 0 || cols < 0)
+        return fail(FLP_EINVAL, "batch, rows and cols must be >= 0 (got %lld, %lld, %lld)", (long long)batch,
+                    (long long)rows, (long long)cols);
+    const int64_t lo = rows < cols ? rows : cols, hi = rows < cols ? cols : rows;
+    const int64_t kMax = ((int64_t)1 << 31) - 1;
+    // tensor-map coordinates and launch grids are 32-bit
+    if (hi > kMax - 512 || lo > 65536 || (lo > 0 && batch > (kMax - 512) / (ceil_div(lo, 64) * 64)) ||
+        batch > kMax / flp::kOrthParts)
+        return fail(FLP_EUNSUPPORTED, "the smaller side must be <= 65536 and batch times it below 2^31");
+    if (hi > 0 && batch > 0 &&
+        (long double)batch * ceil_div(lo, 64) * 2.0L * ceil_div(hi, 64) * 2.0L > (long double)kMax)
+        return fail(FLP_EUNSUPPORTED, "batch * rows * cols is too large");
+    return FLP_OK;
+}
+
+// Tensor map of an FP16 row-major [rows, cols] matrix without padding between
+// rows: boxes of 64 columns x box_rows rows, 128-byte swizzle, zero fill.
+flp_status orth_tmap(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, uint32_t box_rows) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return fail(FLP_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FLP_EINVAL, "tensor map rejected by the driver (error %d)", (int)r);
+    return FLP_OK;
+}
+
+constexpr int kBN = 128;
+
+flp_status orth_setup(int dev) {
+    static std::atomic<bool> ready[kMaxDevices];
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const int bytes = (int)flp::kOrthSmemBytes<kBN>;
+        const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        cudaError_t e = cudaFuncSetAttribute(flp::k_orth_product<flp::kOrthGram, kBN>, attr, bytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(flp::k_orth_product<flp::kOrthPoly, kBN>, attr, bytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(flp::k_orth_product<flp::kOrthApply, kBN>, attr, bytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(flp::k_orth_product<flp::kOrthFinal, kBN>, attr, bytes);
+        if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize setup: %s", cudaGetErrorString(e));
+        ready[dev].store(true, std::memory_order_release);
+    }
+    return FLP_OK;
+}
+
+template <int kMode>
+flp_status orth_product(int sms, const CUtensorMap& tm_a, const CUtensorMap& tm_b, flp::OrthArgs p, cudaStream_t s) {
+    constexpr bool kSym = kMode == flp::kOrthGram || kMode == flp::kOrthPoly;
+    p.tiles_m = (int)ceil_div(p.mp, flp::kOrthBM);
+    p.tiles_n = (int)ceil_div(kSym ? p.mp : p.np, kBN);
+    p.units = p.batch * (kSym ? (int64_t)p.tiles_m * (p.tiles_m + 1) / 2 : (int64_t)p.tiles_m * p.tiles_n);
+    p.nkb = (int)((kMode == flp::kOrthGram ? p.np : p.mp) / flp::kOrthBK);
+    const int grid = (int)(p.units < sms ? p.units : sms);
+    return launch_dependent("orthogonalize product", flp::k_orth_product<kMode, kBN>, grid, flp::kOrthThreads,
+                            flp::kOrthSmemBytes<kBN>, s, tm_a, tm_b, p);
+}
+
+}  // namespace
+
+cudaError_t flp_take_orthogonalize_error(int* code) {
+    int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, flp::g_orth_error, sizeof v);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(flp::g_orth_error, &zero, sizeof zero);
+    *code = v;
+    return e;
+}
+
+extern "C" {
+
+flp_status flp_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols, int64_t* bytes) {
+    if (bytes == nullptr) return fail(FLP_EINVAL, "bytes is a null pointer");
+    flp_status st;
+    if ((st = check_orth_shape(batch, rows, cols)) != FLP_OK) return st;
+    OrthLayout l;
+    if (!orth_layout(batch, rows, cols, &l)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    *bytes = l.total;
+    return ok();
+}
+
+flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t rows, int64_t cols, int64_t ld_x,
+                             int64_t stride_x, int steps, const float* coefficients, float eps, float scale,
+                             void* workspace, int64_t workspace_bytes, void* out, int out_dtype, int64_t ld_out,
+                             int64_t stride_out, flp_stream_t stream) {
+    flp_status st;
+    if ((st = check_dtype(dtype)) != FLP_OK) return st;
+    if (out_dtype != FLP_DTYPE_BF16 && out_dtype != FLP_DTYPE_F32)
+        return fail(FLP_EINVAL, "out_dtype must be FLP_DTYPE_BF16 or FLP_DTYPE_F32 (got %d)", out_dtype);
+    if ((st = check_orth_shape(batch, rows, cols)) != FLP_OK) return st;
+    if (steps < 1 || steps > 64) return fail(FLP_EINVAL, "steps must be in [1, 64] (got %d)", steps);
+    if (coefficients == nullptr) return fail(FLP_EINVAL, "coefficients is a null pointer");
+    for (int k = 0; k < 3 * steps; ++k)
+        if (!isfinite(coefficients[k])) return fail(FLP_EINVAL, "coefficients must be finite");
+    if (!(eps >= 0.f) || !isfinite(eps) || !isfinite(scale))
+        return fail(FLP_EINVAL, "eps must be finite and >= 0 and scale finite");
+    if (ld_x < cols || ld_out < cols)
+        return fail(FLP_EINVAL, "ld_x (%lld) and ld_out (%lld) must be >= cols (%lld)", (long long)ld_x,
+                    (long long)ld_out, (long long)cols);
+    if (batch == 0 || rows == 0 || cols == 0) return ok();
+    int64_t bx, bo, span;
+    if (!span_bytes(rows, cols, ld_x, 1, &bx) || !span_bytes(rows, cols, ld_out, 1, &bo) ||
+        !span_bytes(batch, bx, stride_x, elem_bytes(dtype), &span) ||
+        !span_bytes(batch, bo, stride_out, elem_bytes(out_dtype), &span))
+        return fail(FLP_EINVAL, "x or out extent overflows int64");
+    if (batch > 1 && (stride_x < 0 || stride_out < bo))
+        return fail(FLP_EINVAL, "stride_x must be >= 0 and stride_out cover a matrix");
+    OrthLayout l;
+    if (!orth_layout(batch, rows, cols, &l)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    if (workspace_bytes < l.total)
+        return fail(FLP_EINVAL, "workspace_bytes (%lld) is below the %lld bytes needed", (long long)workspace_bytes,
+                    (long long)l.total);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 127u) != 0)
+        return fail(FLP_EINVAL, "workspace must start on a 128-byte boundary");
+    const void* ptrs[] = {x, workspace, out};
+    const char* names[] = {"x", "workspace", "out"};
+    int dev;
+    if ((st = common_device(3, ptrs, names, nullptr, &dev)) != FLP_OK) return st;
+    if (dev < 0 || dev >= kMaxDevices) return fail(FLP_ECUDA, "device index %d out of range", dev);
+    DeviceGuard guard;
+    if ((st = guard.enter(dev)) != FLP_OK) return st;
+    if ((st = orth_setup(dev)) != FLP_OK) return st;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return fail(FLP_ECUDA, "could not read the SM count of device %d", dev);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    __half* hi[2] = {reinterpret_cast<__half*>(ws + l.hi0), reinterpret_cast<__half*>(ws + l.hi1)};
+    __half* lo = reinterpret_cast<__half*>(ws + l.lo);
+
+    CUtensorMap tm_xk[2], tm_xn[2], tm_a0, tm_b0;
+    const int64_t all_rows = batch * l.mp;
+    for (int k = 0; k < 2; ++k) {
+        if ((st = orth_tmap(&tm_xk[k], hi[k], all_rows, l.np, 128)) != FLP_OK) return st;
+        if ((st = orth_tmap(&tm_xn[k], hi[k], all_rows, l.np, 64)) != FLP_OK) return st;
+    }
+    if ((st = orth_tmap(&tm_a0, ws + l.a0, all_rows, l.mp, 128)) != FLP_OK) return st;
+    if ((st = orth_tmap(&tm_b0, ws + l.b0, all_rows, l.mp, 128)) != FLP_OK) return st;
+
+    const flp::OrthInput in{x, rows, cols, ld_x, stride_x, batch, rows > cols ? 1 : 0, eps,
+                            reinterpret_cast<double*>(ws + l.parts), hi[0], lo, l.mp, l.np};
+    const unsigned gs = (unsigned)(batch * flp::kOrthParts), gl = (unsigned)(batch * (l.np / 32) * (l.mp / 32));
+    if (dtype == FLP_DTYPE_BF16) {
+        flp::k_orth_sumsq<__nv_bfloat16><<<gs, 256, 0, s>>>(in);
+        flp::k_orth_load<__nv_bfloat16><<<gl, 256, 0, s>>>(in);
+    } else if (dtype == FLP_DTYPE_F16) {
+        flp::k_orth_sumsq<__half><<<gs, 256, 0, s>>>(in);
+        flp::k_orth_load<__half><<<gl, 256, 0, s>>>(in);
+    } else {
+        flp::k_orth_sumsq<float><<<gs, 256, 0, s>>>(in);
+        flp::k_orth_load<float><<<gl, 256, 0, s>>>(in);
+    }
+    if ((st = check_launch("orthogonalize input")) != FLP_OK) return st;
+
+    flp::OrthArgs p{};
+    p.batch = batch;
+    p.m = l.m;
+    p.n = l.n;
+    p.mp = l.mp;
+    p.np = l.np;
+    p.d = reinterpret_cast<float*>(ws + l.d);
+    p.e = reinterpret_cast<float*>(ws + l.e);
+    p.x_lo = lo;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.transposed = rows > cols ? 1 : 0;
+    const int ob = elem_bytes(out_dtype);
+    p.vec_out = aligned16(out) && (ld_out * ob) % 16 == 0 && (batch == 1 || (stride_out * ob) % 16 == 0);
+    p.ld_out = ld_out;
+    p.stride_out = stride_out;
+    p.scale = scale;
+    for (int k = 0; k < steps; ++k) {
+        const int cur = k & 1;
+        p.a = coefficients[3 * k];
+        p.b = coefficients[3 * k + 1];
+        p.c = coefficients[3 * k + 2];
+        p.mat = reinterpret_cast<__half*>(ws + l.a0);
+        p.mat_out = reinterpret_cast<__half*>(ws + l.b0);
+        p.x_hi = hi[cur];
+        p.x_out = hi[cur ^ 1];
+        if ((st = orth_product<flp::kOrthGram>(sms, tm_xk[cur], tm_xk[cur], p, s)) != FLP_OK) return st;
+        if ((st = orth_product<flp::kOrthPoly>(sms, tm_a0, tm_a0, p, s)) != FLP_OK) return st;
+        if (k + 1 < steps) st = orth_product<flp::kOrthApply>(sms, tm_b0, tm_xn[cur], p, s);
+        else st = orth_product<flp::kOrthFinal>(sms, tm_b0, tm_xn[cur], p, s);
+        if (st != FLP_OK) return st;
+    }
+    return ok();
+}
+
+}  // extern "C"

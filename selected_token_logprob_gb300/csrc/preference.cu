@@ -123,11 +123,12 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
     if ((st = check_launch("preference sums")) != FLP_OK) return st;
     int64_t pgrid = ceil_div(num_seqs / 2, kWarps);
     pgrid = pgrid < 1 ? 1 : (pgrid > flp::kPrefPairCtas ? flp::kPrefPairCtas : pgrid);
-    if ((st = launch_dependent("preference pairs", flp::k_pref_pairs, (int)pgrid, flp::kPrefThreads, s, a)) != FLP_OK)
+    if ((st = launch_dependent("preference pairs", flp::k_pref_pairs, (int)pgrid, flp::kPrefThreads, (size_t)0, s,
+                               a)) != FLP_OK)
         return st;
     if (n == 0) return ok();
     return launch_dependent("preference grad", vec ? flp::k_pref_grad<true> : flp::k_pref_grad<false>, grid,
-                            flp::kPrefThreads, s, a);
+                            flp::kPrefThreads, (size_t)0, s, a);
 }
 
 }  // extern "C"

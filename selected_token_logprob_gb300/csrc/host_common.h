@@ -165,10 +165,10 @@ inline EncodeTiledFn encode_tiled() {
 // serialization: the kernel may start while the previous work on s runs and
 // waits for it with griddepcontrol.wait.
 template <class... Args>
-inline flp_status launch_dependent(const char* what, void (*kern)(Args...), int grid, int block, size_t smem,
+inline flp_status launch_dependent(const char* what, void (*kern)(Args...), dim3 grid, int block, size_t smem,
                                    cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;

@@ -43,34 +43,100 @@ flp_status check_apart(const Extent& o, const Extent& i, bool same) {
     return FLP_OK;
 }
 
-int norm_row_grid(int64_t n, int sms) {
-    const int64_t most = (int64_t)sms * 8;
-    return (int)(n < most ? n : most);
-}
-
-template <class T>
-void launch_norm_fwd(const flp::NormFwdArgs& a, bool center, int sms, cudaStream_t s) {
-    const int grid = norm_row_grid(a.n, sms);
-    if (center) flp::k_norm_fwd_any<T, true><<<grid, flp::kNormAnyThreads, 0, s>>>(a);
-    else flp::k_norm_fwd_any<T, false><<<grid, flp::kNormAnyThreads, 0, s>>>(a);
-}
-
-template <class T, class G, bool kCenter>
-flp_status launch_norm_bwd_c(const flp::NormBwdArgs& a, int sms, cudaStream_t s) {
-    flp_status st;
-    flp::k_norm_dx_any<T, G, kCenter><<<norm_row_grid(a.n, sms), flp::kNormAnyThreads, 0, s>>>(a);
-    if ((st = check_launch("norm dx")) != FLP_OK) return st;
-    if (a.part_w || a.part_b) {
-        const dim3 grid((unsigned)ceil_div(a.d, flp::kNormAnyThreads), flp::kNormParts);
-        flp::k_norm_dw_any<T, G, kCenter><<<grid, flp::kNormAnyThreads, 0, s>>>(a);
-        if ((st = check_launch("norm dw")) != FLP_OK) return st;
-    }
+// Allows a kernel its ring of shared memory, once per device.
+template <class K>
+flp_status norm_setup(K kern, size_t smem, int dev, std::atomic<bool>* ready) {
+    if (smem == 0 || ready[dev].load(std::memory_order_acquire)) return FLP_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return fail(FLP_ECUDA, "norm setup: %s", cudaGetErrorString(e));
+    ready[dev].store(true, std::memory_order_release);
     return FLP_OK;
 }
 
+// SMs that the persistent grids are sized for: a constant, so that the order
+// of the weight's gradient depends on the problem alone.
+constexpr int kNormSms = 152;
+
+int row_ctas(int64_t n, int rows, int most) {
+    const int64_t c = ceil_div(n, rows);
+    return (int)(c < most ? c : most);
+}
+
+template <class T, int V, int kTpr, bool kCenter>
+flp_status launch_fwd_rows(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
+    static std::atomic<bool> ready[kMaxDevices];
+    constexpr int kThreads = flp::kNormThreads<kTpr>;
+    const auto kern = flp::k_norm_fwd<T, V, kTpr, kCenter>;
+    const size_t smem = V > 1 ? (size_t)kThreads * flp::kNormElems * sizeof(T) * flp::kNormFwdStages<T> : 0;
+    flp_status st;
+    if ((st = norm_setup(kern, smem, dev, ready)) != FLP_OK) return st;
+    kern<<<row_ctas(a.n, kThreads / kTpr, kNormSms * flp::kNormFwdCtas<kTpr>), kThreads, smem, s>>>(a);
+    return check_launch("norm forward");
+}
+
+template <class T, int V, bool kCenter>
+flp_status launch_fwd_v(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
+    constexpr int E = flp::kNormElems;
+    if (a.d <= 32 * E) return launch_fwd_rows<T, V, 32, kCenter>(a, dev, s);
+    if (a.d <= 128 * E) return launch_fwd_rows<T, V, 128, kCenter>(a, dev, s);
+    if (a.d <= 256 * E) return launch_fwd_rows<T, V, 256, kCenter>(a, dev, s);
+    if (a.d <= 512 * E) return launch_fwd_rows<T, V, 512, kCenter>(a, dev, s);
+    if (a.d <= 1024 * E) return launch_fwd_rows<T, V, 1024, kCenter>(a, dev, s);
+    flp::k_norm_fwd_any<T, kCenter><<<row_ctas(a.n, 1, kNormSms * 8), flp::kNormAnyThreads, 0, s>>>(a);
+    return check_launch("norm forward");
+}
+
+template <class T>
+flp_status launch_norm_fwd(const flp::NormFwdArgs& a, bool center, bool vec, int dev, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (vec) return center ? launch_fwd_v<T, V, true>(a, dev, s) : launch_fwd_v<T, V, false>(a, dev, s);
+    return center ? launch_fwd_v<T, 1, true>(a, dev, s) : launch_fwd_v<T, 1, false>(a, dev, s);
+}
+
+// Launches the row kernel; *parts = its CTAs, one partial row each.
+template <class T, class G, int V, int kTpr, bool kFull>
+flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
+    static std::atomic<bool> ready[kMaxDevices];
+    constexpr int kThreads = flp::kNormThreads<kTpr>;
+    static_assert(kNormSms * flp::kNormBwdCtas<kTpr> <= flp::kNormParts, "a partial row per CTA");
+    const auto kern = flp::k_norm_bwd<T, G, V, kTpr, kFull>;
+    const size_t smem =
+        V > 1 ? (size_t)kThreads * flp::kNormElems * (sizeof(T) + sizeof(G)) * flp::kNormBwdStages<T, G> : 0;
+    flp_status st;
+    if ((st = norm_setup(kern, smem, dev, ready)) != FLP_OK) return st;
+    *parts = row_ctas(a.n, kThreads / kTpr, kNormSms * flp::kNormBwdCtas<kTpr>);
+    kern<<<*parts, kThreads, smem, s>>>(a);
+    return check_launch("norm backward");
+}
+
+template <class T, class G, int V, bool kFull>
+flp_status launch_bwd_v(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
+    constexpr int E = flp::kNormElems;
+    if (a.d <= 32 * E) return launch_bwd_rows<T, G, V, 32, kFull>(a, dev, s, parts);
+    if (a.d <= 128 * E) return launch_bwd_rows<T, G, V, 128, kFull>(a, dev, s, parts);
+    if (a.d <= 256 * E) return launch_bwd_rows<T, G, V, 256, kFull>(a, dev, s, parts);
+    return launch_bwd_rows<T, G, V, 512, kFull>(a, dev, s, parts);
+}
+
+template <class T, class G, bool kCenter>
+flp_status launch_bwd_any(const flp::NormBwdArgs& a, cudaStream_t s, int* parts) {
+    flp::k_norm_dx_any<T, G, kCenter><<<row_ctas(a.n, 1, kNormSms * 8), flp::kNormAnyThreads, 0, s>>>(a);
+    if (a.part_w || a.part_b) {
+        const dim3 grid((unsigned)ceil_div(a.d, flp::kNormAnyThreads), flp::kNormAnyParts);
+        flp::k_norm_dw_any<T, G, kCenter><<<grid, flp::kNormAnyThreads, 0, s>>>(a);
+        *parts = flp::kNormAnyParts;
+    }
+    return check_launch("norm backward");
+}
+
 template <class T, class G>
-flp_status launch_norm_bwd(const flp::NormBwdArgs& a, bool center, int sms, cudaStream_t s) {
-    return center ? launch_norm_bwd_c<T, G, true>(a, sms, s) : launch_norm_bwd_c<T, G, false>(a, sms, s);
+flp_status launch_norm_bwd(const flp::NormBwdArgs& a, bool vec, int dev, cudaStream_t s, int* parts) {
+    const bool center = a.mean != nullptr, full = center || a.part_b != nullptr;
+    if (a.d > 512 * flp::kNormElems)
+        return center ? launch_bwd_any<T, G, true>(a, s, parts) : launch_bwd_any<T, G, false>(a, s, parts);
+    constexpr int V = 16 / sizeof(T);
+    if (vec) return full ? launch_bwd_v<T, G, V, true>(a, dev, s, parts) : launch_bwd_v<T, G, V, false>(a, dev, s, parts);
+    return full ? launch_bwd_v<T, G, 1, true>(a, dev, s, parts) : launch_bwd_v<T, G, 1, false>(a, dev, s, parts);
 }
 
 bool norm_workspace_bytes(int64_t d, int64_t* out) {
@@ -109,15 +175,15 @@ flp_status fused_layer_norm_forward(const void* x, int dtype, int64_t n, int64_t
     if (dev < 0 || dev >= kMaxDevices) return fail(FLP_ECUDA, "device index %d out of range", dev);
     DeviceGuard guard;
     if ((st = guard.enter(dev)) != FLP_OK) return st;
-    const int sms = sm_count(dev);
-    if (sms <= 0) return fail(FLP_ECUDA, "could not read the SM count of device %d", dev);
     const flp::NormFwdArgs a{x, n, d, ld_x, {weight, weight_dtype}, {bias, weight_dtype}, eps, 1.f / (float)d,
                              y, ld_y, mean, rstd};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == FLP_DTYPE_BF16) launch_norm_fwd<__nv_bfloat16>(a, center != 0, sms, s);
-    else if (dtype == FLP_DTYPE_F16) launch_norm_fwd<__half>(a, center != 0, sms, s);
-    else launch_norm_fwd<float>(a, center != 0, sms, s);
-    return check_launch("norm forward");
+    // 16-byte vectors need whole, aligned ones in every row and vector
+    const bool vec = (d * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) && rows_aligned16(y, ld_y, dtype) &&
+                     aligned16(weight) && aligned16(bias);
+    if (dtype == FLP_DTYPE_BF16) return launch_norm_fwd<__nv_bfloat16>(a, center != 0, vec, dev, s);
+    if (dtype == FLP_DTYPE_F16) return launch_norm_fwd<__half>(a, center != 0, vec, dev, s);
+    return launch_norm_fwd<float>(a, center != 0, vec, dev, s);
 }
 
 flp_status fused_layer_norm_backward_workspace_size(int64_t d, int64_t* bytes) {
@@ -179,28 +245,27 @@ flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy
     if (dev < 0 || dev >= kMaxDevices) return fail(FLP_ECUDA, "device index %d out of range", dev);
     DeviceGuard guard;
     if ((st = guard.enter(dev)) != FLP_OK) return st;
-    const int sms = sm_count(dev);
-    if (sms <= 0) return fail(FLP_ECUDA, "could not read the SM count of device %d", dev);
     float* ws = static_cast<float*>(workspace);
-    flp::NormBwdArgs a{dy, ld_dy, x, n, d, ld_x, {weight, weight_dtype}, mean, rstd, 1.f / (float)d, dx, ld_dx,
-                       dweight ? ws : nullptr, dbias ? ws + (int64_t)flp::kNormParts * d : nullptr};
-    const bool c = center != 0, wide = dy_dtype == FLP_DTYPE_F32;
+    const flp::NormBwdArgs a{dy, ld_dy, x, n, d, ld_x, {weight, weight_dtype}, center ? mean : nullptr, rstd,
+                             1.f / (float)d, dx, ld_dx, dweight ? ws : nullptr,
+                             dbias ? ws + (int64_t)flp::kNormParts * d : nullptr};
+    const bool wide = dy_dtype == FLP_DTYPE_F32;
+    const bool vec = (d * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) && rows_aligned16(dx, ld_dx, dtype) &&
+                     rows_aligned16(dy, ld_dy, dy_dtype) && aligned16(weight);
+    int parts = 0;
     if (dtype == FLP_DTYPE_BF16)
-        st = wide ? launch_norm_bwd<__nv_bfloat16, float>(a, c, sms, s)
-                  : launch_norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, c, sms, s);
+        st = wide ? launch_norm_bwd<__nv_bfloat16, float>(a, vec, dev, s, &parts)
+                  : launch_norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, vec, dev, s, &parts);
     else if (dtype == FLP_DTYPE_F16)
-        st = wide ? launch_norm_bwd<__half, float>(a, c, sms, s) : launch_norm_bwd<__half, __half>(a, c, sms, s);
+        st = wide ? launch_norm_bwd<__half, float>(a, vec, dev, s, &parts)
+                  : launch_norm_bwd<__half, __half>(a, vec, dev, s, &parts);
     else
-        st = launch_norm_bwd<float, float>(a, c, sms, s);
-    if (st != FLP_OK) return st;
-    const int fold = (int)ceil_div(d, flp::kNormFoldCols);
-    if (dweight)
-        flp::k_norm_fold<<<fold, flp::kNormFoldCols * flp::kNormFoldRows, 0, s>>>(a.part_w, flp::kNormParts, d, dweight,
-                                                                                   accumulate != 0);
-    if (dbias)
-        flp::k_norm_fold<<<fold, flp::kNormFoldCols * flp::kNormFoldRows, 0, s>>>(a.part_b, flp::kNormParts, d, dbias,
-                                                                                   accumulate != 0);
-    return check_launch("norm backward");
+        st = launch_norm_bwd<float, float>(a, vec, dev, s, &parts);
+    if (st != FLP_OK || !sums) return st;
+    const flp::NormFoldArgs f{a.part_w, a.part_b, parts, d, dweight, dbias, accumulate != 0};
+    return launch_dependent("norm fold", flp::k_norm_fold,
+                            dim3((unsigned)ceil_div(d, flp::kNormFoldCols), dweight && dbias ? 2 : 1),
+                            flp::kNormFoldCols * flp::kNormFoldRows, (size_t)0, s, f);
 }
 
 }  // extern "C"

@@ -45,9 +45,12 @@ flp_status check_apart(const Extent& o, const Extent& i, bool same) {
 
 // Allows a kernel its ring of shared memory, once per device.
 template <class K>
-flp_status norm_setup(K kern, size_t smem, int dev, std::atomic<bool>* ready) {
-    if (smem == 0 || ready[dev].load(std::memory_order_acquire)) return FLP_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+flp_status norm_setup(K kern, int dev, std::atomic<bool>* ready) {
+    if (ready[dev].load(std::memory_order_acquire)) return FLP_OK;
+    cudaFuncAttributes f;
+    cudaError_t e = cudaFuncGetAttributes(&f, kern);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - (int)f.sharedSizeBytes);
     if (e != cudaSuccess) return fail(FLP_ECUDA, "norm setup: %s", cudaGetErrorString(e));
     ready[dev].store(true, std::memory_order_release);
     return FLP_OK;
@@ -62,60 +65,50 @@ int row_ctas(int64_t n, int rows, int most) {
     return (int)(c < most ? c : most);
 }
 
-template <class T, int V, int kTpr, bool kCenter>
-flp_status launch_fwd_rows(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
-    static std::atomic<bool> ready[kMaxDevices];
-    constexpr int kThreads = flp::kNormThreads<kTpr>;
-    const auto kern = flp::k_norm_fwd<T, V, kTpr, kCenter>;
-    const size_t smem = V > 1 ? (size_t)kThreads * flp::kNormElems * sizeof(T) * flp::kNormFwdStages<T> : 0;
-    flp_status st;
-    if ((st = norm_setup(kern, smem, dev, ready)) != FLP_OK) return st;
-    kern<<<row_ctas(a.n, kThreads / kTpr, kNormSms * flp::kNormFwdCtas<kTpr>), kThreads, smem, s>>>(a);
-    return check_launch("norm forward");
-}
+constexpr size_t kNormMaxSmem = 232448 - 8192;   // of a CTA, beside the static arrays
 
-template <class T, int V, bool kCenter>
-flp_status launch_fwd_v(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
-    constexpr int E = flp::kNormElems;
-    if (a.d <= 32 * E) return launch_fwd_rows<T, V, 32, kCenter>(a, dev, s);
-    if (a.d <= 128 * E) return launch_fwd_rows<T, V, 128, kCenter>(a, dev, s);
-    if (a.d <= 256 * E) return launch_fwd_rows<T, V, 256, kCenter>(a, dev, s);
-    if (a.d <= 512 * E) return launch_fwd_rows<T, V, 512, kCenter>(a, dev, s);
-    if (a.d <= 1024 * E) return launch_fwd_rows<T, V, 1024, kCenter>(a, dev, s);
+template <class T, bool kCenter>
+flp_status launch_fwd_any(const flp::NormFwdArgs& a, cudaStream_t s) {
     flp::k_norm_fwd_any<T, kCenter><<<row_ctas(a.n, 1, kNormSms * 8), flp::kNormAnyThreads, 0, s>>>(a);
     return check_launch("norm forward");
 }
 
+template <class T, class W, int V, int kTpr, bool kCenter>
+flp_status launch_fwd_rows(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
+    static std::atomic<bool> ready[kMaxDevices];
+    constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = flp::kNormFwdStages<T>;
+    const auto kern = flp::k_norm_fwd<T, W, V, kTpr, kCenter>;
+    const size_t smem =
+        (V > 1 ? (size_t)kThreads * flp::kNormElems * sizeof(T) : (size_t)flp::norm_pitch<T>(a.d) * kRows) * kStages;
+    if (smem > kNormMaxSmem) return launch_fwd_any<T, kCenter>(a, s);
+    flp_status st;
+    if ((st = norm_setup(kern, dev, ready)) != FLP_OK) return st;
+    kern<<<row_ctas(a.n, kRows, kNormSms * flp::kNormFwdCtas<kTpr>), kThreads, smem, s>>>(a);
+    return check_launch("norm forward");
+}
+
+template <class T, class W, int V, bool kCenter>
+flp_status launch_fwd_v(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
+    constexpr int E = flp::kNormElems;
+    if (a.d <= 32 * E) return launch_fwd_rows<T, W, V, 32, kCenter>(a, dev, s);
+    if (a.d <= 128 * E) return launch_fwd_rows<T, W, V, 128, kCenter>(a, dev, s);
+    if (a.d <= 256 * E) return launch_fwd_rows<T, W, V, 256, kCenter>(a, dev, s);
+    if (a.d <= 512 * E) return launch_fwd_rows<T, W, V, 512, kCenter>(a, dev, s);
+    if (a.d <= 1024 * E) return launch_fwd_rows<T, W, V, 1024, kCenter>(a, dev, s);
+    return launch_fwd_any<T, kCenter>(a, s);
+}
+
+template <class T, class W>
+flp_status launch_fwd_w(const flp::NormFwdArgs& a, bool center, bool vec, int dev, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (vec) return center ? launch_fwd_v<T, W, V, true>(a, dev, s) : launch_fwd_v<T, W, V, false>(a, dev, s);
+    return center ? launch_fwd_v<T, W, 1, true>(a, dev, s) : launch_fwd_v<T, W, 1, false>(a, dev, s);
+}
+
 template <class T>
 flp_status launch_norm_fwd(const flp::NormFwdArgs& a, bool center, bool vec, int dev, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
-    if (vec) return center ? launch_fwd_v<T, V, true>(a, dev, s) : launch_fwd_v<T, V, false>(a, dev, s);
-    return center ? launch_fwd_v<T, 1, true>(a, dev, s) : launch_fwd_v<T, 1, false>(a, dev, s);
-}
-
-// Launches the row kernel; *parts = its CTAs, one partial row each.
-template <class T, class G, int V, int kTpr, bool kFull>
-flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
-    static std::atomic<bool> ready[kMaxDevices];
-    constexpr int kThreads = flp::kNormThreads<kTpr>;
-    static_assert(kNormSms * flp::kNormBwdCtas<kTpr> <= flp::kNormParts, "a partial row per CTA");
-    const auto kern = flp::k_norm_bwd<T, G, V, kTpr, kFull>;
-    const size_t smem =
-        V > 1 ? (size_t)kThreads * flp::kNormElems * (sizeof(T) + sizeof(G)) * flp::kNormBwdStages<T, G> : 0;
-    flp_status st;
-    if ((st = norm_setup(kern, smem, dev, ready)) != FLP_OK) return st;
-    *parts = row_ctas(a.n, kThreads / kTpr, kNormSms * flp::kNormBwdCtas<kTpr>);
-    kern<<<*parts, kThreads, smem, s>>>(a);
-    return check_launch("norm backward");
-}
-
-template <class T, class G, int V, bool kFull>
-flp_status launch_bwd_v(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
-    constexpr int E = flp::kNormElems;
-    if (a.d <= 32 * E) return launch_bwd_rows<T, G, V, 32, kFull>(a, dev, s, parts);
-    if (a.d <= 128 * E) return launch_bwd_rows<T, G, V, 128, kFull>(a, dev, s, parts);
-    if (a.d <= 256 * E) return launch_bwd_rows<T, G, V, 256, kFull>(a, dev, s, parts);
-    return launch_bwd_rows<T, G, V, 512, kFull>(a, dev, s, parts);
+    return a.w.dtype == FLP_DTYPE_F32 ? launch_fwd_w<T, float>(a, center, vec, dev, s)
+                                      : launch_fwd_w<T, T>(a, center, vec, dev, s);
 }
 
 template <class T, class G, bool kCenter>
@@ -129,12 +122,40 @@ flp_status launch_bwd_any(const flp::NormBwdArgs& a, cudaStream_t s, int* parts)
     return check_launch("norm backward");
 }
 
+// Launches the row kernel; *parts = its CTAs, one partial row each.
+template <class T, class G, int V, int kTpr, bool kFull>
+flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
+    static std::atomic<bool> ready[kMaxDevices];
+    constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr;
+    static_assert(kNormSms * flp::kNormBwdCtas<kTpr> <= flp::kNormParts, "a partial row per CTA");
+    const auto kern = flp::k_norm_bwd<T, G, V, kTpr, kFull>;
+    const size_t smem = (V > 1 ? (size_t)kThreads * flp::kNormElems * (sizeof(T) + sizeof(G))
+                               : (size_t)(flp::norm_pitch<T>(a.d) + flp::norm_pitch<G>(a.d)) * kRows) *
+                        flp::kNormBwdStages<T, G>;
+    if (smem > kNormMaxSmem)
+        return a.mean ? launch_bwd_any<T, G, true>(a, s, parts) : launch_bwd_any<T, G, false>(a, s, parts);
+    flp_status st;
+    if ((st = norm_setup(kern, dev, ready)) != FLP_OK) return st;
+    *parts = row_ctas(a.n, kRows, kNormSms * flp::kNormBwdCtas<kTpr>);
+    kern<<<*parts, kThreads, smem, s>>>(a);
+    return check_launch("norm backward");
+}
+
+template <class T, class G, int V, bool kFull>
+flp_status launch_bwd_v(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
+    constexpr int E = flp::kNormElems;
+    if (a.d <= 32 * E) return launch_bwd_rows<T, G, V, 32, kFull>(a, dev, s, parts);
+    if (a.d <= 128 * E) return launch_bwd_rows<T, G, V, 128, kFull>(a, dev, s, parts);
+    if (a.d <= 256 * E) return launch_bwd_rows<T, G, V, 256, kFull>(a, dev, s, parts);
+    return launch_bwd_rows<T, G, V, 512, kFull>(a, dev, s, parts);
+}
+
 template <class T, class G>
 flp_status launch_norm_bwd(const flp::NormBwdArgs& a, bool vec, int dev, cudaStream_t s, int* parts) {
     const bool center = a.mean != nullptr, full = center || a.part_b != nullptr;
     if (a.d > 512 * flp::kNormElems)
         return center ? launch_bwd_any<T, G, true>(a, s, parts) : launch_bwd_any<T, G, false>(a, s, parts);
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 16 / sizeof(G);   // of the wider of the two
     if (vec) return full ? launch_bwd_v<T, G, V, true>(a, dev, s, parts) : launch_bwd_v<T, G, V, false>(a, dev, s, parts);
     return full ? launch_bwd_v<T, G, 1, true>(a, dev, s, parts) : launch_bwd_v<T, G, 1, false>(a, dev, s, parts);
 }

@@ -13,6 +13,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace flp {
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -163,13 +165,17 @@ k_norm_dw_any(NormBwdArgs a) {
 
 // A row is held by kTpr threads, kNormElems elements each: kTpr = 32 (a warp
 // per row, four rows a CTA, no block-wide sums) up to 512 columns, then one
-// CTA per row.  Persistent CTAs step through the rows.
+// CTA per row.  Persistent CTAs step through the rows and copy the next ones
+// into a ring in shared memory with cp.async, so that the loads of several
+// rows are in flight while one is reduced and written.
 //
-// V > 1: rows of 16-byte vectors.  Each thread copies the vectors of its next
-// rows into shared memory with cp.async and reads back only its own, so the
-// ring of kStages rows needs no barrier and the loads of several rows are in
-// flight while one is reduced and written.  V = 1 (any alignment, stride and
-// width): element loads straight to registers.
+// V > 1 (16-byte aligned rows of whole vectors): a thread owns vectors of V
+// elements, copies only its own and reads back only its own; the ring needs no
+// barrier.  V is 16 bytes of the wider of x and dy, so that the lanes' copies
+// of both are contiguous (with 8 elements a lane the FP32 dy was fetched in
+// two halves of every sector: 217 instead of XXX us at 32768 x 4096).
+// V = 1 (any alignment, stride and width): the row's threads copy the aligned
+// 16-byte blocks that hold the row, and read elements at their offset.
 constexpr int kNormElems = 16;
 template <int kTpr>
 constexpr int kNormThreads = kTpr < 128 ? 128 : kTpr;
@@ -178,92 +184,110 @@ template <int kTpr>
 constexpr int kNormFwdCtas = 1024 / kNormThreads<kTpr>;
 template <int kTpr>
 constexpr int kNormBwdCtas = 512 / kNormThreads<kTpr>;
+// rows of the ring: 160 .. 192 KB per SM
 template <class T>
-constexpr int kNormFwdStages = sizeof(T) == 2 ? 5 : 3;                           // 160 .. 192 KB of rings per SM
+constexpr int kNormFwdStages = sizeof(T) == 2 ? 5 : 3;
 template <class T, class G>
-constexpr int kNormBwdStages = 24 / (int)(sizeof(T) + sizeof(G));                // 192 KB of rings per SM
+constexpr int kNormBwdStages = 24 / (int)(sizeof(T) + sizeof(G));
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// The first `bytes` of an aligned 16-byte block, zeros after them.
+__device__ __forceinline__ void cp_async_part(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ uint4 norm_lds(uint32_t a) {
-    uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a)
-                 : "memory");
+
+// V consecutive values as raw words, and their FP32 values.
+template <int kBytes>
+struct NormWords {
+    uint32_t w[kBytes / 4];
+};
+template <int kBytes>
+__device__ __forceinline__ NormWords<kBytes> norm_lds(uint32_t a) {
+    NormWords<kBytes> r;
+    if constexpr (kBytes == 16)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(a) : "memory");
+    else asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(a) : "memory");
     return r;
 }
-
-// The values of one 16-byte vector.
-__device__ __forceinline__ void norm_unpack(const uint4& q, float (&v)[4], float) {
-    v[0] = __uint_as_float(q.x);
-    v[1] = __uint_as_float(q.y);
-    v[2] = __uint_as_float(q.z);
-    v[3] = __uint_as_float(q.w);
-}
-__device__ __forceinline__ void norm_unpack(const uint4& q, float (&v)[8], __nv_bfloat16) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(w[k] << 16);
-        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void norm_unpack(const uint4& q, float (&v)[8], __half) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-        v[2 * k] = f.x;
-        v[2 * k + 1] = f.y;
-    }
-}
-__device__ __forceinline__ uint4 norm_pack(const float (&v)[4], float) {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-}
-__device__ __forceinline__ uint4 norm_pack(const float (&v)[8], __nv_bfloat16) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-        w[k] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint4 norm_pack(const float (&v)[8], __half) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
-        w[k] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Elements [i, i + V) of a weight or bias vector.
-template <int V>
-__device__ __forceinline__ void norm_vec_load(const NormVec& v, int i, float absent, float (&o)[V]) {
-    if constexpr (V == 1) {
-        o[0] = norm_vec_at(v, i, absent);
+template <int kBytes>
+__device__ __forceinline__ NormWords<kBytes> norm_ldg(const void* p) {
+    NormWords<kBytes> r;
+    if constexpr (kBytes == 16) {
+        const uint4 q = __ldg(static_cast<const uint4*>(p));
+        r.w[0] = q.x; r.w[1] = q.y; r.w[2] = q.z; r.w[3] = q.w;
     } else {
-        if (v.p == nullptr) {
+        const uint2 q = __ldg(static_cast<const uint2*>(p));
+        r.w[0] = q.x; r.w[1] = q.y;
+    }
+    return r;
+}
+template <int kBytes>
+__device__ __forceinline__ void norm_stg(void* p, const NormWords<kBytes>& r) {
+    if constexpr (kBytes == 16) *static_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else *static_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+}
+template <class T, int V>
+__device__ __forceinline__ void norm_unpack(const NormWords<V * (int)sizeof(T)>& q, float (&v)[V]) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) o[k] = absent;
-        } else if (v.dtype == 2) {
+        for (int k = 0; k < V; ++k) v[k] = __uint_as_float(q.w[k]);
+    } else {
 #pragma unroll
-            for (int h = 0; h < V / 4; ++h) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(v.p) + i) + h);
-                o[4 * h] = f.x;
-                o[4 * h + 1] = f.y;
-                o[4 * h + 2] = f.z;
-                o[4 * h + 3] = f.w;
+        for (int k = 0; k < V / 2; ++k) {
+            if constexpr (std::is_same<T, __half>::value) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q.w[k]));
+                v[2 * k] = f.x;
+                v[2 * k + 1] = f.y;
+            } else {
+                v[2 * k] = __uint_as_float(q.w[k] << 16);
+                v[2 * k + 1] = __uint_as_float(q.w[k] & 0xffff0000u);
             }
-        } else if constexpr (V == 8) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(v.p) + i));
-            if (v.dtype == 0) norm_unpack(q, o, __nv_bfloat16());
-            else norm_unpack(q, o, __half());
+        }
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ NormWords<V * (int)sizeof(T)> norm_pack(const float (&v)[V]) {
+    NormWords<V * (int)sizeof(T)> q;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) q.w[k] = __float_as_uint(v[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {
+            if constexpr (std::is_same<T, __half>::value) {
+                const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+                q.w[k] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                q.w[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    }
+    return q;
+}
+
+// Elements [i, i + V) of a vector of type W (V > 1: in 16-byte loads at most).
+template <class W, int V>
+__device__ __forceinline__ void norm_vec_load(const W* p, int i, float (&o)[V]) {
+    if constexpr (V == 1) {
+        o[0] = to_f32(__ldg(p + i));
+    } else if constexpr (V * sizeof(W) <= 16) {
+        norm_unpack<W, V>(norm_ldg<V * (int)sizeof(W)>(p + i), o);
+    } else {
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h) {
+            float q[4];
+            norm_unpack<W, 4>(norm_ldg<16>(p + i + 4 * h), q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[4 * h + j] = q[j];
         }
     }
 }
@@ -295,79 +319,115 @@ __device__ __forceinline__ void norm_row_sum(float (&v)[kCount], float* red, int
     }
 }
 
-// The vectors of row `p` that this thread owns, into its ring slots at `dst`.
+// Bytes of a ring slot of one unaligned row: its 16-byte blocks, one more than
+// aligned ones would take.
+template <class T>
+__host__ __device__ __forceinline__ uint32_t norm_pitch(int64_t d) {
+    return (uint32_t)((d * (int64_t)sizeof(T) + 15) / 16 + 1) * 16;
+}
+
+// Copies row `r` of `base` (n rows of d elements, ld apart) into the ring: V > 1:
+// this thread's vectors, into its own places from `dst` on; V = 1: this thread's
+// blocks of the row, whose first byte comes to dst + (address mod 16).
 template <class T, int V, int kTpr>
-__device__ __forceinline__ void norm_issue(const T* p, int t, int nvec, uint32_t dst) {
-    constexpr int NV = kNormElems / V, kPer = V * (int)sizeof(T) / 16;
+__device__ __forceinline__ void norm_issue(const T* base, int64_t r, int64_t ld, int d, int t, uint32_t dst) {
+    const T* p = base + r * ld;
+    if constexpr (V > 1) {
+        constexpr int NV = kNormElems / V, kBytes = V * (int)sizeof(T);
+        const int nvec = d / V;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int v = k * kTpr + t;
-        if (v < nvec) {
-#pragma unroll
-            for (int h = 0; h < kPer; ++h)
-                cp_async16(dst + (k * kPer + h) * kNormThreads<kTpr> * 16, reinterpret_cast<const char*>(p + v * V) + 16 * h);
+        for (int k = 0; k < NV; ++k) {
+            const int v = k * kTpr + t;
+            if (v < nvec) cp_async<kBytes>(dst + k * kNormThreads<kTpr> * kBytes, p + v * V);
+        }
+    } else {
+        const int mis = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+        const int bytes = mis + d * (int)sizeof(T);
+        const char* first = reinterpret_cast<const char*>(p) - mis;
+        for (int b = t * 16; b < bytes; b += kTpr * 16) {
+            const char* src = first + b;
+            if (src >= reinterpret_cast<const char*>(base)) {
+                cp_async_part(dst + b, src, bytes - b < 16 ? bytes - b : 16);
+            } else {   // this block starts before the whole buffer: element by element
+                for (int o = mis; o < 16 && o < bytes; o += (int)sizeof(T)) {
+                    if constexpr (sizeof(T) == 4)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + o),
+                                     "r"(*reinterpret_cast<const unsigned int*>(first + o)) : "memory");
+                    else
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + o),
+                                     "h"(*reinterpret_cast<const unsigned short*>(first + o)) : "memory");
+                }
+            }
         }
     }
 }
-// Values of slot k (vector k kTpr + t of the row) as FP32.
+// Values of vector k kTpr + t of the row copied to `src`; V = 1: of that
+// element, `src` being the row's first.
 template <class T, int V, int kTpr>
-__device__ __forceinline__ void norm_slot(uint32_t src, int k, float (&o)[V]) {
-    constexpr int kPer = V * (int)sizeof(T) / 16;
-    if constexpr (kPer == 1) {
-        norm_unpack(norm_lds(src + k * kNormThreads<kTpr> * 16), o, T());
-    } else {   // FP32 values beside 16-bit ones: two vectors
-#pragma unroll
-        for (int h = 0; h < kPer; ++h) {
-            float q[4];
-            norm_unpack(norm_lds(src + (k * kPer + h) * kNormThreads<kTpr> * 16), q, 0.f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[4 * h + j] = q[j];
-        }
+__device__ __forceinline__ void norm_slot(uint32_t src, int k, int t, float (&o)[V]) {
+    if constexpr (V > 1) {
+        norm_unpack<T, V>(norm_lds<V * (int)sizeof(T)>(src + k * kNormThreads<kTpr> * V * (int)sizeof(T)), o);
+    } else if constexpr (sizeof(T) == 4) {
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(o[0]) : "r"(src + (k * kTpr + t) * 4) : "memory");
+    } else {
+        unsigned short h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(src + (k * kTpr + t) * 2) : "memory");
+        o[0] = to_f32(*reinterpret_cast<const T*>(&h));
+    }
+}
+template <class T>
+__device__ __forceinline__ uint32_t norm_misaligned(const T* p) {
+    return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+}
+// After the wait for this thread's copies: those of the row's other threads.
+template <int V, int kTpr>
+__device__ __forceinline__ void norm_copied() {
+    if constexpr (V == 1) {
+        if constexpr (kTpr == 32) __syncwarp();
+        else __syncthreads();
     }
 }
 
-template <class T, int V, int kTpr, bool kCenter>
+template <class T, class W, int V, int kTpr, bool kCenter>
 __global__ void __launch_bounds__(kNormThreads<kTpr>, kNormFwdCtas<kTpr>)
 k_norm_fwd(NormFwdArgs a) {
     constexpr int NV = kNormElems / V, kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr;
     constexpr int kStages = kNormFwdStages<T>;
-    constexpr uint32_t kStageBytes = kThreads * kNormElems * sizeof(T);
     extern __shared__ __align__(16) unsigned char norm_smem[];
     __shared__ float red[2 * 64];
     int turn = 0;
-    const int t = threadIdx.x % kTpr, nvec = (int)a.d / V;
+    const int t = threadIdx.x % kTpr, d = (int)a.d, nvec = d / V;
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / kTpr;
-    const uint32_t ring = V > 1 ? (uint32_t)__cvta_generic_to_shared(norm_smem) + threadIdx.x * 16 : 0;
+    // V > 1: the thread's places; V = 1: the row's slot
+    const uint32_t pitch = V > 1 ? kThreads * kNormElems * (uint32_t)sizeof(T) : norm_pitch<T>(d) * kRows;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(norm_smem) +
+                          (V > 1 ? threadIdx.x * V * (uint32_t)sizeof(T) : threadIdx.x / kTpr * norm_pitch<T>(d));
     const T* x = static_cast<const T*>(a.x);
-    if constexpr (V > 1) {
+    const W *w = static_cast<const W*>(a.w.p), *b = static_cast<const W*>(a.b.p);
 #pragma unroll
-        for (int k = 0; k < kStages - 1; ++k) {
-            if (r + k * step < a.n) norm_issue<T, V, kTpr>(x + (r + k * step) * a.ld_x, t, nvec, ring + k * kStageBytes);
-            cp_async_commit();
-        }
+    for (int k = 0; k < kStages - 1; ++k) {
+        if (r + k * step < a.n) norm_issue<T, V, kTpr>(x, r + k * step, a.ld_x, d, t, ring + k * pitch);
+        cp_async_commit();
     }
     int stage = 0;
     for (; r < a.n; r += step) {
         float v[NV][V];
-        if constexpr (V > 1) {
-            const int64_t ahead = r + (kStages - 1) * step;
-            const int into = stage == 0 ? kStages - 1 : stage - 1;
-            if (ahead < a.n) norm_issue<T, V, kTpr>(x + ahead * a.ld_x, t, nvec, ring + into * kStageBytes);
-            cp_async_commit();
-            cp_async_wait<kStages - 1>();
+        const int64_t ahead = r + (kStages - 1) * step;
+        const int into = stage == 0 ? kStages - 1 : stage - 1;
+        if (ahead < a.n) norm_issue<T, V, kTpr>(x, ahead, a.ld_x, d, t, ring + into * pitch);
+        cp_async_commit();
+        cp_async_wait<kStages - 1>();
+        norm_copied<V, kTpr>();
+        const uint32_t src = ring + stage * pitch + (V > 1 ? 0 : norm_misaligned(x + r * a.ld_x));
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                if (k * kTpr + t < nvec) norm_slot<T, V, kTpr>(ring + stage * kStageBytes, k, v[k]);
-                else
+        for (int k = 0; k < NV; ++k) {
+            if (k * kTpr + t < nvec) norm_slot<T, V, kTpr>(src, k, t, v[k]);
+            else
 #pragma unroll
-                    for (int j = 0; j < V; ++j) v[k][j] = 0.f;
-            }
-            stage = stage == kStages - 1 ? 0 : stage + 1;
-        } else {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) v[k][0] = k * kTpr + t < nvec ? to_f32(x[r * a.ld_x + k * kTpr + t]) : 0.f;
+                for (int j = 0; j < V; ++j) v[k][j] = 0.f;
         }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
         float mu = 0.f;
         if (kCenter) {
             float s[1] = {0.f};
@@ -395,12 +455,20 @@ k_norm_fwd(NormFwdArgs a) {
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
             if (i < nvec) {
-                float w[V], b[V];
-                norm_vec_load<V>(a.w, i * V, 1.f, w);
-                norm_vec_load<V>(a.b, i * V, 0.f, b);
+                float f[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[k][j] = (v[k][j] - mu) * rstd * w[j] + b[j];
-                if constexpr (V > 1) *reinterpret_cast<uint4*>(y + i * V) = norm_pack(v[k], T());
+                for (int j = 0; j < V; ++j) v[k][j] = (v[k][j] - mu) * rstd;
+                if (w != nullptr) {
+                    norm_vec_load<W, V>(w, i * V, f);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) v[k][j] *= f[j];
+                }
+                if (b != nullptr) {
+                    norm_vec_load<W, V>(b, i * V, f);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) v[k][j] += f[j];
+                }
+                if constexpr (V > 1) norm_stg(y + i * V, norm_pack<T, V>(v[k]));
                 else y[i] = from_f32<T>(v[k][0]);
             }
         }
@@ -418,40 +486,49 @@ __global__ void __launch_bounds__(kNormThreads<kTpr>, kNormBwdCtas<kTpr>)
 k_norm_bwd(NormBwdArgs a) {
     constexpr int NV = kNormElems / V, kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr;
     constexpr int kStages = kNormBwdStages<T, G>;
-    constexpr uint32_t kXBytes = kThreads * kNormElems * sizeof(T);
-    constexpr uint32_t kStageBytes = kXBytes + kThreads * kNormElems * sizeof(G);
     extern __shared__ __align__(16) unsigned char norm_smem[];
     __shared__ float red[2 * 64];
     int turn = 0;
-    const int t = threadIdx.x % kTpr, nvec = (int)a.d / V;
+    const int t = threadIdx.x % kTpr, d = (int)a.d, nvec = d / V;
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / kTpr;
-    const uint32_t ring = V > 1 ? (uint32_t)__cvta_generic_to_shared(norm_smem) + threadIdx.x * 16 : 0;
+    const uint32_t xpitch = V > 1 ? kThreads * kNormElems * (uint32_t)sizeof(T) : norm_pitch<T>(d) * kRows;
+    const uint32_t pitch = xpitch + (V > 1 ? kThreads * kNormElems * (uint32_t)sizeof(G) : norm_pitch<G>(d) * kRows);
+    const uint32_t smem = (uint32_t)__cvta_generic_to_shared(norm_smem);
+    const uint32_t ring_x =
+        smem + (V > 1 ? threadIdx.x * V * (uint32_t)sizeof(T) : threadIdx.x / kTpr * norm_pitch<T>(d));
+    const uint32_t ring_g =
+        smem + xpitch + (V > 1 ? threadIdx.x * V * (uint32_t)sizeof(G) : threadIdx.x / kTpr * norm_pitch<G>(d));
     const T* x = static_cast<const T*>(a.x);
     const G* dy = static_cast<const G*>(a.dy);
     const bool center = kFull && a.mean != nullptr;
-
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) {
+        if (r + k * step < a.n) {
+            norm_issue<T, V, kTpr>(x, r + k * step, a.ld_x, d, t, ring_x + k * pitch);
+            norm_issue<G, V, kTpr>(dy, r + k * step, a.ld_dy, d, t, ring_g + k * pitch);
+        }
+        cp_async_commit();
+    }
     float w[NV][V], dw[NV][V], db[kFull ? NV : 1][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int i = k * kTpr + t;
-        if (i < nvec) norm_vec_load<V>(a.w, i * V, 1.f, w[k]);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            if (i >= nvec) w[k][j] = 0.f;
+            w[k][j] = i < nvec ? 1.f : 0.f;
             dw[k][j] = 0.f;
             if (kFull) db[k][j] = 0.f;
         }
     }
-    if constexpr (V > 1) {
+    if (a.w.p != nullptr) {
 #pragma unroll
-        for (int k = 0; k < kStages - 1; ++k) {
-            const int64_t q = r + k * step;
-            if (q < a.n) {
-                norm_issue<T, V, kTpr>(x + q * a.ld_x, t, nvec, ring + k * kStageBytes);
-                norm_issue<G, V, kTpr>(dy + q * a.ld_dy, t, nvec, ring + k * kStageBytes + kXBytes);
+        for (int k = 0; k < NV; ++k) {
+            const int i = k * kTpr + t;
+            if (i < nvec) {
+                if (sizeof(T) == 4 || a.w.dtype == 2) norm_vec_load<float, V>(static_cast<const float*>(a.w.p), i * V, w[k]);
+                else norm_vec_load<T, V>(static_cast<const T*>(a.w.p), i * V, w[k]);
             }
-            cp_async_commit();
         }
     }
     float mu_next = 0.f, rstd_next = 0.f;
@@ -466,29 +543,24 @@ k_norm_bwd(NormBwdArgs a) {
             mu_next = center ? __ldg(a.mean + r + step) : 0.f;
             rstd_next = __ldg(a.rstd + r + step);
         }
-        float xh[NV][V], g[NV][V];   // xh, then dx; dy, then dy w
-        if constexpr (V > 1) {
-            const int64_t ahead = r + (kStages - 1) * step;
-            const int into = stage == 0 ? kStages - 1 : stage - 1;
-            if (ahead < a.n) {
-                norm_issue<T, V, kTpr>(x + ahead * a.ld_x, t, nvec, ring + into * kStageBytes);
-                norm_issue<G, V, kTpr>(dy + ahead * a.ld_dy, t, nvec, ring + into * kStageBytes + kXBytes);
-            }
-            cp_async_commit();
-            cp_async_wait<kStages - 1>();
+        const int64_t ahead = r + (kStages - 1) * step;
+        const int into = stage == 0 ? kStages - 1 : stage - 1;
+        if (ahead < a.n) {
+            norm_issue<T, V, kTpr>(x, ahead, a.ld_x, d, t, ring_x + into * pitch);
+            norm_issue<G, V, kTpr>(dy, ahead, a.ld_dy, d, t, ring_g + into * pitch);
         }
+        cp_async_commit();
+        cp_async_wait<kStages - 1>();
+        norm_copied<V, kTpr>();
+        const uint32_t sx = ring_x + stage * pitch + (V > 1 ? 0 : norm_misaligned(x + r * a.ld_x));
+        const uint32_t sg = ring_g + stage * pitch + (V > 1 ? 0 : norm_misaligned(dy + r * a.ld_dy));
+        float xh[NV][V], g[NV][V];   // xh, then dx; dy, then dy w
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int i = k * kTpr + t;
-            if (i < nvec) {
-                if constexpr (V > 1) {
-                    norm_slot<T, V, kTpr>(ring + stage * kStageBytes, k, xh[k]);
-                    norm_slot<G, V, kTpr>(ring + stage * kStageBytes + kXBytes, k, g[k]);
-                } else {
-                    xh[k][0] = to_f32(x[r * a.ld_x + i]);
-                    g[k][0] = to_f32(dy[r * a.ld_dy + i]);
-                }
+            if (k * kTpr + t < nvec) {
+                norm_slot<T, V, kTpr>(sx, k, t, xh[k]);
+                norm_slot<G, V, kTpr>(sg, k, t, g[k]);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     xh[k][j] = (xh[k][j] - mu) * rstd;
@@ -500,7 +572,7 @@ k_norm_bwd(NormBwdArgs a) {
                 }
             }
         }
-        if constexpr (V > 1) stage = stage == kStages - 1 ? 0 : stage + 1;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
         if constexpr (kFull) {
             norm_row_sum<kTpr, 2>(s, red, turn);
         } else {
@@ -516,21 +588,33 @@ k_norm_bwd(NormBwdArgs a) {
             if (i < nvec) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) xh[k][j] = (g[k][j] - c1 - xh[k][j] * c2) * rstd;
-                if constexpr (V > 1) *reinterpret_cast<uint4*>(dx + i * V) = norm_pack(xh[k], T());
+                if constexpr (V > 1) norm_stg(dx + i * V, norm_pack<T, V>(xh[k]));
                 else dx[i] = from_f32<T>(xh[k][0]);
             }
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the CTA's partial row
     if constexpr (kRows == 1) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
             if (i < nvec) {
+                const int64_t at = (int64_t)blockIdx.x * d + i * V;
+                if constexpr (V > 1) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (a.part_w) a.part_w[(int64_t)blockIdx.x * a.d + i * V + j] = dw[k][j];
-                    if (kFull && a.part_b) a.part_b[(int64_t)blockIdx.x * a.d + i * V + j] = db[k][j];
+                    for (int h = 0; h < V; h += 4) {
+                        if (a.part_w)
+                            *reinterpret_cast<float4*>(a.part_w + at + h) =
+                                make_float4(dw[k][h], dw[k][h + 1], dw[k][h + 2], dw[k][h + 3]);
+                        if constexpr (kFull)
+                            if (a.part_b)
+                                *reinterpret_cast<float4*>(a.part_b + at + h) =
+                                    make_float4(db[k][h], db[k][h + 1], db[k][h + 2], db[k][h + 3]);
+                    }
+                } else {
+                    if (a.part_w) a.part_w[at] = dw[k][0];
+                    if (kFull && a.part_b) a.part_b[at] = db[k][0];
                 }
             }
         }
@@ -551,16 +635,16 @@ k_norm_bwd(NormBwdArgs a) {
             }
             __syncthreads();
         }
-        for (int i = threadIdx.x; i < (int)a.d; i += kThreads) {
-            if (a.part_w) a.part_w[(int64_t)blockIdx.x * a.d + i] = sum[0][i];
-            if (kFull && a.part_b) a.part_b[(int64_t)blockIdx.x * a.d + i] = sum[kFull ? 1 : 0][i];
+        for (int i = threadIdx.x; i < d; i += kThreads) {
+            if (a.part_w) a.part_w[(int64_t)blockIdx.x * d + i] = sum[0][i];
+            if (kFull && a.part_b) a.part_b[(int64_t)blockIdx.x * d + i] = sum[kFull ? 1 : 0][i];
         }
     }
 }
 
 // ---------------------------------------------------------------- partial rows
 
-constexpr int kNormFoldCols = 32, kNormFoldRows = 16;
+constexpr int kNormFoldCols = 32, kNormFoldRows = 32;
 
 struct NormFoldArgs {
     const float *part_w, *part_b;   // [rows, d] or null
@@ -582,8 +666,8 @@ k_norm_fold(NormFoldArgs a) {
     const int64_t c = (int64_t)blockIdx.x * kNormFoldCols + tx;
     float s = 0.f;
     if (c < a.d) {
-#pragma unroll 4
-        for (int r = ty; r < a.rows; r += kNormFoldRows) s += __ldcs(part + (int64_t)r * a.d + c);
+#pragma unroll 10
+        for (int r = ty; r < a.rows; r += kNormFoldRows) s += __ldcg(part + (int64_t)r * a.d + c);
     }
     red[ty][tx] = s;
     __syncthreads();

@@ -629,8 +629,9 @@ flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy
  *            16-byte aligned, caller-owned, no initial contents needed; one
  *            workspace serves one call at a time.
  * logp and ref_logp are never used where the mask is 0 (they may hold NaN or
- * infinities there).  Sums are FP32 within 256-token chunks and FP64 over
- * them, in an order fixed by the layout: repeated calls give identical bits.
+ * infinities there).  Sums are FP32 within 512-token chunks and two-float
+ * sums over them, in an order fixed by the layout: repeated calls give
+ * identical bits.
  * Bounds in cu_seqlens are clamped to [0, n]; when they decrease, the result
  * is unspecified, but every access stays inside the arrays.
  * Errors: FLP_EINVAL for an odd or too large num_seqs, a bad kind or layout,

@@ -11,7 +11,7 @@ namespace {
 
 // Byte offsets of the workspace's parts; false when they overflow.
 struct PrefLayout {
-    int64_t part_loss, part_live, slots, first_seq, coef, total;
+    int64_t part_loss, part_live, slots, coef, total;
 };
 
 bool pref_layout(int64_t n, int64_t nseq, PrefLayout* l) {
@@ -21,8 +21,7 @@ bool pref_layout(int64_t n, int64_t nseq, PrefLayout* l) {
     l->part_loss = 256;   // the ticket and 1 / D
     l->part_live = l->part_loss + 8 * flp::kPrefPairCtas;
     l->slots = l->part_live + 8 * flp::kPrefPairCtas;
-    l->first_seq = l->slots + 8 * slots;
-    l->coef = l->first_seq + 4 * nchunks;
+    l->coef = l->slots + 8 * slots;
     if (__builtin_add_overflow(l->coef, 4 * nseq + 255, &b)) return false;
     l->total = b / 256 * 256;
     return true;
@@ -101,33 +100,58 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
     a.smooth = label_smoothing;
     a.margin = margin;
     a.normalizer = normalizer;
+    const double target = 0.5 / (double)beta;
+    a.target_hi = (float)target;
+    a.target_lo = isfinite(a.target_hi) ? (float)(target - (double)a.target_hi) : 0.f;
     a.loss = loss;
     a.grad = grad;
     a.rewards = rewards;
     char* base = static_cast<char*>(workspace);
     a.ticket = reinterpret_cast<unsigned*>(base);
     a.inv_den = reinterpret_cast<float*>(base + 16);
-    a.part_loss = reinterpret_cast<double*>(base + l.part_loss);
-    a.part_live = reinterpret_cast<int64_t*>(base + l.part_live);
+    a.part_loss = reinterpret_cast<flp::PrefTwo*>(base + l.part_loss);
+    a.part_live = reinterpret_cast<int*>(base + l.part_live);
     a.slots = reinterpret_cast<flp::PrefSlot*>(base + l.slots);
-    a.first_seq = reinterpret_cast<int32_t*>(base + l.first_seq);
     a.coef = reinterpret_cast<float*>(base + l.coef);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool vec = aligned16(logp) && aligned16(ref_logp) && aligned16(grad) &&
                      (reinterpret_cast<uintptr_t>(active_mask) & 3u) == 0;
+    // A batch that leaves a cluster's warps a few chunks and pairs each runs in
+    // one launch; above that the whole GPU's bandwidth is worth two more launches.
+    constexpr int64_t kClusterWarps = flp::kPrefClusterCtas * flp::kPrefClusterThreads / 32;
+    if (a.nchunks <= 8 * kClusterWarps && num_seqs <= 16 * kClusterWarps) {
+        (vec ? flp::k_pref_cluster<true> : flp::k_pref_cluster<false>)<<<flp::kPrefClusterCtas,
+                                                                         flp::kPrefClusterThreads, 0, s>>>(a);
+        return check_launch("preference loss");
+    }
+    // Token passes: a run of chunks per warp.
     constexpr int kWarps = flp::kPrefThreads / 32;
-    const int64_t most = (int64_t)sms * 8;
     const int64_t ctas = a.nchunks <= kWarps ? 1 : ceil_div(a.nchunks, kWarps);
-    const int grid = (int)(ctas < most ? ctas : most);
-    (vec ? flp::k_pref_sums<true> : flp::k_pref_sums<false>)<<<grid, flp::kPrefThreads, 0, s>>>(a);
+    auto token_grid = [&](int per_sm) { return (int)(ctas < (int64_t)sms * per_sm ? ctas : (int64_t)sms * per_sm); };
+    if (vec) {
+        constexpr int kRing = flp::kPrefStages * (int)flp::kPrefStageBytes;
+        static std::atomic<bool> ready[kMaxDevices];
+        if (!ready[dev].load(std::memory_order_acquire)) {
+            const cudaError_t e = cudaFuncSetAttribute(flp::k_pref_sums<true>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+            if (e != cudaSuccess) return fail(FLP_ECUDA, "preference setup: %s", cudaGetErrorString(e));
+            ready[dev].store(true, std::memory_order_release);
+        }
+        flp::k_pref_sums<true><<<token_grid(flp::kPrefSumCtas), flp::kPrefThreads, kRing, s>>>(a);
+    } else {
+        flp::k_pref_sums<false><<<token_grid(flp::kPrefSumCtas), flp::kPrefThreads, 0, s>>>(a);
+    }
     if ((st = check_launch("preference sums")) != FLP_OK) return st;
-    int64_t pgrid = ceil_div(num_seqs / 2, kWarps);
+    // 8 lanes per pair while a sequence has a few slots, a warp beyond that
+    const bool narrow = a.nchunks <= 16 * num_seqs;
+    int64_t pgrid = ceil_div(num_seqs / 2, flp::kPrefThreads / (narrow ? 8 : 32));
     pgrid = pgrid < 1 ? 1 : (pgrid > flp::kPrefPairCtas ? flp::kPrefPairCtas : pgrid);
-    if ((st = launch_dependent("preference pairs", flp::k_pref_pairs, (int)pgrid, flp::kPrefThreads, (size_t)0, s,
-                               a)) != FLP_OK)
+    if ((st = launch_dependent("preference pairs", narrow ? flp::k_pref_pairs<8> : flp::k_pref_pairs<32>, (int)pgrid,
+                               flp::kPrefThreads, (size_t)0, s, a)) != FLP_OK)
         return st;
     if (n == 0) return ok();
-    return launch_dependent("preference grad", vec ? flp::k_pref_grad<true> : flp::k_pref_grad<false>, grid,
+    return launch_dependent("preference grad", vec ? flp::k_pref_grad<true> : flp::k_pref_grad<false>,
+                            token_grid(flp::kPrefGradCtas),
                             flp::kPrefThreads, (size_t)0, s, a);
 }
 

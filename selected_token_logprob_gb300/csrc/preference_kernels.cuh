@@ -10,14 +10,20 @@
 // token) divided by their number D.  The gradient of token t of sequence s is
 // +-(dl/dh) / D, divided by n_s when averaging.
 //
-// Three launches.  Sums: the batch is cut into fixed chunks of 256 tokens, one
-// warp each; a chunk writes the sum and the active count of every sequence it
-// meets into slot (chunk + sequence).  Along the packed batch each next piece
-// moves to the next chunk, the next sequence or both, so slots never collide
-// and a sequence's pieces lie side by side.  Pairs: a warp per pair adds both
-// sides' slots in FP64 and forms the loss and the sequences' coefficients; the
-// last CTA folds the loss and D.  Grad: a warp per chunk writes the gradients.
-// Nothing depends on timing.
+// Three phases.  Sums: the batch is cut into fixed chunks of 512 tokens; a warp
+// takes a run of consecutive chunks and writes, for every sequence that a chunk
+// meets, the sum and the active count into slot (chunk + sequence).  Along the
+// packed batch each next piece moves to the next chunk, the next sequence or
+// both, so slots never collide and a sequence's pieces lie side by side.  Pairs:
+// 8 (or 32) lanes per pair add both sides' slots in FP64 and form the loss and
+// the sequences' coefficients; the loss and D are folded in a fixed order.
+// Grad: the warps write their chunks' gradients.  A large batch runs them as
+// three dependent launches, a small one in a single cluster of 8 CTAs with
+// cluster barriers between them.  Nothing depends on timing or on the grid.
+//
+// A run's cursor holds the bounds (and coefficients) of 32 sequences, one a
+// lane, so that a chunk reads no bounds from memory; the next chunk's tokens are
+// copied into shared memory while this one's are summed.
 #pragma once
 
 #include <math.h>
@@ -25,9 +31,11 @@
 
 namespace flp {
 
-constexpr int kPrefChunk = 256;        // tokens per warp and step
+constexpr int kPrefChunk = 512;        // tokens per warp and step
+constexpr int kPrefQuads = kPrefChunk / 128;   // groups of four neighbouring tokens a lane holds of it
 constexpr int kPrefThreads = 256;
-constexpr int kPrefPairCtas = 1024;    // most CTAs of the pair kernel (the fold's shape)
+constexpr int kPrefSumCtas = 3, kPrefGradCtas = 4;   // CTAs per SM of the token passes
+constexpr int kPrefPairCtas = 304;     // most CTAs of the pair kernel (the fold's shape)
 
 enum PrefKind { kPrefSigmoid = 0, kPrefHinge = 1, kPrefIpo = 2 };
 
@@ -36,6 +44,27 @@ struct PrefSlot {
     int count;
 };
 
+// An unevaluated sum of two FP32 numbers: about 48 bits.  (FP64 adds, at 1/64 of
+// the FP32 rate, took most of the pair phase.)
+struct PrefTwo {
+    float hi, lo;
+};
+__device__ __forceinline__ PrefTwo pref_add(PrefTwo x, float y) {   // Knuth's TwoSum
+    const float s = __fadd_rn(x.hi, y), b = __fsub_rn(s, x.hi);
+    return {s, __fadd_rn(x.lo, __fadd_rn(__fsub_rn(x.hi, __fsub_rn(s, b)), __fsub_rn(y, b)))};
+}
+__device__ __forceinline__ PrefTwo pref_add(PrefTwo x, PrefTwo y) {
+    PrefTwo r = pref_add(x, y.hi);
+    r.lo = __fadd_rn(r.lo, y.lo);
+    return r;
+}
+// An infinite or NaN hi makes lo meaningless (inf - inf): keep hi alone.
+__device__ __forceinline__ PrefTwo pref_settle(PrefTwo x) { return isfinite(x.hi) ? x : PrefTwo{x.hi, 0.f}; }
+__device__ __forceinline__ float pref_value(PrefTwo x) {
+    x = pref_settle(x);
+    return x.hi + x.lo;
+}
+
 struct PrefArgs {
     const float *logp, *ref;      // ref nullable
     const uint8_t* mask;          // nullable
@@ -43,14 +72,14 @@ struct PrefArgs {
     int64_t n, nseq, nchunks;
     int kind, average, halves;
     float beta, smooth, margin, normalizer;
+    float target_hi, target_lo;   // 1 / (2 beta) as two floats
     float *loss, *grad, *rewards;
     // workspace
     unsigned* ticket;
     float* inv_den;
-    double* part_loss;            // [kPrefPairCtas]
-    int64_t* part_live;           // [kPrefPairCtas]
+    PrefTwo* part_loss;           // [kPrefPairCtas]
+    int* part_live;               // [kPrefPairCtas]
     PrefSlot* slots;              // [nchunks + nseq]
-    int32_t* first_seq;           // [nchunks] first sequence that ends after the chunk's start
     float* coef;                  // [nseq] dl/dr before the division by D
 };
 
@@ -79,139 +108,285 @@ __device__ __forceinline__ int64_t pref_first_seq(const PrefArgs& a, int64_t pos
     return lo;
 }
 
-// Token j of lane in a chunk: four neighbours in each half.
-__device__ __forceinline__ int pref_tok(int lane, int j) { return (j >> 2) * 128 + lane * 4 + (j & 3); }
-
-__device__ __forceinline__ void pref_load4(const float* p, int64_t i, int64_t n, bool vec, float (&v)[4]) {
-    if (vec && i + 4 <= n) {
-        const float4 q = __ldcs(reinterpret_cast<const float4*>(p + i));
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = i + k < n ? __ldcs(p + i + k) : 0.f;
+// Walks the sequences that a run of tokens [base, base + len) meets.  Bounds are
+// held relative to base, clamped to [-1, len + 1].
+struct PrefCursor {
+    int64_t s0;       // sequence of lane 0's bound
+    int32_t bound;    // lane l: start of sequence s0 + l
+    float coef;       // lane l: coefficient of sequence s0 + l (grad phase)
+    int k;            // current sequence - s0
+};
+template <bool kCoef>
+__device__ __forceinline__ void pref_window(const PrefArgs& a, int64_t base, int64_t len, int64_t s, float inv_den,
+                                            PrefCursor& c) {
+    const int lane = threadIdx.x & 31;
+    const int64_t i = s + lane;
+    int64_t v = (i <= a.nseq ? pref_cu(a, i) : a.n) - base;
+    v = v < -1 ? -1 : (v > len + 1 ? len + 1 : v);
+    c.s0 = s;
+    c.bound = (int32_t)v;
+    c.coef = kCoef && i < a.nseq ? __ldcg(a.coef + i) * inv_den : 0.f;
+    c.k = 0;
+}
+// Calls piece(sequence, lo, hi, coefficient) for every sequence with tokens in the chunk
+// [t, t + size) of the run, lo and hi relative to the chunk; advances the cursor.
+template <bool kCoef, class F>
+__device__ __forceinline__ void pref_walk(const PrefArgs& a, int64_t base, int64_t len, float inv_den, PrefCursor& c,
+                                          int32_t t, int32_t size, F piece) {
+    while (c.s0 + c.k < a.nseq) {
+        if (c.k == 31) pref_window<kCoef>(a, base, len, c.s0 + c.k, inv_den, c);
+        const int32_t b = __shfl_sync(0xffffffffu, c.bound, c.k), e = __shfl_sync(0xffffffffu, c.bound, c.k + 1);
+        if (b >= t + size) break;
+        const int32_t lo = b > t ? b - t : 0, hi = e < t + size ? e - t : size;
+        const float g = kCoef ? __shfl_sync(0xffffffffu, c.coef, c.k) : 0.f;
+        if (hi > lo) piece(c.s0 + c.k, lo, hi, g);
+        if (e > t + size) break;   // goes on in the next chunk
+        ++c.k;
     }
 }
-// Bit k: token i + k exists and is active.
-__device__ __forceinline__ uint32_t pref_mask4(const uint8_t* m, int64_t i, int64_t n, bool vec) {
-    uint32_t bits = 0;
-    if (m != nullptr && vec && i + 4 <= n) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(m + i));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) bits |= ((w >> (8 * k)) & 0xffu) ? (1u << k) : 0u;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + k < n && (m == nullptr || __ldg(m + i + k) != 0)) bits |= 1u << k;
-    }
-    return bits;
-}
 
+// A lane's tokens of a chunk: quad h holds tokens h 128 + 4 lane .. + 3.
+struct PrefRaw {
+    float p[4 * kPrefQuads], q[4 * kPrefQuads];
+    uint32_t m[kPrefQuads];   // mask bytes; 0 for tokens past the batch's end
+};
+__device__ __forceinline__ bool pref_active(const uint32_t (&m)[kPrefQuads], int j) {
+    return (m[j >> 2] & (0xffu << (8 * (j & 3)))) != 0;
+}
 template <bool kVec>
-__global__ void __launch_bounds__(kPrefThreads)
-k_pref_sums(PrefArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (kPrefThreads / 32);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-    for (int64_t c = (int64_t)blockIdx.x * (kPrefThreads / 32) + (threadIdx.x >> 5); c < a.nchunks; c += warps) {
-        const int64_t t0 = c * kPrefChunk, t1 = t0 + kPrefChunk < a.n ? t0 + kPrefChunk : a.n;
-        float v[8];
-        uint32_t bits = 0;
+__device__ __forceinline__ void pref_mask(const PrefArgs& a, int64_t t0, uint32_t (&m)[kPrefQuads]) {
+    const int64_t i0 = t0 + (threadIdx.x & 31) * 4;
+    if (kVec && t0 + kPrefChunk <= a.n) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t i = t0 + h * 128 + lane * 4;
-            float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
-            pref_load4(a.logp, i, a.n, kVec, p);
-            if (a.ref) pref_load4(a.ref, i, a.n, kVec, q);
-            const uint32_t m = pref_mask4(a.mask, i, a.n, kVec);
+        for (int h = 0; h < kPrefQuads; ++h)
+            m[h] = a.mask ? __ldg(reinterpret_cast<const uint32_t*>(a.mask + i0) + 32 * h) : 0x01010101u;
+    } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[4 * h + k] = (m >> k) & 1u ? p[k] - q[k] : 0.f;   // a masked value is not read
-            bits |= m << (4 * h);
-        }
-        int64_t s = pref_first_seq(a, t0);
-        if (lane == 0) a.first_seq[c] = (int32_t)s;
-        int64_t b = s < a.nseq ? pref_cu(a, s) : t1;
-        while (s < a.nseq && b < t1) {
-            const int64_t e = pref_cu(a, s + 1);
-            if (e > b && e > t0) {
-                float sum = 0.f;
-                int cnt = 0;
-                const int lo = b > t0 ? (int)(b - t0) : 0, hi = e < t1 ? (int)(e - t0) : kPrefChunk;
+        for (int h = 0; h < kPrefQuads; ++h) {
+            m[h] = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int k = pref_tok(lane, j);
-                    if (k >= lo && k < hi) {
-                        sum += v[j];
-                        cnt += (bits >> j) & 1u;
-                    }
-                }
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) {
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-                }
-                if (lane == 0) a.slots[c + s] = PrefSlot{sum, cnt};
+            for (int k = 0; k < 4; ++k) {
+                const int64_t i = i0 + h * 128 + k;
+                if (i < a.n) m[h] |= (a.mask ? (uint32_t)__ldg(a.mask + i) : 1u) << (8 * k);
             }
-            b = e;
-            ++s;
         }
     }
 }
+template <bool kVec>
+__device__ __forceinline__ void pref_tokens(const float* x, int64_t t0, int64_t n, float (&v)[4 * kPrefQuads]) {
+    const int64_t i0 = t0 + (threadIdx.x & 31) * 4;
+    if (kVec && t0 + kPrefChunk <= n) {
+#pragma unroll
+        for (int h = 0; h < kPrefQuads; ++h) {
+            const float4 q = __ldcs(reinterpret_cast<const float4*>(x + i0) + 32 * h);
+            v[4 * h] = q.x;
+            v[4 * h + 1] = q.y;
+            v[4 * h + 2] = q.z;
+            v[4 * h + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4 * kPrefQuads; ++j) {
+            const int64_t i = i0 + (j >> 2) * 128 + (j & 3);
+            v[j] = i < n ? __ldcs(x + i) : 0.f;
+        }
+    }
+}
+template <bool kVec>
+__device__ __forceinline__ void pref_load(const PrefArgs& a, int64_t t0, PrefRaw& r) {
+    pref_tokens<kVec>(a.logp, t0, a.n, r.p);
+    if (a.ref) pref_tokens<kVec>(a.ref, t0, a.n, r.q);
+    pref_mask<kVec>(a, t0, r.m);
+}
 
-// (sum, active tokens) of sequence s, in every lane.
-__device__ __forceinline__ void pref_sequence(const PrefArgs& a, int64_t s, double& sum, int64_t& cnt) {
+// Chunks [c0, c1) of warp `w` of `warps`.
+__device__ __forceinline__ void pref_run(const PrefArgs& a, int64_t w, int64_t warps, int64_t& c0, int64_t& c1) {
+    c0 = a.nchunks / warps * w + a.nchunks % warps * w / warps;
+    c1 = a.nchunks / warps * (w + 1) + a.nchunks % warps * (w + 1) / warps;
+}
+
+// This lane's places in its warp's ring of kPrefStages chunks (thread-private:
+// a lane copies and reads back only its own tokens, so no barrier is needed).
+constexpr int kPrefStages = 2;
+constexpr uint32_t kPrefStageBytes = kPrefThreads * kPrefQuads * (16 + 16 + 4);
+__device__ __forceinline__ void pref_ring_issue(const PrefArgs& a, int64_t t0, uint32_t stage) {
     const int lane = threadIdx.x & 31;
-    const int64_t b = pref_cu(a, s), e = pref_cu(a, s + 1);
-    sum = 0.0;
+    const float *p = a.logp + t0 + lane * 4, *q = a.ref + t0 + lane * 4;
+    const uint8_t* m = a.mask + t0 + lane * 4;
+#pragma unroll
+    for (int h = 0; h < kPrefQuads; ++h) {
+        const uint32_t at = stage + (h * kPrefThreads + threadIdx.x) * 16;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(p + 128 * h) : "memory");
+        if (a.ref)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + kPrefQuads * kPrefThreads * 16),
+                         "l"(q + 128 * h) : "memory");
+        if (a.mask)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                             stage + kPrefQuads * kPrefThreads * 32 + (h * kPrefThreads + threadIdx.x) * 4),
+                         "l"(m + 128 * h) : "memory");
+    }
+}
+__device__ __forceinline__ void pref_ring_read(const PrefArgs& a, uint32_t stage, PrefRaw& r) {
+#pragma unroll
+    for (int h = 0; h < kPrefQuads; ++h) {
+        const uint32_t at = stage + (h * kPrefThreads + threadIdx.x) * 16;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(r.p[4 * h]), "=f"(r.p[4 * h + 1]), "=f"(r.p[4 * h + 2]), "=f"(r.p[4 * h + 3]) : "r"(at)
+                     : "memory");
+        if (a.ref)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(r.q[4 * h]), "=f"(r.q[4 * h + 1]), "=f"(r.q[4 * h + 2]), "=f"(r.q[4 * h + 3])
+                         : "r"(at + kPrefQuads * kPrefThreads * 16) : "memory");
+        r.m[h] = 0x01010101u;
+        if (a.mask)
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r.m[h])
+                         : "r"(stage + kPrefQuads * kPrefThreads * 32 + (h * kPrefThreads + threadIdx.x) * 4)
+                         : "memory");
+    }
+}
+__device__ __forceinline__ int pref_bytes_set(uint32_t m) {
+    return __popc((m | ((m & 0x7f7f7f7fu) + 0x7f7f7f7fu)) & 0x80808080u);
+}
+
+template <bool kVec, bool kRing>
+__device__ __forceinline__ void pref_sums(const PrefArgs& a, int64_t w, int64_t warps, uint32_t ring) {
+    const int lane = threadIdx.x & 31;
+    int64_t c0, c1;
+    pref_run(a, w, warps, c0, c1);
+    if (c0 >= c1) return;
+    const int64_t base = c0 * kPrefChunk, len = (c1 - c0) * kPrefChunk;
+    const int64_t full = a.n / kPrefChunk;   // chunks before this are whole
+    if constexpr (kRing) {
+#pragma unroll
+        for (int k = 0; k < kPrefStages - 1; ++k) {
+            if (c0 + k < c1 && c0 + k < full) pref_ring_issue(a, base + k * kPrefChunk, ring + k * kPrefStageBytes);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+    PrefCursor cur;
+    pref_window<false>(a, base, len, pref_first_seq(a, base), 0.f, cur);
+    int stage = 0;
+    for (int64_t c = c0; c < c1; ++c) {
+        PrefRaw r;
+        if constexpr (kRing) {
+            const int64_t ahead = c + kPrefStages - 1;
+            const int into = stage == 0 ? kPrefStages - 1 : stage - 1;
+            if (ahead < c1 && ahead < full) pref_ring_issue(a, ahead * kPrefChunk, ring + into * kPrefStageBytes);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(kPrefStages - 1) : "memory");
+            if (c < full) pref_ring_read(a, ring + stage * kPrefStageBytes, r);
+            else pref_load<false>(a, c * kPrefChunk, r);
+            stage = stage == kPrefStages - 1 ? 0 : stage + 1;
+        } else {
+            pref_load<kVec>(a, c * kPrefChunk, r);
+        }
+        // a masked value is not used
+        float v[4 * kPrefQuads], quad[kPrefQuads];
+#pragma unroll
+        for (int h = 0; h < kPrefQuads; ++h) {
+#pragma unroll
+            for (int j = 4 * h; j < 4 * h + 4; ++j)
+                v[j] = pref_active(r.m, j) ? (a.ref ? r.p[j] - r.q[j] : r.p[j]) : 0.f;
+            quad[h] = (v[4 * h] + v[4 * h + 1]) + (v[4 * h + 2] + v[4 * h + 3]);
+        }
+        pref_walk<false>(a, base, len, 0.f, cur, (int32_t)((c - c0) * kPrefChunk), kPrefChunk,
+                         [&](int64_t s, int32_t lo, int32_t hi, float) {
+            float sum = 0.f;
+            int cnt = 0;
+#pragma unroll
+            for (int h = 0; h < kPrefQuads; ++h) {
+                const int q = h * 128 + lane * 4;
+                if (q >= lo && q + 4 <= hi) {
+                    sum += quad[h];
+                    cnt += pref_bytes_set(r.m[h]);
+                } else if (q + 4 > lo && q < hi) {   // a bound inside the quad: one lane or two
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (q + j >= lo && q + j < hi) {
+                            sum += v[4 * h + j];
+                            cnt += pref_active(r.m, 4 * h + j) ? 1 : 0;
+                        }
+                }
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            cnt = __reduce_add_sync(0xffffffffu, cnt);
+            if (lane == 0) a.slots[c + s] = PrefSlot{sum, cnt};
+        });
+    }
+}
+
+template <int kLanes>
+__device__ __forceinline__ int pref_group_sum(int v) {
+#pragma unroll
+    for (int o = kLanes / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int kLanes>
+__device__ __forceinline__ PrefTwo pref_group_sum(PrefTwo v) {
+#pragma unroll
+    for (int o = kLanes / 2; o >= 1; o >>= 1) {
+        // the same order in both lanes of an exchange, so that they get the same bits
+        const PrefTwo w{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)};
+        v = threadIdx.x & o ? pref_add(w, v) : pref_add(v, w);
+    }
+    return v;
+}
+
+// This lane's share of the sum and active tokens of the sequence [b, e).
+template <int kLanes>
+__device__ __forceinline__ void pref_sequence(const PrefArgs& a, int64_t s, int64_t b, int64_t e, PrefTwo& sum,
+                                              int& cnt) {
+    sum = {0.f, 0.f};
     cnt = 0;
     if (e > b) {
         const int64_t c1 = (e - 1) / kPrefChunk;
-        for (int64_t c = b / kPrefChunk + lane; c <= c1; c += 32) {
-            const PrefSlot q = a.slots[c + s];
-            sum += (double)q.sum;
-            cnt += q.count;
+        for (int64_t c = b / kPrefChunk + (threadIdx.x & (kLanes - 1)); c <= c1; c += kLanes) {
+            const float2 q = __ldcg(reinterpret_cast<const float2*>(a.slots + c + s));
+            sum = pref_add(sum, q.x);
+            cnt += __float_as_int(q.y);
         }
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
     }
 }
 
-__global__ void __launch_bounds__(kPrefThreads)
-k_pref_pairs(PrefArgs a) {
-    __shared__ double s_loss[kPrefThreads / 32];
-    __shared__ int64_t s_live[kPrefThreads / 32];
-    __shared__ bool s_last;
-    grid_dep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Pairs `first`, first + step, ... (one per group of kLanes lanes): coefficients and
+// rewards; this thread's share of the loss and of the live pairs.
+template <int kLanes>
+__device__ __forceinline__ void pref_pairs(const PrefArgs& a, int64_t first, int64_t step, PrefTwo& loss, int& live) {
     const int64_t pairs = a.nseq / 2;
-    double loss = 0.0;
-    int64_t live = 0;
-    for (int64_t p = (int64_t)blockIdx.x * (kPrefThreads / 32) + warp; p < pairs;
-         p += (int64_t)gridDim.x * (kPrefThreads / 32)) {
+    loss = {0.f, 0.f};
+    live = 0;
+    // every lane of the warp takes every turn (the sums are warp-wide shuffles)
+    for (int64_t p0 = first; __any_sync(0xffffffffu, p0 < pairs); p0 += step) {
+        const bool real = p0 < pairs;
+        const int64_t p = real ? p0 : pairs - 1;
         const int64_t sc = a.halves ? p : 2 * p, sj = a.halves ? p + pairs : 2 * p + 1;
-        double rc, rj;
-        int64_t nc, nj;
-        pref_sequence(a, sc, rc, nc);
-        pref_sequence(a, sj, rj, nj);
-        if (lane == 0) {
+        const int64_t bc = pref_cu(a, sc), ec = pref_cu(a, sc + 1), bj = pref_cu(a, sj), ej = pref_cu(a, sj + 1);
+        PrefTwo rc, rj;
+        int nc, nj;
+        pref_sequence<kLanes>(a, sc, bc, ec, rc, nc);
+        pref_sequence<kLanes>(a, sj, bj, ej, rj, nj);
+        rc = pref_settle(pref_group_sum<kLanes>(rc));
+        rj = pref_settle(pref_group_sum<kLanes>(rj));
+        nc = pref_group_sum<kLanes>(nc);
+        nj = pref_group_sum<kLanes>(nj);
+        if (real && (threadIdx.x & (kLanes - 1)) == 0) {
             float wc = 1.f, wj = 1.f;
             if (a.average) {
-                rc = nc > 0 ? rc / (double)nc : 0.0;
-                rj = nj > 0 ? rj / (double)nj : 0.0;
-                wc = nc > 0 ? 1.f / (float)nc : 0.f;
-                wj = nj > 0 ? 1.f / (float)nj : 0.f;
+                wc = nc > 0 ? __frcp_rn((float)nc) : 0.f;
+                wj = nj > 0 ? __frcp_rn((float)nj) : 0.f;
+                rc = {nc > 0 ? __fdiv_rn(rc.hi + rc.lo, (float)nc) : 0.f, 0.f};
+                rj = {nj > 0 ? __fdiv_rn(rj.hi + rj.lo, (float)nj) : 0.f, 0.f};
             }
             float each = 0.f, dh = 0.f;
             if (nc > 0 && nj > 0) {
-                const double h = rc - rj;
+                PrefTwo h = pref_settle(pref_add(rc, PrefTwo{-rj.hi, -rj.lo}));
                 if (a.kind == kPrefIpo) {
-                    const float t = (float)(h - 0.5 / (double)a.beta);
+                    const float t = pref_value(pref_add(h, PrefTwo{-a.target_hi, -a.target_lo}));
                     each = t * t;
                     dh = 2.f * t;
                 } else {
-                    const float u = (float)((double)a.beta * h - (double)a.margin);
+                    const float u = fmaf(a.beta, h.hi, fmaf(a.beta, h.lo, -a.margin));
                     if (a.kind == kPrefHinge) {
                         each = u != u ? u : fmaxf(0.f, 1.f - u);
                         dh = u != u ? u : (u < 1.f ? -a.beta : 0.f);
@@ -224,26 +399,127 @@ k_pref_pairs(PrefArgs a) {
                     }
                 }
                 ++live;
-                loss += (double)each;
+                loss = pref_add(loss, each);
             }
             a.coef[sc] = dh * wc;
             a.coef[sj] = -dh * wj;
-            a.rewards[2 * p] = (float)((double)a.beta * rc);
-            a.rewards[2 * p + 1] = (float)((double)a.beta * rj);
+            a.rewards[2 * p] = a.beta * (rc.hi + rc.lo);
+            a.rewards[2 * p + 1] = a.beta * (rj.hi + rj.lo);
         }
     }
+}
+
+// Sum of (l, k) over a CTA of kThreads, in thread 0, in a fixed order.
+template <int kThreads>
+__device__ __forceinline__ void pref_cta_sum(PrefTwo& l, int& k, PrefTwo* sl, int* sk) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    l = pref_group_sum<32>(l);
+    k = pref_group_sum<32>(k);
+    __syncthreads();
     if (lane == 0) {
-        s_loss[warp] = loss;
-        s_live[warp] = live;
+        sl[warp] = l;
+        sk[warp] = k;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        double l = 0.0;
-        int64_t k = 0;
-        for (int w = 0; w < kPrefThreads / 32; ++w) {
-            l += s_loss[w];
-            k += s_live[w];
+        l = {0.f, 0.f};
+        k = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            l = pref_add(l, sl[w]);
+            k += sk[w];
         }
+    }
+}
+__device__ __forceinline__ float pref_inv_den(const PrefArgs& a, int live) {
+    return live > 0 ? __frcp_rn(a.normalizer > 0.f ? a.normalizer : (float)live) : 0.f;
+}
+__device__ __forceinline__ float pref_loss(const PrefArgs& a, PrefTwo loss, int live) {
+    return live > 0 ? __fdiv_rn(pref_value(loss), a.normalizer > 0.f ? a.normalizer : (float)live) : 0.f;
+}
+
+// The gradients of warp w's chunks; `wait` returns 1 / D once it and the
+// coefficients are there.
+template <bool kVec, class F>
+__device__ __forceinline__ void pref_grad(const PrefArgs& a, int64_t w, int64_t warps, F wait) {
+    const int lane = threadIdx.x & 31;
+    int64_t c0, c1;
+    pref_run(a, w, warps, c0, c1);
+    if (c0 >= c1) {
+        wait();
+        return;
+    }
+    const int64_t base = c0 * kPrefChunk, len = (c1 - c0) * kPrefChunk;
+    uint32_t next[kPrefQuads];
+    pref_mask<kVec>(a, base, next);
+    const int64_t s = pref_first_seq(a, base);
+    const float inv_den = wait();
+    PrefCursor cur;
+    pref_window<true>(a, base, len, s, inv_den, cur);
+    for (int64_t c = c0; c < c1; ++c) {
+        const int64_t t0 = c * kPrefChunk;
+        uint32_t m[kPrefQuads];
+#pragma unroll
+        for (int h = 0; h < kPrefQuads; ++h) m[h] = next[h];
+        if (c + 1 < c1) pref_mask<kVec>(a, t0 + kPrefChunk, next);
+        float v[4 * kPrefQuads] = {};
+        pref_walk<true>(a, base, len, inv_den, cur, (int32_t)((c - c0) * kPrefChunk), kPrefChunk,
+                        [&](int64_t, int32_t lo, int32_t hi, float g) {
+#pragma unroll
+            for (int h = 0; h < kPrefQuads; ++h) {
+                const int q = h * 128 + lane * 4;
+                if (q >= lo && q + 4 <= hi) {
+                    v[4 * h] = v[4 * h + 1] = v[4 * h + 2] = v[4 * h + 3] = g;
+                } else if (q + 4 > lo && q < hi) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (q + j >= lo && q + j < hi) v[4 * h + j] = g;
+                }
+            }
+        });
+#pragma unroll
+        for (int j = 0; j < 4 * kPrefQuads; ++j) v[j] = pref_active(m, j) ? v[j] : 0.f;
+        const int64_t i0 = t0 + lane * 4;
+        if (kVec && t0 + kPrefChunk <= a.n) {
+#pragma unroll
+            for (int h = 0; h < kPrefQuads; ++h)
+                __stcs(reinterpret_cast<float4*>(a.grad + i0) + 32 * h,
+                       make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4 * kPrefQuads; ++j) {
+                const int64_t i = i0 + (j >> 2) * 128 + (j & 3);
+                if (i < a.n) a.grad[i] = v[j];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- three launches
+
+template <bool kVec>
+__global__ void __launch_bounds__(kPrefThreads, kPrefSumCtas)
+k_pref_sums(PrefArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+    extern __shared__ __align__(16) unsigned char pref_smem[];
+    pref_sums<kVec, kVec>(a, (int64_t)blockIdx.x * (kPrefThreads / 32) + (threadIdx.x >> 5),
+                          (int64_t)gridDim.x * (kPrefThreads / 32), (uint32_t)__cvta_generic_to_shared(pref_smem));
+}
+
+template <int kLanes>
+__global__ void __launch_bounds__(kPrefThreads)
+k_pref_pairs(PrefArgs a) {
+    __shared__ PrefTwo sl[kPrefThreads / 32];
+    __shared__ int sk[kPrefThreads / 32];
+    __shared__ bool s_last;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_dep_wait();
+    constexpr int kGroups = kPrefThreads / kLanes;
+    PrefTwo l;
+    int k;
+    pref_pairs<kLanes>(a, (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes, (int64_t)gridDim.x * kGroups, l, k);
+    pref_cta_sum<kPrefThreads>(l, k, sl, sk);
+    if (threadIdx.x == 0) {
         a.part_loss[blockIdx.x] = l;
         a.part_live[blockIdx.x] = k;
         __threadfence();
@@ -253,76 +529,68 @@ k_pref_pairs(PrefArgs a) {
     __syncthreads();
     if (!s_last) return;
     // the last CTA: fold in an order fixed by the grid
-    double l = 0.0;
-    int64_t k = 0;
+    l = {0.f, 0.f};
+    k = 0;
     for (int i = threadIdx.x; i < (int)gridDim.x; i += kPrefThreads) {
-        l += __ldcg(a.part_loss + i);
+        const float2 q = __ldcg(reinterpret_cast<const float2*>(a.part_loss + i));
+        l = pref_add(l, PrefTwo{q.x, q.y});
         k += __ldcg(a.part_live + i);
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        l += __shfl_xor_sync(0xffffffffu, l, o);
-        k += __shfl_xor_sync(0xffffffffu, k, o);
-    }
-    if (lane == 0) {
-        s_loss[warp] = l;
-        s_live[warp] = k;
-    }
-    __syncthreads();
+    pref_cta_sum<kPrefThreads>(l, k, sl, sk);
     if (threadIdx.x == 0) {
-        l = 0.0;
-        k = 0;
-        for (int w = 0; w < kPrefThreads / 32; ++w) {
-            l += s_loss[w];
-            k += s_live[w];
-        }
-        const double den = a.normalizer > 0.f ? (double)a.normalizer : (double)k;
-        *a.inv_den = k > 0 ? (float)(1.0 / den) : 0.f;
-        *a.loss = k > 0 ? (float)(l / den) : 0.f;
+        *a.inv_den = pref_inv_den(a, k);
+        *a.loss = pref_loss(a, l, k);
     }
 }
 
 template <bool kVec>
-__global__ void __launch_bounds__(kPrefThreads)
+__global__ void __launch_bounds__(kPrefThreads, kPrefGradCtas)
 k_pref_grad(PrefArgs a) {
-    grid_dep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (kPrefThreads / 32);
-    const float inv_den = __ldcg(a.inv_den);
-    for (int64_t c = (int64_t)blockIdx.x * (kPrefThreads / 32) + (threadIdx.x >> 5); c < a.nchunks; c += warps) {
-        const int64_t t0 = c * kPrefChunk, t1 = t0 + kPrefChunk < a.n ? t0 + kPrefChunk : a.n;
-        uint32_t bits = pref_mask4(a.mask, t0 + lane * 4, a.n, kVec);
-        bits |= pref_mask4(a.mask, t0 + 128 + lane * 4, a.n, kVec) << 4;
-        float v[8] = {};
-        int64_t s = a.first_seq[c];
-        int64_t b = s < a.nseq ? pref_cu(a, s) : t1;
-        while (s < a.nseq && b < t1) {
-            const int64_t e = pref_cu(a, s + 1);
-            if (e > b && e > t0) {
-                const float g = __ldcg(a.coef + s) * inv_den;
-                const int lo = b > t0 ? (int)(b - t0) : 0, hi = e < t1 ? (int)(e - t0) : kPrefChunk;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int k = pref_tok(lane, j);
-                    if (k >= lo && k < hi && ((bits >> j) & 1u)) v[j] = g;
-                }
-            }
-            b = e;
-            ++s;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t i = t0 + h * 128 + lane * 4;
-            if (kVec && i + 4 <= a.n) {
-                __stcs(reinterpret_cast<float4*>(a.grad + i),
-                       make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]));
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (i + k < a.n) a.grad[i + k] = v[4 * h + k];
-            }
-        }
+    pref_grad<kVec>(a, (int64_t)blockIdx.x * (kPrefThreads / 32) + (threadIdx.x >> 5),
+                    (int64_t)gridDim.x * (kPrefThreads / 32), [&] {
+        grid_dep_wait();
+        return __ldcg(a.inv_den);
+    });
+}
+
+// ---------------------------------------------------------------- one cluster
+
+constexpr int kPrefClusterCtas = 8, kPrefClusterThreads = 512;
+
+__device__ __forceinline__ void pref_cluster_sync() {
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <bool kVec>
+__global__ void __cluster_dims__(kPrefClusterCtas, 1, 1) __launch_bounds__(kPrefClusterThreads)
+k_pref_cluster(PrefArgs a) {
+    constexpr int kWarps = kPrefClusterThreads / 32, kGroups = kPrefClusterThreads / 8;
+    __shared__ PrefTwo sl[kWarps];
+    __shared__ int sk[kWarps];
+    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * kWarps;
+    pref_sums<kVec, false>(a, w, warps, 0);
+    pref_cluster_sync();
+    PrefTwo l;
+    int k;
+    pref_pairs<8>(a, (int64_t)blockIdx.x * kGroups + threadIdx.x / 8, (int64_t)gridDim.x * kGroups, l, k);
+    pref_cta_sum<kPrefClusterThreads>(l, k, sl, sk);
+    if (threadIdx.x == 0) {
+        a.part_loss[blockIdx.x] = l;
+        a.part_live[blockIdx.x] = k;
     }
+    pref_cluster_sync();
+    l = {0.f, 0.f};
+    k = 0;
+#pragma unroll
+    for (int i = 0; i < kPrefClusterCtas; ++i) {
+        const float2 q = __ldcg(reinterpret_cast<const float2*>(a.part_loss + i));
+        l = pref_add(l, PrefTwo{q.x, q.y});
+        k += __ldcg(a.part_live + i);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.loss = pref_loss(a, l, k);
+    const float inv_den = pref_inv_den(a, k);
+    pref_grad<kVec>(a, w, warps, [&] { return inv_den; });
 }
 
 }  // namespace flp

@@ -8,20 +8,24 @@ import ctypes
 import torch
 
 from . import _lib
-from ._args import _cuda, _dtype, _opt_ptr, _rows, _stream, _vec
+from ._args import _DTYPES, _cuda, _dtype, _opt_ptr, _rows, _stream, _vec
 
 
 def _affine(weight, bias, x, d: int) -> int:
     """The C dtype of weight and bias (x's when neither is given)."""
-    given = [(name, t) for name, t in (("weight", weight), ("bias", bias)) if t is not None]
-    for name, t in given:
-        if t.dtype not in (x.dtype, torch.float32):
-            raise TypeError(f"{name} must be {x.dtype} or torch.float32, got {t.dtype}")
-        if t.dtype != given[0][1].dtype:
-            raise TypeError("weight and bias must have the same dtype")
-        _vec(t, name, d, t.dtype)
-        _cuda(t)
-    return _dtype(given[0][1] if given else x, "weight")
+    first = weight if weight is not None else bias
+    if first is None:
+        return _DTYPES[x.dtype]
+    dtype = first.dtype
+    if dtype != x.dtype and dtype != torch.float32:
+        raise TypeError(f"weight and bias must be {x.dtype} or torch.float32, got {dtype}")
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            if t.dtype != dtype:
+                raise TypeError("weight and bias must have the same dtype")
+            _vec(t, name, d, dtype)
+            _cuda(t)
+    return _DTYPES[dtype]
 
 
 def fused_layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -35,27 +39,34 @@ def fused_layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None
     n, d, ld = _rows(x, "x")
     dt = _dtype(x, "x")
     wdt = _affine(weight, bias, x, d)
-    if not 0.0 <= float(eps) < float("inf"):
+    if not 0.0 <= eps < float("inf"):
         raise ValueError(f"eps must be finite and >= 0, got {eps}")
-    dev = x.device
-    y = torch.empty((n, d), dtype=x.dtype, device=dev) if y is None else y
-    if y.dtype != x.dtype or tuple(y.shape) != (n, d):
-        raise ValueError("y must have x's dtype and shape")
-    _, _, ld_y = _rows(y, "y")
-    if center and mean is None:
-        mean = torch.empty(n, dtype=torch.float32, device=dev)
-    rstd = torch.empty(n, dtype=torch.float32, device=dev) if rstd is None else rstd
-    _cuda(x, y, rstd)
-    _vec(rstd, "rstd", n, torch.float32)
-    if center:
+    _cuda(x)
+    if y is None:
+        y, ld_y = torch.empty((n, d), dtype=x.dtype, device=x.device), d
+    else:
+        if y.dtype != x.dtype or tuple(y.shape) != (n, d):
+            raise ValueError("y must have x's dtype and shape")
+        _, _, ld_y = _rows(y, "y")
+        _cuda(y)
+    if rstd is None:
+        rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+    else:
+        _vec(rstd, "rstd", n, torch.float32)
+        _cuda(rstd)
+    if not center:
+        mean = None
+    elif mean is None:
+        mean = torch.empty(n, dtype=torch.float32, device=x.device)
+    else:
         _vec(mean, "mean", n, torch.float32)
         _cuda(mean)
     if n > 0:
         st = _lib.load().fused_layer_norm_forward(
-            x.data_ptr(), dt, n, d, ld, _opt_ptr(weight), _opt_ptr(bias), wdt, float(eps), int(bool(center)),
-            y.data_ptr(), ld_y, _opt_ptr(mean) if center else None, rstd.data_ptr(), _stream(x))
+            x.data_ptr(), dt, n, d, ld, _opt_ptr(weight), _opt_ptr(bias), wdt, eps, 1 if center else 0,
+            y.data_ptr(), ld_y, _opt_ptr(mean), rstd.data_ptr(), _stream(x))
         _lib.check("fused_layer_norm_forward", st)
-    return y, (mean if center else None), rstd
+    return y, mean, rstd
 
 
 def fused_layer_norm_backward_workspace_size(d: int) -> int:
@@ -81,44 +92,52 @@ def fused_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.T
     n, d, ld = _rows(x, "x")
     dt = _dtype(x, "x")
     wdt = _affine(weight, None, x, d)
-    if dy.dtype not in (x.dtype, torch.float32):
+    if dy.dtype != x.dtype and dy.dtype != torch.float32:
         raise TypeError(f"dy must be {x.dtype} or torch.float32, got {dy.dtype}")
     if tuple(dy.shape) != (n, d):
         raise ValueError(f"dy must have x's shape {(n, d)}, got {tuple(dy.shape)}")
     _, _, ld_dy = _rows(dy, "dy")
     _vec(rstd, "rstd", n, torch.float32)
-    if center:
-        if mean is None:
-            raise ValueError("center=True needs the forward's mean")
+    _cuda(dy, x, rstd)
+    if not center:
+        mean = None
+    elif mean is None:
+        raise ValueError("center=True needs the forward's mean")
+    else:
         _vec(mean, "mean", n, torch.float32)
         _cuda(mean)
-    dev = x.device
-    dx = torch.empty((n, d), dtype=x.dtype, device=dev) if dx is None else dx
-    if dx.dtype != x.dtype or tuple(dx.shape) != (n, d):
-        raise ValueError("dx must have x's dtype and shape")
-    _, _, ld_dx = _rows(dx, "dx")
-    if accumulate and ((with_dweight and dweight is None) or (with_dbias and dbias is None)):
-        raise ValueError("accumulate needs the dweight and dbias tensors to add to")
-    if with_dweight and dweight is None:
-        dweight = torch.empty(d, dtype=torch.float32, device=dev)
-    if with_dbias and dbias is None:
-        dbias = torch.empty(d, dtype=torch.float32, device=dev)
-    dweight, dbias = (dweight if with_dweight else None), (dbias if with_dbias else None)
-    for name, t in (("dweight", dweight), ("dbias", dbias)):
-        if t is not None:
+    if dx is None:
+        dx, ld_dx = torch.empty((n, d), dtype=x.dtype, device=x.device), d
+    else:
+        if dx.dtype != x.dtype or tuple(dx.shape) != (n, d):
+            raise ValueError("dx must have x's dtype and shape")
+        _, _, ld_dx = _rows(dx, "dx")
+        _cuda(dx)
+    sums = []
+    for name, t, wanted in (("dweight", dweight, with_dweight), ("dbias", dbias, with_dbias)):
+        if not wanted:
+            t = None
+        elif t is not None:
             _vec(t, name, d, torch.float32)
             _cuda(t)
-    _cuda(dy, x, rstd, dx)
-    if workspace is None and n > 0 and (with_dweight or with_dbias):
-        workspace = torch.empty(fused_layer_norm_backward_workspace_size(d), dtype=torch.uint8, device=dev)
+        elif accumulate:
+            raise ValueError(f"accumulate needs the {name} tensor to add to")
+        else:
+            t = torch.empty(d, dtype=torch.float32, device=x.device)
+        sums.append(t)
+    dweight, dbias = sums
     wptr, wbytes = None, 0
     if workspace is not None:
         _cuda(workspace)
         wptr, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif n > 0 and (with_dweight or with_dbias):
+        wbytes = fused_layer_norm_backward_workspace_size(d)
+        workspace = torch.empty(wbytes, dtype=torch.uint8, device=x.device)
+        wptr = workspace.data_ptr()
     st = _lib.load().fused_layer_norm_backward(
-        dy.data_ptr(), _dtype(dy, "dy"), ld_dy, x.data_ptr(), dt, n, d, ld, _opt_ptr(weight), wdt,
-        _opt_ptr(mean) if center else None, rstd.data_ptr(), int(bool(center)), wptr, wbytes, dx.data_ptr(), ld_dx,
-        _opt_ptr(dweight), _opt_ptr(dbias), int(bool(accumulate)), _stream(x))
+        dy.data_ptr(), _DTYPES[dy.dtype], ld_dy, x.data_ptr(), dt, n, d, ld, _opt_ptr(weight), wdt,
+        _opt_ptr(mean), rstd.data_ptr(), 1 if center else 0, wptr, wbytes, dx.data_ptr(), ld_dx,
+        _opt_ptr(dweight), _opt_ptr(dbias), 1 if accumulate else 0, _stream(x))
     _lib.check("fused_layer_norm_backward", st)
     return dx, dweight, dbias
 

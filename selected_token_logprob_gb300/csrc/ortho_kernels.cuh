@@ -22,8 +22,11 @@
 // A and B are symmetric: only tiles on and above the diagonal are computed, and
 // each is written to both places.
 //
-// Each product is one launch of persistent CTAs with six warps: one TMA
-// producer, one MMA issuer, four epilogue warps (one accumulator row a thread).
+// Each product is one launch of persistent CTAs (or CTA pairs) with six warps:
+// one TMA producer, one MMA issuer, four epilogue warps (one accumulator row a
+// thread).  The epilogue of a tile overlaps the next tile's MMAs; what it reads
+// beside the accumulators (X's hi and lo, or A0) comes by TMA into boxes of 32
+// rows x 64 columns a warp, which it rewrites in place and stores by TMA.
 // Every wait is bounded: a wait that runs out sets the error word and the CTA's
 // abort flag, the copies and MMAs in flight are waited for, TMEM is freed and
 // the kernel returns.
@@ -39,7 +42,6 @@ constexpr float kOrthScale = 256.f;          // of every FP16 operand
 constexpr float kOrthLoScale = 2048.f;       // of lo, on top: hi's rounding is below 2^-11
 constexpr long long kOrthWaitCycles = 4000000000LL;
 constexpr int kOrthThreads = 192;
-constexpr int kOrthBM = 128;
 constexpr int kOrthBK = 64;
 constexpr int kOrthParts = 128;              // partial sums of squares per matrix
 
@@ -48,18 +50,15 @@ static __device__ int g_orth_error;          // 1 = a bounded wait ran out
 enum OrthMode { kOrthGram = 0, kOrthPoly = 1, kOrthApply = 2, kOrthFinal = 3 };
 
 struct OrthArgs {
-    int64_t batch, m, n;      // m <= n, of X
+    int64_t m, n;             // m <= n, of X
     int64_t mp, np;           // padded to multiples of 64
-    int tiles_m, tiles_n;     // of the output: rows of 128, columns of the kernel's N
-    int64_t units;            // output tiles over the batch
+    int tiles_m, tiles_n;     // of the output: rows of 128 (a pair: 256), columns of the kernel's N
+    int64_t per;              // output tiles of one matrix
+    int64_t units;            // over the batch
     int nkb;                  // K blocks of 64
     float a, b, c;            // this step's coefficients
-    __half *mat;              // Gram: A0 out; Poly: A0 in
-    __half *mat_out;          // Poly: B0 out
+    __half* mat_out;          // Gram: A0, Poly: B0 (for the mirrored tiles)
     float *d, *e;             // [batch mp] diagonals
-    const __half *x_hi;       // Apply, Final: X
-    __half *x_lo;             // Apply: in place; Final: read
-    __half *x_out;            // Apply: the next X's hi
     void* out;                // Final
     int out_dtype, transposed, vec_out;
     int64_t ld_out, stride_out;
@@ -79,9 +78,9 @@ __device__ __forceinline__ uint64_t orth_desc_mn(uint32_t saddr) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 // kind::f16 with FP16 operands (type fields 0), FP32 accumulators; bit 16: B MN-major.
-template <int kBN, bool kBmn>
+template <int kBM, int kBN, bool kBmn>
 __host__ __device__ constexpr uint32_t orth_idesc() {
-    return (1u << 4) | ((kBmn ? 1u : 0u) << 16) | ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(kOrthBM >> 4) << 24);
+    return (1u << 4) | ((kBmn ? 1u : 0u) << 16) | ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
 }
 
 __device__ __forceinline__ bool orth_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -100,25 +99,44 @@ __device__ __forceinline__ bool orth_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+template <bool kPair>
+__device__ __forceinline__ bool orth_wait_acc(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if constexpr (!kPair) return orth_wait(bar, parity, abort_flag);
+    if (mbar_try_cluster(bar, parity)) return true;   // the peer's warps arrive on it too
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_cluster(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > kOrthWaitCycles) {
+                *abort_flag = 1;
+                atomicExch(&g_orth_error, 1);
+                return false;
+            }
+        }
+    }
+}
+
 struct OrthUnit {
     int64_t batch;
     int mb, nb;
 };
-// Output tile u: row by row; of a symmetric product only tiles with nb >= mb.
-template <bool kSym>
+// Output tile u: row by row; of a symmetric product only tiles that reach the
+// diagonal or lie right of it.
+template <bool kSym, int kBM, int kBN>
 __device__ __forceinline__ OrthUnit orth_unit(int64_t u, const OrthArgs& p) {
     OrthUnit w;
-    const int64_t per = kSym ? (int64_t)p.tiles_m * (p.tiles_m + 1) / 2 : (int64_t)p.tiles_m * p.tiles_n;
-    w.batch = u / per;
-    int64_t t = u - w.batch * per;
+    w.batch = u / p.per;
+    int64_t t = u - w.batch * p.per;
     if (kSym) {
-        int mb = 0;
-        while (t >= p.tiles_m - mb) {
-            t -= p.tiles_m - mb;
+        int mb = 0, first = 0;
+        while (t >= p.tiles_n - first) {
+            t -= p.tiles_n - first;
             ++mb;
+            first = mb * kBM / kBN;
         }
         w.mb = mb;
-        w.nb = mb + (int)t;
+        w.nb = first + (int)t;
     } else {
         w.mb = (int)(t / p.tiles_n);
         w.nb = (int)(t - (int64_t)w.mb * p.tiles_n);
@@ -126,75 +144,103 @@ __device__ __forceinline__ OrthUnit orth_unit(int64_t u, const OrthArgs& p) {
     return w;
 }
 
-template <int kBN>
-constexpr uint32_t kOrthStageBytes = (kOrthBM + kBN) * kOrthBK * 2;
-template <int kBN>
-constexpr int kOrthStages = 196608 / (int)kOrthStageBytes<kBN>;
-template <int kBN>
-constexpr size_t kOrthSmemBytes = 1024 + (size_t)kOrthStages<kBN> * kOrthStageBytes<kBN> + 256;
+// Shared memory of a CTA: the stages (128 rows of A and its rows or columns of
+// B per K block), a block of barriers, and two 8 KB boxes per epilogue warp.
+constexpr uint32_t kOrthABytes = 128 * kOrthBK * 2;
+template <int kBN, bool kPair>
+constexpr uint32_t kOrthBBytes = (kPair ? kBN / 2 : kBN) * kOrthBK * 2;
+template <int kBN, bool kPair>
+constexpr uint32_t kOrthStageBytes = kOrthABytes + kOrthBBytes<kBN, kPair>;
+template <int kBN, bool kPair>
+constexpr int kOrthStages = 131072 / (int)kOrthStageBytes<kBN, kPair>;
+constexpr uint32_t kOrthBoxBytes = 32 * 64 * 2;
+template <int kBN, bool kPair>
+constexpr size_t kOrthSmemBytes =
+    1024 + (size_t)kOrthStages<kBN, kPair> * kOrthStageBytes<kBN, kPair> + 1024 + 4 * 4 * (size_t)kOrthBoxBytes;
 
 __device__ __forceinline__ uint32_t orth_pack(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// 16-byte piece j of row `lane` of a box.
+__device__ __forceinline__ uint32_t orth_piece(uint32_t box, int lane, int j) {
+    return box + (uint32_t)lane * 128 + (uint32_t)((j ^ (lane & 7)) * 16);
+}
 
-// The 32 accumulators of row i, columns c0 .. c0 + 31 (all inside the padded
-// output) of one matrix of the batch.
+// Where a warp's 32 rows of a tile lie.
+struct OrthRows {
+    int64_t row;      // this thread's row of the batch's padded rows
+    int64_t i;        // of its matrix
+    int64_t i_warp;   // the warp's first
+};
+
+// 32 accumulators of row w.i, columns c0 .. c0 + 31 (c0 a multiple of 32, all
+// inside the padded output), with the boxes of the 64-column chunk they lie in;
+// the results go back into the boxes.  `diag`: these columns meet the warp's rows.
 template <int kMode>
-__device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int64_t batch, bool mirror, int64_t i, int64_t c0,
-                                              uint32_t (&r)[32]) {
+__device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows& w, bool diag, bool mirror,
+                                              int64_t batch, int64_t c0, uint32_t box, int lane, uint32_t (&r)[32]) {
     constexpr float kInv = 1.f / kOrthScale;
-    const int64_t row = batch * p.mp + i;
+    const int half = (int)((c0 >> 5) & 1) * 4;   // first 16-byte piece of these columns
+    float v[32];
     if constexpr (kMode == kOrthGram || kMode == kOrthPoly) {
-        float v[32];
         if constexpr (kMode == kOrthGram) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                v[j] = __uint_as_float(r[j]) * kInv;   // scaled A
-                if (c0 + j == i) {
-                    p.d[row] = v[j] * kInv;
-                    v[j] = 0.f;
-                }
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * kInv;   // scaled A
+            if (diag) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c0 + j == w.i) {
+                        p.d[w.row] = v[j] * kInv;
+                        v[j] = 0.f;
+                    }
             }
         } else {
-            const uint4* src = reinterpret_cast<const uint4*>(p.mat + row * p.mp + c0);
-            const float di = p.d[row];
+            const float di = p.d[w.row];
+            const float4* dc = reinterpret_cast<const float4*>(p.d + batch * p.mp + c0);
+            const float k0 = p.b + p.c * di;
+            float sq = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint4 w = src[q];
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                const uint4 x = lds_v4(orth_piece(box, lane, half + q));
+                const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int j = 8 * q + k;
-                    const float a0 = (k & 1) ? h_hi(ws[k >> 1]) : h_lo(ws[k >> 1]);
-                    const float dj = p.d[batch * p.mp + c0 + j];
-                    const float sq = __uint_as_float(r[j]) * kInv;   // scaled A0^2
-                    v[j] = (p.b + p.c * (di + dj)) * a0 + p.c * sq;
-                    if (c0 + j == i) {
-                        p.e[row] = p.b * di + p.c * (di * di) + p.c * (sq * kInv);
-                        v[j] = 0.f;
+                for (int g = 0; g < 2; ++g) {
+                    const float4 dj = dc[2 * q + g];
+                    const float ds[4] = {dj.x, dj.y, dj.z, dj.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = 8 * q + 4 * g + k;
+                        const float a0 = (k & 1) ? h_hi(ws[2 * g + (k >> 1)]) : h_lo(ws[2 * g + (k >> 1)]);
+                        const float s = __uint_as_float(r[j]) * kInv;   // scaled A0^2
+                        if (diag && c0 + j == w.i) sq = s;
+                        v[j] = (k0 + p.c * ds[k]) * a0 + p.c * s;
                     }
                 }
             }
+            if (diag && w.i >= c0 && w.i < c0 + 32) {
+                p.e[w.row] = p.b * di + p.c * (di * di) + p.c * (sq * kInv);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c0 + j == w.i) v[j] = 0.f;
+            }
         }
-        __half* dst = kMode == kOrthGram ? p.mat : p.mat_out;
-        uint4* o = reinterpret_cast<uint4*>(dst + row * p.mp + c0);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            o[q] = make_uint4(orth_pack(v[8 * q], v[8 * q + 1]), orth_pack(v[8 * q + 2], v[8 * q + 3]),
-                              orth_pack(v[8 * q + 4], v[8 * q + 5]), orth_pack(v[8 * q + 6], v[8 * q + 7]));
+            sts_v4(orth_piece(box, lane, half + q), orth_pack(v[8 * q], v[8 * q + 1]),
+                   orth_pack(v[8 * q + 2], v[8 * q + 3]), orth_pack(v[8 * q + 4], v[8 * q + 5]),
+                   orth_pack(v[8 * q + 6], v[8 * q + 7]));
         if (mirror) {
+            __half* o = p.mat_out + (batch * p.mp + c0) * p.mp + w.i;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) dst[(batch * p.mp + c0 + j) * p.mp + i] = __float2half_rn(v[j]);
+            for (int j = 0; j < 32; ++j) o[j * p.mp] = __float2half_rn(v[j]);
         }
     } else {
-        const float ai = p.a + p.e[row];
-        const uint4* hi = reinterpret_cast<const uint4*>(p.x_hi + row * p.np + c0);
-        uint4* lo = reinterpret_cast<uint4*>(p.x_lo + row * p.np + c0);
-        float v[32];
+        const float ai = p.a + p.e[w.row];
+        const uint32_t lo_box = box + kOrthBoxBytes;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const uint4 h = hi[q], l = lo[q];
+            const uint4 h = lds_v4(orth_piece(box, lane, half + q)), l = lds_v4(orth_piece(lo_box, lane, half + q));
             const uint32_t hs[4] = {h.x, h.y, h.z, h.w}, ls[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -204,7 +250,6 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int64_t batch, 
             }
         }
         if constexpr (kMode == kOrthApply) {
-            uint4* o = reinterpret_cast<uint4*>(p.x_out + row * p.np + c0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t hw[4], lw[4];
@@ -214,63 +259,128 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int64_t batch, 
                     hw[k] = orth_pack(x0, x1);
                     lw[k] = orth_pack((x0 - h_lo(hw[k])) * kOrthLoScale, (x1 - h_hi(hw[k])) * kOrthLoScale);
                 }
-                o[q] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                lo[q] = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                sts_v4(orth_piece(box, lane, half + q), hw[0], hw[1], hw[2], hw[3]);
+                sts_v4(orth_piece(lo_box, lane, half + q), lw[0], lw[1], lw[2], lw[3]);
             }
         } else {
-            if (i >= p.m) return;
             const float s = p.scale * kInv;
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= s;
             const int64_t base = batch * p.stride_out;
-            if (p.vec_out && !p.transposed && c0 + 32 <= p.n) {
-                if (p.out_dtype == 2) {
-                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + base + i * p.ld_out + c0);
+            if (p.transposed) {   // 32 lanes, 32 neighbours of each output row
+                if (w.i < p.m) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                } else {
-                    uint4* o =
-                        reinterpret_cast<uint4*>(static_cast<unsigned short*>(p.out) + base + i * p.ld_out + c0);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(v[8 * q + 2 * k], v[8 * q + 2 * k + 1]);
-                        o[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int j = 0; j < 32; ++j) {
+                        if (c0 + j < p.n) {
+                            const int64_t at = base + (c0 + j) * p.ld_out + w.i;
+                            if (p.out_dtype == 2) static_cast<float*>(p.out)[at] = v[j];
+                            else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v[j]);
+                        }
                     }
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    if (c0 + j < p.n) {
-                        const int64_t at = base + (p.transposed ? (c0 + j) * p.ld_out + i : i * p.ld_out + c0 + j);
-                        if (p.out_dtype == 2) static_cast<float*>(p.out)[at] = v[j];
-                        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v[j]);
+                for (int q = 0; q < 4; ++q)
+                    sts_v4(orth_piece(box, lane, half + q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                           pack_bf16x2(v[8 * q + 2], v[8 * q + 3]), pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                           pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+            }
+        }
+    }
+}
+
+// Final, FP32 output: 64 columns from both boxes back into both boxes (32 columns each).
+__device__ __forceinline__ void orth_final_f32(const OrthArgs& p, const OrthRows& w, uint32_t box, int lane,
+                                               uint32_t (&r0)[32], uint32_t (&r1)[32]) {
+    constexpr float kInv = 1.f / kOrthScale;
+    const float ai = p.a + p.e[w.row], s = p.scale * kInv;
+    const uint32_t lo_box = box + kOrthBoxBytes;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const uint4 h = lds_v4(orth_piece(box, lane, q)), l = lds_v4(orth_piece(lo_box, lane, q));
+        const uint32_t hs[4] = {h.x, h.y, h.z, h.w}, ls[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float xh = (k & 1) ? h_hi(hs[k >> 1]) : h_lo(hs[k >> 1]);
+            const float xl = (k & 1) ? h_hi(ls[k >> 1]) : h_lo(ls[k >> 1]);
+            uint32_t& r = q < 4 ? r0[8 * q + k] : r1[8 * (q - 4) + k];
+            r = __float_as_uint(s * (ai * (xh + xl * (1.f / kOrthLoScale)) + __uint_as_float(r) * kInv));
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        sts_v4(orth_piece(box, lane, q), r0[4 * q], r0[4 * q + 1], r0[4 * q + 2], r0[4 * q + 3]);
+        sts_v4(orth_piece(lo_box, lane, q), r1[4 * q], r1[4 * q + 1], r1[4 * q + 2], r1[4 * q + 3]);
+    }
+}
+
+// Final: one box (32 rows of 128 bytes, kEach values a row from column c0 on) to
+// the output, a row's pieces by neighbouring lanes.
+template <class T>
+__device__ __forceinline__ void orth_write_out(const OrthArgs& p, const OrthRows& w, int64_t batch, int64_t c0,
+                                               uint32_t box, int lane) {
+    constexpr int kEach = 128 / (int)sizeof(T), kPiece = 16 / (int)sizeof(T);
+    T* out = static_cast<T*>(p.out) + batch * p.stride_out;
+    if (p.vec_out && c0 + kEach <= p.n) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            const int r = g * 4 + (lane >> 3), j = lane & 7;
+            if (w.i_warp + r < p.m) {
+                const uint4 x = lds_v4(orth_piece(box, r, j));
+                *reinterpret_cast<uint4*>(out + (w.i_warp + r) * p.ld_out + c0 + j * kPiece) = x;
+            }
+        }
+    } else {
+        for (int r = 0; r < 32 && w.i_warp + r < p.m; ++r) {
+#pragma unroll
+            for (int k = 0; k < kEach / 32; ++k) {
+                const int e = k * 32 + lane;
+                if (c0 + e < p.n) {
+                    const uint32_t at = orth_piece(box, r, e / kPiece) + (e % kPiece) * (uint32_t)sizeof(T);
+                    T x;
+                    if constexpr (sizeof(T) == 4) {
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+                    } else {
+                        unsigned short h;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at) : "memory");
+                        x = *reinterpret_cast<const T*>(&h);
                     }
+                    out[(w.i_warp + r) * p.ld_out + c0 + e] = x;
                 }
             }
         }
     }
 }
 
-template <int kMode, int kBN>
+// D tiles = A B^T (Gram, Poly; both operands K-major rows) or A B (Apply, Final;
+// B read MN-major).  tm_a, tm_b: operands, boxes of 64 columns x 64 rows.  Boxes
+// of 64 columns x 32 rows for the epilogue: tm_in, tm_lo what it reads (Poly: A0;
+// Apply, Final: hi and lo), tm_out what it writes beside lo.
+template <int kMode, int kBN, bool kPair>
 __global__ void __launch_bounds__(kOrthThreads, 1)
-k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, OrthArgs p) {
+k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+               const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_lo,
+               const __grid_constant__ CUtensorMap tm_out, OrthArgs p) {
     constexpr bool kSym = kMode == kOrthGram || kMode == kOrthPoly;
-    constexpr int kStages = kOrthStages<kBN>;
-    constexpr uint32_t kStageBytes = kOrthStageBytes<kBN>, kABytes = kOrthBM * kOrthBK * 2;
+    constexpr int kBM = kPair ? 256 : 128, kStages = kOrthStages<kBN, kPair>;
+    constexpr uint32_t kStageBytes = kOrthStageBytes<kBN, kPair>;
     extern __shared__ __align__(1024) unsigned char orth_smem_raw[];
     const uint32_t raw = smem_u32(orth_smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t base = (raw + 1023u) & ~1023u;   // the same offset in both CTAs of a pair
     const uint32_t bars = base + kStages * kStageBytes;
     const uint32_t full0 = bars, empty0 = bars + 8 * kStages;
     const uint32_t tfull0 = bars + 16 * kStages, tempty0 = tfull0 + 16;
     const uint32_t drain = tempty0 + 16;
-    const uint32_t slot = drain + 8;
+    const uint32_t in0 = drain + 8;   // 4 epilogue warps x 2 boxes
+    const uint32_t slot = in0 + 64;
     unsigned char* slot_gen = orth_smem_raw + (slot - raw);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(slot_gen);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(slot_gen + 4);
+    const uint32_t boxes = bars + 1024;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = kPair ? cluster_rank() : 0;
+    const bool leader = rank == 0;
+    const int64_t first = kPair ? cluster_id_x() : blockIdx.x, step = kPair ? cluster_count_x() : gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -279,48 +389,65 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull0 + 8 * a, 1);
-            mbar_init(tempty0 + 8 * a, 128);
+            mbar_init(tempty0 + 8 * a, kPair ? 8 : 4);   // one arrival per epilogue warp
         }
         mbar_init(drain, 1);
+        for (int k = 0; k < 8; ++k) mbar_init(in0 + 8 * k, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_a);
         prefetch_tmap(&tm_b);
+        if (kMode != kOrthGram) prefetch_tmap(&tm_in);
+        if (!kSym) prefetch_tmap(&tm_lo);
+        if (kMode != kOrthFinal) prefetch_tmap(&tm_out);
     }
     if (warp == 1) {
-        tmem_alloc(slot, 2 * kBN);
-        tmem_relinquish();
+        if constexpr (kPair) {
+            tmem_alloc_pair(slot, 2 * kBN);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(slot, 2 * kBN);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (kPair) cluster_sync_all();
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     orth_dep_wait();   // the operands are the previous launch's output
 
     if (warp == 0) {
-        // ---------------- TMA producer
+        // ---------------- TMA producer: this CTA's rows of A and its part of B; in
+        // a pair every copy completes on the even CTA's stage barrier
         if (lane == 0) {
+            const uint32_t full = kPair ? map_to_rank(full0, 0) : full0;
             int stage = 0;
             uint32_t phase = 0, issued = 0, last_par = 0;
             bool ok = true;
-            for (int64_t u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-                const OrthUnit w = orth_unit<kSym>(u, p);
+            auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+                if constexpr (kPair) tma_load_2d_pair(dst, map, x, y, bar);
+                else tma_load_2d(dst, map, x, y, bar);
+            };
+            for (int64_t u = first; ok && u < p.units; u += step) {
+                const OrthUnit w = orth_unit<kSym, kBM, kBN>(u, p);
                 const int row0 = (int)(w.batch * p.mp);
+                const int m0 = row0 + w.mb * kBM + (int)rank * 128;
+                const int n0 = w.nb * kBN + (kPair ? (int)rank * (kBN / 2) : 0);
                 for (int kb = 0; kb < p.nkb; ++kb) {
                     if (!orth_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = base + stage * kStageBytes, bar = full0 + 8 * stage;
-                    mbar_arrive_expect_tx(bar, kStageBytes);
-                    tma_load_2d(dst, &tm_a, kb * kOrthBK, row0 + w.mb * kOrthBM, bar);
-                    if constexpr (kSym) {
-                        tma_load_2d(dst + kABytes, &tm_b, kb * kOrthBK, row0 + w.nb * kBN, bar);
-                    } else {
+                    const uint32_t dst = base + stage * kStageBytes, bar = full + 8 * stage;
+                    if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, (kPair ? 2 : 1) * kStageBytes);
 #pragma unroll
-                        for (int j = 0; j < kBN / 64; ++j)
-                            tma_load_2d(dst + kABytes + j * 8192, &tm_b, w.nb * kBN + 64 * j, row0 + kb * kOrthBK,
-                                        bar);
+                    for (int j = 0; j < 2; ++j) load(dst + j * 8192, &tm_a, kb * kOrthBK, m0 + 64 * j, bar);
+#pragma unroll
+                    for (int j = 0; j < (int)(kOrthBBytes<kBN, kPair> / 8192); ++j) {
+                        if constexpr (kSym) load(dst + kOrthABytes + j * 8192, &tm_b, kb * kOrthBK, row0 + n0 + 64 * j, bar);
+                        else load(dst + kOrthABytes + j * 8192, &tm_b, n0 + 64 * j, row0 + kb * kOrthBK, bar);
                     }
                     issued |= 1u << stage;
                     last_par = (last_par & ~(1u << stage)) | (phase << stage);
@@ -330,21 +457,30 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                     }
                 }
             }
-            if (!ok) {
+            if (!ok && leader) {
                 for (int s = 0; s < kStages; ++s)
                     if (issued & (1u << s)) mbar_wait(full0 + 8 * s, (last_par >> s) & 1u, kOrthWaitCycles);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc = orth_idesc<kBN, !kSym>();
+        // ---------------- MMA issuer (of a pair: the even CTA's, for both)
+        if (leader && lane == 0) {
+            constexpr uint32_t idesc = orth_idesc<kBM, kBN, !kSym>();
+            const uint32_t empty_peer = kPair ? map_to_rank(empty0, 1) : 0, tfull_peer = kPair ? map_to_rank(tfull0, 1) : 0;
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int64_t u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-                if (!orth_wait(tempty0 + 8 * acc, acc_phase ^ 1u, abort_flag)) break;
+            auto commit = [&](uint32_t bar, uint32_t peer) {
+                if constexpr (kPair) {
+                    umma_commit_pair(bar);
+                    umma_commit_pair(peer);
+                } else {
+                    umma_commit(bar);
+                }
+            };
+            for (int64_t u = first; ok && u < p.units; u += step) {
+                if (!orth_wait_acc<kPair>(tempty0 + 8 * acc, acc_phase ^ 1u, abort_flag)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem + (uint32_t)(acc * kBN);
                 for (int kb = 0; kb < p.nkb; ++kb) {
@@ -355,63 +491,153 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                     tc_fence_after();
                     const uint32_t addr = base + stage * kStageBytes;
                     const uint64_t a_desc = orth_desc_k(addr);
-                    const uint64_t b_desc = kSym ? orth_desc_k(addr + kABytes) : orth_desc_mn(addr + kABytes);
+                    const uint64_t b_desc = kSym ? orth_desc_k(addr + kOrthABytes) : orth_desc_mn(addr + kOrthABytes);
                     constexpr uint64_t kBStep = kSym ? (32 >> 4) : (2048 >> 4);
 #pragma unroll
-                    for (int k = 0; k < kOrthBK / 16; ++k)
-                        umma_bf16(d_tmem, a_desc + (32 >> 4) * k, b_desc + kBStep * k, idesc,
-                                  (kb != 0 || k != 0) ? 1u : 0u);
-                    umma_commit(empty0 + 8 * stage);
+                    for (int k = 0; k < kOrthBK / 16; ++k) {
+                        const uint32_t more = (kb != 0 || k != 0) ? 1u : 0u;
+                        if constexpr (kPair) umma_bf16_pair(d_tmem, a_desc + (32 >> 4) * k, b_desc + kBStep * k, idesc, more);
+                        else umma_bf16(d_tmem, a_desc + (32 >> 4) * k, b_desc + kBStep * k, idesc, more);
+                    }
+                    commit(empty0 + 8 * stage, empty_peer + 8 * stage);
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                umma_commit(tfull0 + 8 * acc);
+                commit(tfull0 + 8 * acc, tfull_peer + 8 * acc);
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
-            umma_commit(drain);
+            if constexpr (kPair) umma_commit_pair(drain);
+            else umma_commit(drain);
             mbar_wait(drain, 0, kOrthWaitCycles);
         }
         __syncwarp();
     } else {
-        // ---------------- epilogue: one output row per thread
+        // ---------------- epilogue: 32 rows a warp, 64 columns at a time
         const int q = warp & 3;
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+        const uint32_t tempty = kPair ? map_to_rank(tempty0, 0) : tempty0;
         const int64_t cols = kSym ? p.mp : p.np;
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-            const OrthUnit w = orth_unit<kSym>(u, p);
-            if (!orth_wait(tfull0 + 8 * acc, acc_phase, abort_flag)) break;
-            tc_fence_after();
-            const int64_t i = (int64_t)w.mb * kOrthBM + q * 32 + lane;
-#pragma unroll 1
-            for (int c = 0; c < kBN / 32; ++c) {
-                const int64_t c0 = (int64_t)w.nb * kBN + c * 32;
-                if (c0 >= cols) break;   // uniform over the CTA
-                __syncwarp();
-                uint32_t r[32];
-                tmem_ld32(lane_addr + (uint32_t)(acc * kBN + c * 32), r);
-                if (i < p.mp) orth_epilogue<kMode>(p, w.batch, kSym && w.mb != w.nb, i, c0, r);
+        const uint32_t my_boxes = boxes + (uint32_t)q * 4 * kOrthBoxBytes, my_in = in0 + (uint32_t)q * 16;
+        constexpr bool kReads = kMode != kOrthGram;
+        int acc = 0, buf = 0;
+        uint32_t acc_phase = 0, in_phase = 0, pending = 0;   // bit per box pair
+        bool ok = true;
+        for (int64_t u = first; ok && u < p.units; u += step) {
+            const OrthUnit w = orth_unit<kSym, kBM, kBN>(u, p);
+            OrthRows o;
+            o.i_warp = (int64_t)w.mb * kBM + (int64_t)rank * 128 + q * 32;
+            o.i = o.i_warp + lane;
+            o.row = w.batch * p.mp + o.i;
+            const int64_t n0 = (int64_t)w.nb * kBN;
+            const int y = (int)(w.batch * p.mp + o.i_warp);
+            const bool mirror = kSym && n0 >= (int64_t)(w.mb + 1) * kBM;
+            int chunks = o.i_warp < p.mp ? (int)((cols - n0 + 63) / 64) : 0;
+            if (chunks > kBN / 64) chunks = kBN / 64;
+            auto fetch = [&](int c, int b) {   // lane 0: the boxes of chunk c
+                const uint32_t box = my_boxes + (uint32_t)b * 2 * kOrthBoxBytes, bar = my_in + 8 * b;
+                mbar_arrive_expect_tx(bar, kSym ? kOrthBoxBytes : 2 * kOrthBoxBytes);
+                tma_load_2d(box, &tm_in, (int)n0 + 64 * c, y, bar);
+                if constexpr (!kSym) tma_load_2d(box + kOrthBoxBytes, &tm_lo, (int)n0 + 64 * c, y, bar);
+            };
+            if (kReads && chunks > 0) {
+                if (lane == 0) {
+                    bulk_wait_read<0>();   // the stores out of these boxes have read them
+                    fetch(0, buf);
+                }
+                pending |= 1u << buf;
             }
+            ok = __all_sync(0xffffffffu, orth_wait(tfull0 + 8 * acc, acc_phase, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t box = my_boxes + (uint32_t)buf * 2 * kOrthBoxBytes;
+                if (kReads) {
+                    if (c + 1 < chunks) {
+                        if (lane == 0) {
+                            bulk_wait_read<0>();
+                            fetch(c + 1, buf ^ 1);
+                        }
+                        pending |= 1u << (buf ^ 1);
+                    }
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, orth_wait(my_in + 8 * buf, (in_phase >> buf) & 1u, abort_flag));
+                    if (!ok) break;
+                    in_phase ^= 1u << buf;
+                    pending &= ~(1u << buf);
+                } else if (lane == 0) {
+                    bulk_wait_read<1>();   // the store before last read this box
+                }
+                __syncwarp();
+                const int64_t c0 = n0 + 64 * c;
+                const bool diag = kSym && c0 < o.i_warp + 32 && o.i_warp < c0 + 64;
+                if (kMode == kOrthFinal && p.out_dtype == 2 && !p.transposed) {
+                    uint32_t r0[32], r1[32];   // 64 FP32 results take both boxes
+                    tmem_ld32(lane_addr + (uint32_t)(acc * kBN + 64 * c), r0);
+                    tmem_ld32(lane_addr + (uint32_t)(acc * kBN + 64 * c + 32), r1);
+                    orth_final_f32(p, o, box, lane, r0, r1);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[32];
+                        tmem_ld32(lane_addr + (uint32_t)(acc * kBN + 64 * c + 32 * h), r);
+                        orth_epilogue<kMode>(p, o, diag, mirror, w.batch, c0 + 32 * h, box, lane, r);
+                    }
+                }
+                if constexpr (kMode == kOrthFinal) {
+                    if (!p.transposed) {
+                        __syncwarp();
+                        if (p.out_dtype == 2) {
+                            orth_write_out<float>(p, o, w.batch, c0, box, lane);
+                            orth_write_out<float>(p, o, w.batch, c0 + 32, box + kOrthBoxBytes, lane);
+                        } else {
+                            orth_write_out<__nv_bfloat16>(p, o, w.batch, c0, box, lane);
+                        }
+                    }
+                    fence_proxy_async_smem();   // before the next copy into these boxes
+                    __syncwarp();
+                } else {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tm_out, (int)c0, y, box);
+                        if constexpr (!kSym) tma_store_2d(&tm_lo, (int)c0, y, box + kOrthBoxBytes);
+                        bulk_commit_group();
+                    }
+                }
+                buf ^= 1;
+            }
+            if (!ok) break;
             tc_fence_before();
-            mbar_arrive(tempty0 + 8 * acc);
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (kPair) mbar_arrive_cluster(tempty + 8 * acc);
+                else mbar_arrive(tempty + 8 * acc);
+            }
             if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;
             }
         }
+        if (!ok && lane == 0) {   // the boxes' copies in flight
+            for (int b = 0; b < 2; ++b)
+                if (pending & (1u << b)) mbar_wait(my_in + 8 * b, (in_phase >> b) & 1u, kOrthWaitCycles);
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_sync_all();   // no copy, arrival or MMA of the pair still targets either CTA
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * kBN);
+        if constexpr (kPair) tmem_dealloc_pair(tmem, 2 * kBN);
+        else tmem_dealloc(tmem, 2 * kBN);
     }
 }
 

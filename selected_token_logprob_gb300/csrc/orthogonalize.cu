@@ -69,33 +69,107 @@ flp_status orth_tmap(CUtensorMap* map, const void* ptr, int64_t rows, int64_t co
     return FLP_OK;
 }
 
-constexpr int kBN = 128;
+// A launch of one product: its kernel for this shape, once per device allowed
+// its shared memory.
+struct OrthMaps {
+    CUtensorMap a, b, in, lo, out;
+};
 
-flp_status orth_setup(int dev) {
+template <int kMode, int kBN, bool kPair>
+flp_status orth_launch(int dev, int fit, const OrthMaps& t, const flp::OrthArgs& p, cudaStream_t s) {
     static std::atomic<bool> ready[kMaxDevices];
+    const auto kern = flp::k_orth_product<kMode, kBN, kPair>;
+    constexpr size_t smem = flp::kOrthSmemBytes<kBN, kPair>;
+    static_assert(smem <= 232448, "shared memory per CTA");
     if (!ready[dev].load(std::memory_order_acquire)) {
-        const int bytes = (int)flp::kOrthSmemBytes<kBN>;
-        const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        cudaError_t e = cudaFuncSetAttribute(flp::k_orth_product<flp::kOrthGram, kBN>, attr, bytes);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(flp::k_orth_product<flp::kOrthPoly, kBN>, attr, bytes);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(flp::k_orth_product<flp::kOrthApply, kBN>, attr, bytes);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(flp::k_orth_product<flp::kOrthFinal, kBN>, attr, bytes);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize setup: %s", cudaGetErrorString(e));
         ready[dev].store(true, std::memory_order_release);
     }
+    const int64_t ctas = (p.units < fit ? p.units : fit) * (kPair ? 2 : 1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(flp::kOrthThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, t.a, t.b, t.in, t.lo, t.out, p);
+    if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize product launch: %s", cudaGetErrorString(e));
     return FLP_OK;
 }
 
+// Output tiles of one matrix.
+int64_t orth_tiles(bool sym, int64_t rows, int64_t cols, int bm, int bn) {
+    const int64_t tm = ceil_div(rows, bm), tn = ceil_div(cols, bn);
+    if (!sym) return tm * tn;
+    int64_t t = 0;
+    for (int64_t mb = 0; mb < tm; ++mb) t += tn - mb * bm / bn;
+    return t;
+}
+
+// CTA pairs that can be resident at once on `dev` (cached; 0 if the query fails).
+int orth_pairs(int dev) {
+    static std::atomic<int> count[kMaxDevices];
+    int c = count[dev].load(std::memory_order_acquire);
+    if (c == 0) {
+        const auto kern = flp::k_orth_product<flp::kOrthGram, 256, true>;
+        constexpr size_t smem = flp::kOrthSmemBytes<256, true>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(flp::kOrthThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&c, (void*)kern, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        count[dev].store(c, std::memory_order_release);
+    }
+    return c;
+}
+
 template <int kMode>
-flp_status orth_product(int sms, const CUtensorMap& tm_a, const CUtensorMap& tm_b, flp::OrthArgs p, cudaStream_t s) {
+flp_status orth_product(int dev, int sms, int pairs, int64_t batch, const OrthMaps& t, flp::OrthArgs p, cudaStream_t s) {
     constexpr bool kSym = kMode == flp::kOrthGram || kMode == flp::kOrthPoly;
-    p.tiles_m = (int)ceil_div(p.mp, flp::kOrthBM);
-    p.tiles_n = (int)ceil_div(kSym ? p.mp : p.np, kBN);
-    p.units = p.batch * (kSym ? (int64_t)p.tiles_m * (p.tiles_m + 1) / 2 : (int64_t)p.tiles_m * p.tiles_n);
+    const int64_t cols = kSym ? p.mp : p.np;
     p.nkb = (int)((kMode == flp::kOrthGram ? p.np : p.mp) / flp::kOrthBK);
-    const int grid = (int)(p.units < sms ? p.units : sms);
-    return launch_dependent("orthogonalize product", flp::k_orth_product<kMode, kBN>, grid, flp::kOrthThreads,
-                            flp::kOrthSmemBytes<kBN>, s, tm_a, tm_b, p);
+    auto shape = [&](int bm, int bn) {
+        p.tiles_m = (int)ceil_div(p.mp, bm);
+        p.tiles_n = (int)ceil_div(cols, bn);
+        p.per = orth_tiles(kSym, p.mp, cols, bm, bn);
+        p.units = batch * p.per;
+    };
+    // One CTA per 128 x 128 tile while a matrix has no second block of 128 rows
+    // (half of a pair's rows would be padding).
+    if (p.mp <= 128 || pairs <= 0) {
+        shape(128, 128);
+        return orth_launch<kMode, 128, false>(dev, sms, t, p, s);
+    }
+    // CTA pairs: 256 x 256 tiles, or 256 x 128 where their finer waves finish
+    // sooner.
+    const int64_t wide = ceil_div(batch * orth_tiles(kSym, p.mp, cols, 256, 256), pairs) * 2;
+    const int64_t narrow = ceil_div(batch * orth_tiles(kSym, p.mp, cols, 256, 128), pairs);
+    if (narrow < wide) {
+        shape(256, 128);
+        return orth_launch<kMode, 128, true>(dev, pairs, t, p, s);
+    }
+    shape(256, 256);
+    return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
 }
 
 }  // namespace
@@ -160,22 +234,26 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     if (dev < 0 || dev >= kMaxDevices) return fail(FLP_ECUDA, "device index %d out of range", dev);
     DeviceGuard guard;
     if ((st = guard.enter(dev)) != FLP_OK) return st;
-    if ((st = orth_setup(dev)) != FLP_OK) return st;
     const int sms = sm_count(dev);
     if (sms <= 0) return fail(FLP_ECUDA, "could not read the SM count of device %d", dev);
+    const int pairs = orth_pairs(dev);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     __half* hi[2] = {reinterpret_cast<__half*>(ws + l.hi0), reinterpret_cast<__half*>(ws + l.hi1)};
     __half* lo = reinterpret_cast<__half*>(ws + l.lo);
 
-    CUtensorMap tm_xk[2], tm_xn[2], tm_a0, tm_b0;
+    // operands in boxes of 64 rows, the epilogues' reads and writes in boxes of 32
+    CUtensorMap op_x[2], op_a0, op_b0, ep_x[2], ep_lo, ep_a0, ep_b0;
     const int64_t all_rows = batch * l.mp;
     for (int k = 0; k < 2; ++k) {
-        if ((st = orth_tmap(&tm_xk[k], hi[k], all_rows, l.np, 128)) != FLP_OK) return st;
-        if ((st = orth_tmap(&tm_xn[k], hi[k], all_rows, l.np, 64)) != FLP_OK) return st;
+        if ((st = orth_tmap(&op_x[k], hi[k], all_rows, l.np, 64)) != FLP_OK) return st;
+        if ((st = orth_tmap(&ep_x[k], hi[k], all_rows, l.np, 32)) != FLP_OK) return st;
     }
-    if ((st = orth_tmap(&tm_a0, ws + l.a0, all_rows, l.mp, 128)) != FLP_OK) return st;
-    if ((st = orth_tmap(&tm_b0, ws + l.b0, all_rows, l.mp, 128)) != FLP_OK) return st;
+    if ((st = orth_tmap(&ep_lo, lo, all_rows, l.np, 32)) != FLP_OK) return st;
+    if ((st = orth_tmap(&op_a0, ws + l.a0, all_rows, l.mp, 64)) != FLP_OK) return st;
+    if ((st = orth_tmap(&ep_a0, ws + l.a0, all_rows, l.mp, 32)) != FLP_OK) return st;
+    if ((st = orth_tmap(&op_b0, ws + l.b0, all_rows, l.mp, 64)) != FLP_OK) return st;
+    if ((st = orth_tmap(&ep_b0, ws + l.b0, all_rows, l.mp, 32)) != FLP_OK) return st;
 
     const flp::OrthInput in{x, rows, cols, ld_x, stride_x, batch, rows > cols ? 1 : 0, eps,
                             reinterpret_cast<double*>(ws + l.parts), hi[0], lo, l.mp, l.np};
@@ -193,14 +271,12 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     if ((st = check_launch("orthogonalize input")) != FLP_OK) return st;
 
     flp::OrthArgs p{};
-    p.batch = batch;
     p.m = l.m;
     p.n = l.n;
     p.mp = l.mp;
     p.np = l.np;
     p.d = reinterpret_cast<float*>(ws + l.d);
     p.e = reinterpret_cast<float*>(ws + l.e);
-    p.x_lo = lo;
     p.out = out;
     p.out_dtype = out_dtype;
     p.transposed = rows > cols ? 1 : 0;
@@ -214,14 +290,15 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
         p.a = coefficients[3 * k];
         p.b = coefficients[3 * k + 1];
         p.c = coefficients[3 * k + 2];
-        p.mat = reinterpret_cast<__half*>(ws + l.a0);
+        p.mat_out = reinterpret_cast<__half*>(ws + l.a0);
+        OrthMaps t{op_x[cur], op_x[cur], ep_a0, ep_a0, ep_a0};   // Gram reads nothing beside its operands
+        if ((st = orth_product<flp::kOrthGram>(dev, sms, pairs, batch, t, p, s)) != FLP_OK) return st;
         p.mat_out = reinterpret_cast<__half*>(ws + l.b0);
-        p.x_hi = hi[cur];
-        p.x_out = hi[cur ^ 1];
-        if ((st = orth_product<flp::kOrthGram>(sms, tm_xk[cur], tm_xk[cur], p, s)) != FLP_OK) return st;
-        if ((st = orth_product<flp::kOrthPoly>(sms, tm_a0, tm_a0, p, s)) != FLP_OK) return st;
-        if (k + 1 < steps) st = orth_product<flp::kOrthApply>(sms, tm_b0, tm_xn[cur], p, s);
-        else st = orth_product<flp::kOrthFinal>(sms, tm_b0, tm_xn[cur], p, s);
+        t = OrthMaps{op_a0, op_a0, ep_a0, ep_a0, ep_b0};
+        if ((st = orth_product<flp::kOrthPoly>(dev, sms, pairs, batch, t, p, s)) != FLP_OK) return st;
+        t = OrthMaps{op_b0, op_x[cur], ep_x[cur], ep_lo, ep_x[cur ^ 1]};
+        if (k + 1 < steps) st = orth_product<flp::kOrthApply>(dev, sms, pairs, batch, t, p, s);
+        else st = orth_product<flp::kOrthFinal>(dev, sms, pairs, batch, t, p, s);
         if (st != FLP_OK) return st;
     }
     return ok();

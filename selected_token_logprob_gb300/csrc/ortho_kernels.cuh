@@ -43,7 +43,7 @@ constexpr float kOrthLoScale = 2048.f;       // of lo, on top: hi's rounding is 
 constexpr long long kOrthWaitCycles = 4000000000LL;
 constexpr int kOrthThreads = 192;
 constexpr int kOrthBK = 64;
-constexpr int kOrthParts = 128;              // partial sums of squares per matrix
+constexpr int kOrthParts = 256;              // most partial sums of squares per matrix
 
 static __device__ int g_orth_error;          // 1 = a bounded wait ran out
 
@@ -145,26 +145,33 @@ __device__ __forceinline__ OrthUnit orth_unit(int64_t u, const OrthArgs& p) {
 }
 
 // Shared memory of a CTA: the stages (128 rows of A and its rows or columns of
-// B per K block), a block of barriers, and two 8 KB boxes per epilogue warp.
+// B per K block), a block of barriers, and two 4 KB boxes per epilogue warp.  A
+// TMA copy takes 2000 (idle) to 3100 (loaded) cycles to arrive, so nearly all
+// of shared memory goes to the stages: with 4 of them (and 64 KB of boxes) a
+// K block of a 256 x 256 pair tile took 776 cycles, 512 being the MMAs' own.
 constexpr uint32_t kOrthABytes = 128 * kOrthBK * 2;
 template <int kBN, bool kPair>
 constexpr uint32_t kOrthBBytes = (kPair ? kBN / 2 : kBN) * kOrthBK * 2;
 template <int kBN, bool kPair>
 constexpr uint32_t kOrthStageBytes = kOrthABytes + kOrthBBytes<kBN, kPair>;
 template <int kBN, bool kPair>
-constexpr int kOrthStages = 131072 / (int)kOrthStageBytes<kBN, kPair>;
-constexpr uint32_t kOrthBoxBytes = 32 * 64 * 2;
+constexpr int kOrthStages = 196608 / (int)kOrthStageBytes<kBN, kPair>;
+constexpr uint32_t kOrthBoxBytes = 4096;   // 32 rows x 64 columns of one matrix, or x 32 columns of hi and of lo
 template <int kBN, bool kPair>
 constexpr size_t kOrthSmemBytes =
-    1024 + (size_t)kOrthStages<kBN, kPair> * kOrthStageBytes<kBN, kPair> + 1024 + 4 * 4 * (size_t)kOrthBoxBytes;
+    1024 + (size_t)kOrthStages<kBN, kPair> * kOrthStageBytes<kBN, kPair> + 1024 + 4 * 2 * (size_t)kOrthBoxBytes;
 
 __device__ __forceinline__ uint32_t orth_pack(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 16-byte piece j of row `lane` of a box.
-__device__ __forceinline__ uint32_t orth_piece(uint32_t box, int lane, int j) {
-    return box + (uint32_t)lane * 128 + (uint32_t)((j ^ (lane & 7)) * 16);
+// 16-byte piece j of row r of a box with 128-byte rows (128-byte swizzle) or
+// 64-byte rows (64-byte swizzle), as the tensor maps lay them out.
+__device__ __forceinline__ uint32_t orth_piece(uint32_t box, int r, int j) {
+    return box + (uint32_t)r * 128 + (uint32_t)((j ^ (r & 7)) * 16);
+}
+__device__ __forceinline__ uint32_t orth_piece64(uint32_t box, int r, int j) {
+    return box + (uint32_t)r * 64 + (uint32_t)((j ^ ((r >> 1) & 3)) * 16);
 }
 
 // Where a warp's 32 rows of a tile lie.
@@ -237,10 +244,10 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
         }
     } else {
         const float ai = p.a + p.e[w.row];
-        const uint32_t lo_box = box + kOrthBoxBytes;
+        const uint32_t lo_box = box + kOrthBoxBytes / 2;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const uint4 h = lds_v4(orth_piece(box, lane, half + q)), l = lds_v4(orth_piece(lo_box, lane, half + q));
+            const uint4 h = lds_v4(orth_piece64(box, lane, q)), l = lds_v4(orth_piece64(lo_box, lane, q));
             const uint32_t hs[4] = {h.x, h.y, h.z, h.w}, ls[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -259,16 +266,16 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
                     hw[k] = orth_pack(x0, x1);
                     lw[k] = orth_pack((x0 - h_lo(hw[k])) * kOrthLoScale, (x1 - h_hi(hw[k])) * kOrthLoScale);
                 }
-                sts_v4(orth_piece(box, lane, half + q), hw[0], hw[1], hw[2], hw[3]);
-                sts_v4(orth_piece(lo_box, lane, half + q), lw[0], lw[1], lw[2], lw[3]);
+                sts_v4(orth_piece64(box, lane, q), hw[0], hw[1], hw[2], hw[3]);
+                sts_v4(orth_piece64(lo_box, lane, q), lw[0], lw[1], lw[2], lw[3]);
             }
         } else {
             const float s = p.scale * kInv;
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= s;
-            const int64_t base = batch * p.stride_out;
             if (p.transposed) {   // 32 lanes, 32 neighbours of each output row
                 if (w.i < p.m) {
+                    const int64_t base = batch * p.stride_out;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         if (c0 + j < p.n) {
@@ -278,10 +285,16 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
                         }
                     }
                 }
+            } else if (p.out_dtype == 2) {   // both boxes as 32 rows of 128 bytes
+                __syncwarp();                // every lane has read its hi and lo
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    sts_v4(orth_piece(box, lane, q), __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                           __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    sts_v4(orth_piece(box, lane, half + q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                    sts_v4(orth_piece64(box, lane, q), pack_bf16x2(v[8 * q], v[8 * q + 1]),
                            pack_bf16x2(v[8 * q + 2], v[8 * q + 3]), pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
                            pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
             }
@@ -289,73 +302,42 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
     }
 }
 
-// Final, FP32 output: 64 columns from both boxes back into both boxes (32 columns each).
-__device__ __forceinline__ void orth_final_f32(const OrthArgs& p, const OrthRows& w, uint32_t box, int lane,
-                                               uint32_t (&r0)[32], uint32_t (&r1)[32]) {
-    constexpr float kInv = 1.f / kOrthScale;
-    const float ai = p.a + p.e[w.row], s = p.scale * kInv;
-    const uint32_t lo_box = box + kOrthBoxBytes;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const uint4 h = lds_v4(orth_piece(box, lane, q)), l = lds_v4(orth_piece(lo_box, lane, q));
-        const uint32_t hs[4] = {h.x, h.y, h.z, h.w}, ls[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float xh = (k & 1) ? h_hi(hs[k >> 1]) : h_lo(hs[k >> 1]);
-            const float xl = (k & 1) ? h_hi(ls[k >> 1]) : h_lo(ls[k >> 1]);
-            uint32_t& r = q < 4 ? r0[8 * q + k] : r1[8 * (q - 4) + k];
-            r = __float_as_uint(s * (ai * (xh + xl * (1.f / kOrthLoScale)) + __uint_as_float(r) * kInv));
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        sts_v4(orth_piece(box, lane, q), r0[4 * q], r0[4 * q + 1], r0[4 * q + 2], r0[4 * q + 3]);
-        sts_v4(orth_piece(lo_box, lane, q), r1[4 * q], r1[4 * q + 1], r1[4 * q + 2], r1[4 * q + 3]);
-    }
-}
-
-// Final: one box (32 rows of 128 bytes, kEach values a row from column c0 on) to
-// the output, a row's pieces by neighbouring lanes.
+// Final: a box of 32 rows and columns to the output, a row's 16-byte pieces by
+// neighbouring lanes.
 template <class T>
 __device__ __forceinline__ void orth_write_out(const OrthArgs& p, const OrthRows& w, int64_t batch, int64_t c0,
                                                uint32_t box, int lane) {
-    constexpr int kEach = 128 / (int)sizeof(T), kPiece = 16 / (int)sizeof(T);
+    constexpr int kPiece = 16 / (int)sizeof(T), kPieces = 32 / kPiece;   // values a piece, pieces a row
     T* out = static_cast<T*>(p.out) + batch * p.stride_out;
-    if (p.vec_out && c0 + kEach <= p.n) {
+    auto piece = [&](int r, int j) { return sizeof(T) == 4 ? orth_piece(box, r, j) : orth_piece64(box, r, j); };
+    if (p.vec_out && c0 + 32 <= p.n) {
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            const int r = g * 4 + (lane >> 3), j = lane & 7;
-            if (w.i_warp + r < p.m) {
-                const uint4 x = lds_v4(orth_piece(box, r, j));
-                *reinterpret_cast<uint4*>(out + (w.i_warp + r) * p.ld_out + c0 + j * kPiece) = x;
-            }
+        for (int g = 0; g < kPieces; ++g) {
+            const int r = g * (32 / kPieces) + lane / kPieces, j = lane % kPieces;
+            if (w.i_warp + r < p.m)
+                *reinterpret_cast<uint4*>(out + (w.i_warp + r) * p.ld_out + c0 + j * kPiece) = lds_v4(piece(r, j));
         }
-    } else {
+    } else if (c0 + lane < p.n) {
         for (int r = 0; r < 32 && w.i_warp + r < p.m; ++r) {
-#pragma unroll
-            for (int k = 0; k < kEach / 32; ++k) {
-                const int e = k * 32 + lane;
-                if (c0 + e < p.n) {
-                    const uint32_t at = orth_piece(box, r, e / kPiece) + (e % kPiece) * (uint32_t)sizeof(T);
-                    T x;
-                    if constexpr (sizeof(T) == 4) {
-                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
-                    } else {
-                        unsigned short h;
-                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at) : "memory");
-                        x = *reinterpret_cast<const T*>(&h);
-                    }
-                    out[(w.i_warp + r) * p.ld_out + c0 + e] = x;
-                }
+            const uint32_t at = piece(r, lane / kPiece) + (lane % kPiece) * (uint32_t)sizeof(T);
+            T x;
+            if constexpr (sizeof(T) == 4) {
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+            } else {
+                unsigned short h;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at) : "memory");
+                x = *reinterpret_cast<const T*>(&h);
             }
+            out[(w.i_warp + r) * p.ld_out + c0 + lane] = x;
         }
     }
 }
 
 // D tiles = A B^T (Gram, Poly; both operands K-major rows) or A B (Apply, Final;
-// B read MN-major).  tm_a, tm_b: operands, boxes of 64 columns x 64 rows.  Boxes
-// of 64 columns x 32 rows for the epilogue: tm_in, tm_lo what it reads (Poly: A0;
-// Apply, Final: hi and lo), tm_out what it writes beside lo.
+// B read MN-major).  tm_a, tm_b: operands, boxes of 64 columns x 64 rows.  For
+// the epilogue boxes of 32 rows x 64 columns (Gram, Poly) or 32 columns (Apply,
+// Final): tm_in, tm_lo what it reads (Poly: A0; Apply, Final: hi and lo), tm_out
+// what it writes beside lo.
 template <int kMode, int kBN, bool kPair>
 __global__ void __launch_bounds__(kOrthThreads, 1)
 k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -523,10 +505,11 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t tempty = kPair ? map_to_rank(tempty0, 0) : tempty0;
         const int64_t cols = kSym ? p.mp : p.np;
-        const uint32_t my_boxes = boxes + (uint32_t)q * 4 * kOrthBoxBytes, my_in = in0 + (uint32_t)q * 16;
+        const uint32_t my_boxes = boxes + (uint32_t)q * 2 * kOrthBoxBytes, my_in = in0 + (uint32_t)q * 16;
         constexpr bool kReads = kMode != kOrthGram;
+        constexpr int kWide = kSym ? 64 : 32;   // columns of a chunk
         int acc = 0, buf = 0;
-        uint32_t acc_phase = 0, in_phase = 0, pending = 0;   // bit per box pair
+        uint32_t acc_phase = 0, in_phase = 0, pending = 0;   // bit per box
         bool ok = true;
         for (int64_t u = first; ok && u < p.units; u += step) {
             const OrthUnit w = orth_unit<kSym, kBM, kBN>(u, p);
@@ -537,13 +520,13 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
             const int64_t n0 = (int64_t)w.nb * kBN;
             const int y = (int)(w.batch * p.mp + o.i_warp);
             const bool mirror = kSym && n0 >= (int64_t)(w.mb + 1) * kBM;
-            int chunks = o.i_warp < p.mp ? (int)((cols - n0 + 63) / 64) : 0;
-            if (chunks > kBN / 64) chunks = kBN / 64;
-            auto fetch = [&](int c, int b) {   // lane 0: the boxes of chunk c
-                const uint32_t box = my_boxes + (uint32_t)b * 2 * kOrthBoxBytes, bar = my_in + 8 * b;
-                mbar_arrive_expect_tx(bar, kSym ? kOrthBoxBytes : 2 * kOrthBoxBytes);
-                tma_load_2d(box, &tm_in, (int)n0 + 64 * c, y, bar);
-                if constexpr (!kSym) tma_load_2d(box + kOrthBoxBytes, &tm_lo, (int)n0 + 64 * c, y, bar);
+            int chunks = o.i_warp < p.mp ? (int)((cols - n0) / kWide) : 0;   // cols and n0 are multiples of 64
+            if (chunks > kBN / kWide) chunks = kBN / kWide;
+            auto fetch = [&](int c, int b) {   // lane 0: what chunk c reads
+                const uint32_t box = my_boxes + (uint32_t)b * kOrthBoxBytes, bar = my_in + 8 * b;
+                mbar_arrive_expect_tx(bar, kOrthBoxBytes);
+                tma_load_2d(box, &tm_in, (int)n0 + kWide * c, y, bar);
+                if constexpr (!kSym) tma_load_2d(box + kOrthBoxBytes / 2, &tm_lo, (int)n0 + kWide * c, y, bar);
             };
             if (kReads && chunks > 0) {
                 if (lane == 0) {
@@ -556,7 +539,7 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
             if (!ok) break;
             tc_fence_after();
             for (int c = 0; c < chunks; ++c) {
-                const uint32_t box = my_boxes + (uint32_t)buf * 2 * kOrthBoxBytes;
+                const uint32_t box = my_boxes + (uint32_t)buf * kOrthBoxBytes;
                 if (kReads) {
                     if (c + 1 < chunks) {
                         if (lane == 0) {
@@ -574,39 +557,28 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                     bulk_wait_read<1>();   // the store before last read this box
                 }
                 __syncwarp();
-                const int64_t c0 = n0 + 64 * c;
-                const bool diag = kSym && c0 < o.i_warp + 32 && o.i_warp < c0 + 64;
-                if (kMode == kOrthFinal && p.out_dtype == 2 && !p.transposed) {
-                    uint32_t r0[32], r1[32];   // 64 FP32 results take both boxes
-                    tmem_ld32(lane_addr + (uint32_t)(acc * kBN + 64 * c), r0);
-                    tmem_ld32(lane_addr + (uint32_t)(acc * kBN + 64 * c + 32), r1);
-                    orth_final_f32(p, o, box, lane, r0, r1);
-                } else {
+                const int64_t c0 = n0 + kWide * c;
+                const bool diag = kSym && c0 < o.i_warp + 32 && o.i_warp < c0 + kWide;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[32];
-                        tmem_ld32(lane_addr + (uint32_t)(acc * kBN + 64 * c + 32 * h), r);
-                        orth_epilogue<kMode>(p, o, diag, mirror, w.batch, c0 + 32 * h, box, lane, r);
-                    }
+                for (int h = 0; h < kWide / 32; ++h) {
+                    uint32_t r[32];
+                    tmem_ld32(lane_addr + (uint32_t)(acc * kBN + kWide * c + 32 * h), r);
+                    orth_epilogue<kMode>(p, o, diag, mirror, w.batch, c0 + 32 * h, box, lane, r);
                 }
                 if constexpr (kMode == kOrthFinal) {
                     if (!p.transposed) {
                         __syncwarp();
-                        if (p.out_dtype == 2) {
-                            orth_write_out<float>(p, o, w.batch, c0, box, lane);
-                            orth_write_out<float>(p, o, w.batch, c0 + 32, box + kOrthBoxBytes, lane);
-                        } else {
-                            orth_write_out<__nv_bfloat16>(p, o, w.batch, c0, box, lane);
-                        }
+                        if (p.out_dtype == 2) orth_write_out<float>(p, o, w.batch, c0, box, lane);
+                        else orth_write_out<__nv_bfloat16>(p, o, w.batch, c0, box, lane);
                     }
-                    fence_proxy_async_smem();   // before the next copy into these boxes
+                    fence_proxy_async_smem();   // before the next copy into this box
                     __syncwarp();
                 } else {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         tma_store_2d(&tm_out, (int)c0, y, box);
-                        if constexpr (!kSym) tma_store_2d(&tm_lo, (int)c0, y, box + kOrthBoxBytes);
+                        if constexpr (!kSym) tma_store_2d(&tm_lo, (int)c0, y, box + kOrthBoxBytes / 2);
                         bulk_commit_group();
                     }
                 }
@@ -628,7 +600,7 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
             for (int b = 0; b < 2; ++b)
                 if (pending & (1u << b)) mbar_wait(my_in + 8 * b, (in_phase >> b) & 1u, kOrthWaitCycles);
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0) bulk_wait_read<0>();   // shared memory is read before the CTA exits
         __syncwarp();
     }
     tc_fence_before();
@@ -644,11 +616,15 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
 // ---------------------------------------------------------------- the input
 
 struct OrthInput {
-    const void* x;            // [rows, ld] of `dtype`, matrices `stride` elements apart
-    int64_t rows, cols, ld, stride, batch;
+    const void* x;            // [rows, ld] of T, matrices `stride` elements apart
+    int64_t rows, cols, ld, stride;
+    int64_t tiles_m, tiles;   // of X: 64 x 64 tiles down, and of one matrix
+    int64_t all_tiles;        // of the batch
     int transposed;           // X = x^T
+    int vec;                  // rows of x are whole, aligned 16-byte vectors
+    int parts;                // partial sums of a matrix, at most 256
     float eps;
-    double* parts;            // [batch, kOrthParts]
+    float* sums;              // [batch, parts]
     __half *hi, *lo;          // [batch mp, np]
     int64_t mp, np;
 };
@@ -656,74 +632,149 @@ struct OrthInput {
 __device__ __forceinline__ float orth_f32(float v) { return v; }
 __device__ __forceinline__ float orth_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float orth_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// Partial sums of squares: part q of a matrix takes its rows q, q + kOrthParts, ...
+// The 16 / sizeof(T) values of a vector.
 template <class T>
-__global__ void __launch_bounds__(256)
-k_orth_sumsq(OrthInput p) {
-    __shared__ double red[8];
-    const int64_t b = blockIdx.x / kOrthParts;
-    const int q = (int)(blockIdx.x % kOrthParts);
-    const T* x = static_cast<const T*>(p.x) + b * p.stride;
-    double s = 0.0;
-    for (int64_t r = q; r < p.rows; r += kOrthParts) {
-        float f = 0.f;
-        for (int64_t c = threadIdx.x; c < p.cols; c += 256) {
-            const float v = orth_f32(x[r * p.ld + c]);
-            f += v * v;
-        }
-        s += (double)f;
-    }
+__device__ __forceinline__ void orth_vec(const T* p, float (&v)[16 / sizeof(T)]) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const T* e = reinterpret_cast<const T*>(&q);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    for (int k = 0; k < 16 / (int)sizeof(T); ++k) v[k] = orth_f32(e[k]);
+}
+
+// Partial sums of squares: part q of a matrix takes its rows q, q + parts, ...
+constexpr int kOrthSumThreads = 512;
+template <class T>
+__global__ void __launch_bounds__(kOrthSumThreads)
+k_orth_sumsq(OrthInput p) {
+    constexpr int V = 16 / sizeof(T);
+    __shared__ float red[kOrthSumThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t b = blockIdx.x / p.parts;
+    const int q = (int)(blockIdx.x - b * p.parts);
+    const T* x = static_cast<const T*>(p.x) + b * p.stride;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};   // four chains: the adds of one would wait on each other
+    if (p.vec) {
+        // a warp takes a row's vectors 32 apart, four loads ahead
+        const int lane = threadIdx.x & 31;
+        const int64_t nv = p.cols / V;
+        for (int64_t r = q + (int64_t)(threadIdx.x >> 5) * p.parts; r < p.rows; r += (int64_t)p.parts * (kOrthSumThreads / 32)) {
+            const T* row = x + r * p.ld;
+            for (int64_t c = lane; c < nv; c += 128) {
+                float v[4][V];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (c + 32 * k < nv) orth_vec<T>(row + (c + 32 * k) * V, v[k]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (c + 32 * k < nv)
+#pragma unroll
+                        for (int j = 0; j < V; ++j) s[k] += v[k][j] * v[k][j];
+            }
+        }
+    } else {
+        const int lane = threadIdx.x & 31;
+        for (int64_t r = q + (int64_t)(threadIdx.x >> 5) * p.parts; r < p.rows; r += (int64_t)p.parts * (kOrthSumThreads / 32)) {
+            const T* row = x + r * p.ld;
+            for (int64_t c = lane; c < p.cols; c += 128) {
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = c + 32 * k < p.cols ? orth_f32(row[c + 32 * k]) : 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[k] += v[k] * v[k];
+            }
+        }
+    }
+    float t = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double t = 0.0;
-        for (int k = 0; k < 8; ++k) t += red[k];
-        p.parts[b * kOrthParts + q] = t;
+    if (threadIdx.x < 32) {
+        t = threadIdx.x < kOrthSumThreads / 32 ? red[threadIdx.x] : 0.f;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (threadIdx.x == 0) p.sums[blockIdx.x] = t;
     }
 }
 
-// X (hi, lo) = x / (|x| + eps), zero in the padding; 32 x 32 tiles, turned
-// through shared memory when X is x's transpose.
+// X (hi, lo) = x / (|x| + eps), zero in the padding: a 64 x 64 tile of X a turn,
+// through shared memory (turned there when X is x's transpose) unless x's rows
+// are aligned vectors already in X's order.
+constexpr int kOrthLoadThreads = 256;
 template <class T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kOrthLoadThreads)
 k_orth_load(OrthInput p) {
-    __shared__ float tile[32][33];
+    constexpr int V = 16 / sizeof(T);
+    __shared__ float tile[64][65];
     __shared__ float s_inv;
-    const int64_t tn = p.np / 32, tm = p.mp / 32;
-    const int64_t b = blockIdx.x / (tn * tm);
-    const int64_t t = blockIdx.x - b * tn * tm;
-    const int64_t i0 = t / tn * 32, j0 = t % tn * 32;
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    if (ty == 0) {
-        double s = 0.0;
-        for (int k = tx; k < kOrthParts; k += 32) s += p.parts[b * kOrthParts + k];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    orth_dep_wait();   // the partial sums
+    int64_t have = -1;
+    float inv = 0.f;
+    for (int64_t u = blockIdx.x; u < p.all_tiles; u += gridDim.x) {
+        const int64_t b = u / p.tiles, t = u - b * p.tiles;
+        const int64_t j0 = t / p.tiles_m * 64, i0 = t % p.tiles_m * 64;
+        if (b != have) {   // the matrix's scale
+            __syncthreads();
+            if (threadIdx.x < 32) {
+                float s = 0.f;
+                for (int k = threadIdx.x; k < p.parts; k += 32) s += __ldcg(p.sums + b * p.parts + k);
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        // an infinite sum of squares (FP32 overflow) makes X NaN, not 0
-        if (tx == 0)
-            s_inv = isfinite(s) ? (float)((double)kOrthScale / (sqrt(s) + (double)p.eps)) : __int_as_float(0x7fc00000);
-    }
-    const T* x = static_cast<const T*>(p.x) + b * p.stride;
-    // tile[a][c] = x at row (transposed ? j0 : i0) + a, column (transposed ? i0 : j0) + c
-    const int64_t r0 = p.transposed ? j0 : i0, c0 = p.transposed ? i0 : j0;
+                for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                // an infinite sum of squares (FP32 overflow) makes X NaN, not 0
+                if (threadIdx.x == 0)
+                    s_inv = isfinite(s) ? kOrthScale / (__fsqrt_rn(s) + p.eps) : __int_as_float(0x7fc00000);
+            }
+            __syncthreads();
+            inv = s_inv;
+            have = b;
+        }
+        const T* x = static_cast<const T*>(p.x) + b * p.stride;
+        const bool direct = p.vec && !p.transposed;
+        if (!direct) {
+            __syncthreads();   // the last tile's readers
+            // tile[a][c] = x at row r0 + a, column c0 + c
+            const int64_t r0 = p.transposed ? j0 : i0, c0 = p.transposed ? i0 : j0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int64_t r = r0 + ty + 8 * k, c = c0 + tx;
-        tile[ty + 8 * k][tx] = r < p.rows && c < p.cols ? orth_f32(x[r * p.ld + c]) : 0.f;
-    }
-    __syncthreads();
-    const float inv = s_inv;
+            for (int k = 0; k < 16; ++k) {
+                const int e = k * kOrthLoadThreads + threadIdx.x, a = e >> 6, c = e & 63;
+                tile[a][c] = r0 + a < p.rows && c0 + c < p.cols ? orth_f32(x[(r0 + a) * p.ld + c0 + c]) : 0.f;
+            }
+            __syncthreads();
+        }
+        // 8 neighbouring values of X a thread and turn
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int a = ty + 8 * k;
-        const float v = (p.transposed ? tile[tx][a] : tile[a][tx]) * inv;
-        const __half h = __float2half_rn(v);
-        const int64_t at = (b * p.mp + i0 + a) * p.np + j0 + tx;
-        p.hi[at] = h;
-        p.lo[at] = __float2half_rn((v - __half2float(h)) * kOrthLoScale);
+        for (int k = 0; k < 2; ++k) {
+            const int e = k * kOrthLoadThreads + threadIdx.x, i = e >> 3, j = (e & 7) * 8;
+            float v[8];
+            if (direct) {
+                const bool in = i0 + i < p.rows;
+                const T* src = x + (i0 + i) * p.ld + j0 + j;
+#pragma unroll
+                for (int h = 0; h < 8 / V; ++h) {
+                    float f[V];
+                    if (in && j0 + j + V * h < p.cols) orth_vec<T>(src + V * h, f);   // whole vectors in a row
+                    else
+#pragma unroll
+                        for (int q = 0; q < V; ++q) f[q] = 0.f;
+#pragma unroll
+                    for (int q = 0; q < V; ++q) v[V * h + q] = f[q];
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = p.transposed ? tile[j + q][i] : tile[i][j + q];
+            }
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float x0 = v[2 * q] * inv, x1 = v[2 * q + 1] * inv;
+                hw[q] = orth_pack(x0, x1);
+                lw[q] = orth_pack((x0 - h_lo(hw[q])) * kOrthLoScale, (x1 - h_hi(hw[q])) * kOrthLoScale);
+            }
+            const int64_t at = (b * p.mp + i0 + i) * p.np + j0 + j;
+            *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        }
     }
 }
 

@@ -26,7 +26,7 @@ bool orth_layout(int64_t batch, int64_t rows, int64_t cols, OrthLayout* l) {
     if (x > INT64_MAX / 16 || a > INT64_MAX / 16) return false;
     auto up = [](int64_t v) { return ceil_div(v, 1024) * 1024; };
     l->parts = 0;
-    l->d = up(batch * flp::kOrthParts * 8);
+    l->d = up(batch * flp::kOrthParts * 4);
     l->e = l->d + up(all_rows * 4);
     l->hi0 = l->e + up(all_rows * 4);
     l->hi1 = l->hi0 + up(x);
@@ -54,16 +54,19 @@ flp_status check_orth_shape(int64_t batch, int64_t rows, int64_t cols) {
 }
 
 // Tensor map of an FP16 row-major [rows, cols] matrix without padding between
-// rows: boxes of 64 columns x box_rows rows, 128-byte swizzle, zero fill.
-flp_status orth_tmap(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, uint32_t box_rows) {
+// rows: boxes of box_cols (64: 128-byte swizzle, 32: 64-byte swizzle) x box_rows,
+// zero fill.
+flp_status orth_tmap(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, uint32_t box_rows,
+                     uint32_t box_cols = 64) {
     const EncodeTiledFn fn = encode_tiled();
     if (!fn) return fail(FLP_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(FLP_EINVAL, "tensor map rejected by the driver (error %d)", (int)r);
     return FLP_OK;
@@ -154,22 +157,25 @@ flp_status orth_product(int dev, int sms, int pairs, int64_t batch, const OrthMa
         p.per = orth_tiles(kSym, p.mp, cols, bm, bn);
         p.units = batch * p.per;
     };
-    // One CTA per 128 x 128 tile while a matrix has no second block of 128 rows
-    // (half of a pair's rows would be padding).
-    if (p.mp <= 128 || pairs <= 0) {
-        shape(128, 128);
-        return orth_launch<kMode, 128, false>(dev, sms, t, p, s);
+    // Cycles of a launch by tile: a K block takes its MMAs' time or the copies'
+    // turn-around over the stages, a tile some 5000 on top, a wave each.
+    struct Tile { int bm, bn, kblock; int64_t slots; };
+    const Tile tiles[] = {{256, 256, 540, pairs}, {128, 128, 420, sms}, {128, 64, 320, sms}};
+    int64_t best = -1;
+    int pick = 1;
+    for (int k = 0; k < 3; ++k) {
+        if (tiles[k].slots <= 0) continue;
+        const int64_t units = batch * orth_tiles(kSym, p.mp, cols, tiles[k].bm, tiles[k].bn);
+        const int64_t c = ceil_div(units, tiles[k].slots) * ((int64_t)p.nkb * tiles[k].kblock) + 5000;
+        if (best < 0 || c < best) {
+            best = c;
+            pick = k;
+        }
     }
-    // CTA pairs: 256 x 256 tiles, or 256 x 128 where their finer waves finish
-    // sooner.
-    const int64_t wide = ceil_div(batch * orth_tiles(kSym, p.mp, cols, 256, 256), pairs) * 2;
-    const int64_t narrow = ceil_div(batch * orth_tiles(kSym, p.mp, cols, 256, 128), pairs);
-    if (narrow < wide) {
-        shape(256, 128);
-        return orth_launch<kMode, 128, true>(dev, pairs, t, p, s);
-    }
-    shape(256, 256);
-    return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
+    shape(tiles[pick].bm, tiles[pick].bn);
+    if (pick == 0) return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
+    if (pick == 1) return orth_launch<kMode, 128, false>(dev, sms, t, p, s);
+    return orth_launch<kMode, 64, false>(dev, sms, t, p, s);
 }
 
 }  // namespace
@@ -247,28 +253,49 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     const int64_t all_rows = batch * l.mp;
     for (int k = 0; k < 2; ++k) {
         if ((st = orth_tmap(&op_x[k], hi[k], all_rows, l.np, 64)) != FLP_OK) return st;
-        if ((st = orth_tmap(&ep_x[k], hi[k], all_rows, l.np, 32)) != FLP_OK) return st;
+        if ((st = orth_tmap(&ep_x[k], hi[k], all_rows, l.np, 32, 32)) != FLP_OK) return st;
     }
-    if ((st = orth_tmap(&ep_lo, lo, all_rows, l.np, 32)) != FLP_OK) return st;
+    if ((st = orth_tmap(&ep_lo, lo, all_rows, l.np, 32, 32)) != FLP_OK) return st;
     if ((st = orth_tmap(&op_a0, ws + l.a0, all_rows, l.mp, 64)) != FLP_OK) return st;
     if ((st = orth_tmap(&ep_a0, ws + l.a0, all_rows, l.mp, 32)) != FLP_OK) return st;
     if ((st = orth_tmap(&op_b0, ws + l.b0, all_rows, l.mp, 64)) != FLP_OK) return st;
     if ((st = orth_tmap(&ep_b0, ws + l.b0, all_rows, l.mp, 32)) != FLP_OK) return st;
 
-    const flp::OrthInput in{x, rows, cols, ld_x, stride_x, batch, rows > cols ? 1 : 0, eps,
-                            reinterpret_cast<double*>(ws + l.parts), hi[0], lo, l.mp, l.np};
-    const unsigned gs = (unsigned)(batch * flp::kOrthParts), gl = (unsigned)(batch * (l.np / 32) * (l.mp / 32));
-    if (dtype == FLP_DTYPE_BF16) {
-        flp::k_orth_sumsq<__nv_bfloat16><<<gs, 256, 0, s>>>(in);
-        flp::k_orth_load<__nv_bfloat16><<<gl, 256, 0, s>>>(in);
-    } else if (dtype == FLP_DTYPE_F16) {
-        flp::k_orth_sumsq<__half><<<gs, 256, 0, s>>>(in);
-        flp::k_orth_load<__half><<<gl, 256, 0, s>>>(in);
-    } else {
-        flp::k_orth_sumsq<float><<<gs, 256, 0, s>>>(in);
-        flp::k_orth_load<float><<<gl, 256, 0, s>>>(in);
-    }
-    if ((st = check_launch("orthogonalize input")) != FLP_OK) return st;
+    flp::OrthInput in{};
+    in.x = x;
+    in.rows = rows;
+    in.cols = cols;
+    in.ld = ld_x;
+    in.stride = stride_x;
+    in.tiles_m = l.mp / 64;
+    in.tiles = in.tiles_m * (l.np / 64);
+    in.all_tiles = batch * in.tiles;
+    in.transposed = rows > cols ? 1 : 0;
+    const int eb = elem_bytes(dtype);
+    in.vec = (cols * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) && (batch == 1 || (stride_x * eb) % 16 == 0);
+    // parts of at least 16 K elements; their number must not depend on the batch
+    int64_t parts = ceil_div(rows * cols, 16384);
+    parts = parts < rows ? parts : rows;
+    in.parts = (int)(parts < flp::kOrthParts ? parts : flp::kOrthParts);
+    in.eps = eps;
+    in.sums = reinterpret_cast<float*>(ws + l.parts);
+    in.hi = hi[0];
+    in.lo = lo;
+    in.mp = l.mp;
+    in.np = l.np;
+    const int64_t gs = batch * in.parts;
+    const int64_t gl = in.all_tiles < 8 * (int64_t)sms ? in.all_tiles : 8 * (int64_t)sms;
+    auto input = [&](auto sum, auto load) {
+        sum<<<(unsigned)gs, flp::kOrthSumThreads, 0, s>>>(in);
+        const flp_status e = check_launch("orthogonalize norm");
+        return e != FLP_OK ? e
+                           : launch_dependent("orthogonalize input", load, dim3((unsigned)gl), flp::kOrthLoadThreads,
+                                              (size_t)0, s, in);
+    };
+    st = dtype == FLP_DTYPE_BF16 ? input(flp::k_orth_sumsq<__nv_bfloat16>, flp::k_orth_load<__nv_bfloat16>)
+         : dtype == FLP_DTYPE_F16 ? input(flp::k_orth_sumsq<__half>, flp::k_orth_load<__half>)
+                                  : input(flp::k_orth_sumsq<float>, flp::k_orth_load<float>);
+    if (st != FLP_OK) return st;
 
     flp::OrthArgs p{};
     p.m = l.m;

@@ -667,8 +667,8 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
  *   coefficients  HOST pointer to steps x 3 floats; they should keep singular
  *            values in [0, 1] below 2 (FP16 overflows where an entry of X,
  *            X X^T or b A + c A^2 passes 255)
- *   out      out_dtype BF16 or FP32, ld_out, stride_out; may be x itself or
- *            overlap it (x is read before out is written)
+ *   out      out_dtype BF16 or FP32, ld_out, stride_out; may be x itself (same
+ *            layout and element size), any other overlap is FLP_EINVAL
  *   workspace  flp_orthogonalize_workspace_size(batch, rows, cols) bytes,
  *            128-byte aligned, caller-owned, no initial contents needed
  * The products run on FP16 operands with FP32 accumulators; X is carried as

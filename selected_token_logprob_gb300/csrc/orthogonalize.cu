@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "host_common.h"
+#include "ortho_cluster.cuh"
 #include "ortho_kernels.cuh"
 
 using namespace flp_host;
@@ -178,6 +179,54 @@ flp_status orth_product(int dev, int sms, int pairs, int64_t batch, const OrthMa
     return orth_launch<kMode, 64, false>(dev, sms, t, p, s);
 }
 
+// CTAs of the cluster that holds a matrix with m <= 128 in one launch (0: the
+// tiled kernels): at most 4 blocks of 64 columns a CTA, 6 with the most CTAs.
+int orth_cluster_ctas(int64_t m, int64_t blocks) {
+    if (m > 128) return 0;
+    for (int c = 1; c <= flp::kOrthCluMaxCtas; c *= 2)
+        if (ceil_div(blocks, c) <= (c == flp::kOrthCluMaxCtas ? flp::kOrthCluMaxBlocks : 4)) return c;
+    return 0;
+}
+
+// Launches the one-cluster form; *done = false where the device cannot hold the cluster.
+template <class T>
+flp_status orth_cluster_launch(int dev, int ctas, int64_t batch, const flp::OrthCluArgs& p, cudaStream_t s, bool* done) {
+    static std::atomic<int> fits[kMaxDevices][5];   // by log2 of the CTAs: 0 unknown, 1 yes, 2 no
+    const auto kern = flp::k_orth_cluster<T>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(batch * ctas));
+    cfg.blockDim = dim3(flp::kOrthCluThreads);
+    cfg.dynamicSmemBytes = flp::kOrthCluSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int log = 0;
+    while ((1 << log) < ctas) ++log;
+    int f = fits[dev][log].load(std::memory_order_acquire);
+    if (f == 0) {
+        int n = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)flp::kOrthCluSmem) !=
+                cudaSuccess ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, (void*)kern, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        f = n > 0 ? 1 : 2;
+        fits[dev][log].store(f, std::memory_order_release);
+    }
+    *done = f == 1;
+    if (f != 1) return FLP_OK;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize cluster launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
 }  // namespace
 
 cudaError_t flp_take_orthogonalize_error(int* code) {
@@ -219,13 +268,20 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
         return fail(FLP_EINVAL, "ld_x (%lld) and ld_out (%lld) must be >= cols (%lld)", (long long)ld_x,
                     (long long)ld_out, (long long)cols);
     if (batch == 0 || rows == 0 || cols == 0) return ok();
-    int64_t bx, bo, span;
+    int64_t bx, bo, span_x, span_o;
     if (!span_bytes(rows, cols, ld_x, 1, &bx) || !span_bytes(rows, cols, ld_out, 1, &bo) ||
-        !span_bytes(batch, bx, stride_x, elem_bytes(dtype), &span) ||
-        !span_bytes(batch, bo, stride_out, elem_bytes(out_dtype), &span))
+        !span_bytes(batch, bx, stride_x, elem_bytes(dtype), &span_x) ||
+        !span_bytes(batch, bo, stride_out, elem_bytes(out_dtype), &span_o))
         return fail(FLP_EINVAL, "x or out extent overflows int64");
     if (batch > 1 && (stride_x < 0 || stride_out < bo))
         return fail(FLP_EINVAL, "stride_x must be >= 0 and stride_out cover a matrix");
+    // a matrix's x is read before its out is written, but matrices do not wait for
+    // one another: out is x in place, or apart from it
+    const uintptr_t xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
+    const bool in_place = x == out && ld_x == ld_out && (batch == 1 || stride_x == stride_out) &&
+                          elem_bytes(dtype) == elem_bytes(out_dtype);
+    if (!in_place && x != nullptr && out != nullptr && xa < oa + (uintptr_t)span_o && oa < xa + (uintptr_t)span_x)
+        return fail(FLP_EINVAL, "out overlaps x");
     OrthLayout l;
     if (!orth_layout(batch, rows, cols, &l)) return fail(FLP_EINVAL, "workspace size overflows int64");
     if (workspace_bytes < l.total)
@@ -242,8 +298,39 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     if ((st = guard.enter(dev)) != FLP_OK) return st;
     const int sms = sm_count(dev);
     if (sms <= 0) return fail(FLP_ECUDA, "could not read the SM count of device %d", dev);
-    const int pairs = orth_pairs(dev);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int eb = elem_bytes(dtype), ob = elem_bytes(out_dtype);
+    const bool vec_in = (cols * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) &&
+                        (batch == 1 || (stride_x * eb) % 16 == 0);
+    const bool vec_out = aligned16(out) && (ld_out * ob) % 16 == 0 && (batch == 1 || (stride_out * ob) % 16 == 0);
+    const int ctas = orth_cluster_ctas(l.m, l.np / 64);
+    if (ctas > 0 && batch * ctas < kMaxGrid) {
+        flp::OrthCluArgs c{};
+        c.x = x;
+        c.ld = ld_x;
+        c.stride = stride_x;
+        c.m = l.m;
+        c.n = l.n;
+        c.mp = (int)l.mp;
+        c.blocks = (int)(l.np / 64);
+        c.transposed = rows > cols ? 1 : 0;
+        c.vec = vec_in;
+        c.steps = steps;
+        c.eps = eps;
+        c.scale = scale;
+        c.out = out;
+        c.out_dtype = out_dtype;
+        c.vec_out = vec_out;
+        c.ld_out = ld_out;
+        c.stride_out = stride_out;
+        for (int k = 0; k < 3 * steps; ++k) c.coef[k] = coefficients[k];
+        bool done = false;
+        st = dtype == FLP_DTYPE_BF16 ? orth_cluster_launch<__nv_bfloat16>(dev, ctas, batch, c, s, &done)
+             : dtype == FLP_DTYPE_F16 ? orth_cluster_launch<__half>(dev, ctas, batch, c, s, &done)
+                                      : orth_cluster_launch<float>(dev, ctas, batch, c, s, &done);
+        if (st != FLP_OK || done) return st;
+    }
+    const int pairs = orth_pairs(dev);
     char* ws = static_cast<char*>(workspace);
     __half* hi[2] = {reinterpret_cast<__half*>(ws + l.hi0), reinterpret_cast<__half*>(ws + l.hi1)};
     __half* lo = reinterpret_cast<__half*>(ws + l.lo);
@@ -271,8 +358,7 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     in.tiles = in.tiles_m * (l.np / 64);
     in.all_tiles = batch * in.tiles;
     in.transposed = rows > cols ? 1 : 0;
-    const int eb = elem_bytes(dtype);
-    in.vec = (cols * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) && (batch == 1 || (stride_x * eb) % 16 == 0);
+    in.vec = vec_in;
     // parts of at least 16 K elements; their number must not depend on the batch
     int64_t parts = ceil_div(rows * cols, 16384);
     parts = parts < rows ? parts : rows;
@@ -307,8 +393,7 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     p.out = out;
     p.out_dtype = out_dtype;
     p.transposed = rows > cols ? 1 : 0;
-    const int ob = elem_bytes(out_dtype);
-    p.vec_out = aligned16(out) && (ld_out * ob) % 16 == 0 && (batch == 1 || (stride_out * ob) % 16 == 0);
+    p.vec_out = vec_out;
     p.ld_out = ld_out;
     p.stride_out = stride_out;
     p.scale = scale;

@@ -87,7 +87,9 @@ def _gradient(shape, seed, rank=None, floor=0.3, dtype=torch.float32):
 
 SHAPES = [(1, 1), (1, 17), (2, 3), (5, 5), (16, 4096), (31, 33), (33, 31), (63, 64), (64, 64), (65, 64), (64, 1024),
           (100, 1000), (127, 129), (128, 128), (129, 128), (130, 500), (192, 192), (200, 250), (256, 256),
-          (257, 1023), (384, 640), (500, 70), (1001, 2050), (1024, 4096), (2050, 1001), (4097, 70), (2048, 2048)]
+          (257, 1023), (384, 640), (500, 70), (1001, 2050), (1024, 4096), (2050, 1001), (4097, 70), (2048, 2048),
+          (8, 257), (70, 513), (128, 1025), (24, 2049), (2100, 127), (96, 4161), (128, 6144), (6100, 100), (20, 6145),
+          (7000, 128)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -99,7 +101,7 @@ def test_sizes(shape, out_dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("shape", [(3, 64, 96), (2, 130, 65), (5, 40, 200), (4, 256, 256), (2, 320, 1000),
-                                   (3, 600, 300)])
+                                   (3, 600, 300), (40, 100, 600), (20, 33, 4099), (12, 1500, 64)])
 def test_stacks_and_types(dtype, shape):
     x = _gradient(shape, 3, dtype=dtype)
     got = flp.orthogonalize(x, out_dtype=torch.float32)
@@ -228,5 +230,8 @@ def test_refusals():
                dict(workspace=torch.empty(64, dtype=torch.uint8, device=DEV))):
         with pytest.raises(flp.FusedLogpError):
             flp.orthogonalize(x, **kw)
+    with pytest.raises(flp.FusedLogpError):   # shifted onto its own input
+        buf = torch.ones(200, device=DEV)
+        flp.orthogonalize(buf[:128].view(8, 16), out=buf[16:144].view(8, 16))
     with pytest.raises(flp.FusedLogpError):
         flp.orthogonalize_workspace_size(1, 70000, 70000)

@@ -334,7 +334,8 @@ __device__ __forceinline__ void orth_write_out(const OrthArgs& p, const OrthRows
 }
 
 // D tiles = A B^T (Gram, Poly; both operands K-major rows) or A B (Apply, Final;
-// B read MN-major).  tm_a, tm_b: operands, boxes of 64 columns x 64 rows.  For
+// B read MN-major).  tm_a, tm_b: operands, boxes of 64 columns x the CTA's rows of
+// a K block (MN-major: x 64 rows).  For
 // the epilogue boxes of 32 rows x 64 columns (Gram, Poly) or 32 columns (Apply,
 // Final): tm_in, tm_lo what it reads (Poly: A0; Apply, Final: hi and lo), tm_out
 // what it writes beside lo.
@@ -424,12 +425,13 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                     }
                     const uint32_t dst = base + stage * kStageBytes, bar = full + 8 * stage;
                     if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, (kPair ? 2 : 1) * kStageBytes);
+                    load(dst, &tm_a, kb * kOrthBK, m0, bar);
+                    if constexpr (kSym) {
+                        load(dst + kOrthABytes, &tm_b, kb * kOrthBK, row0 + n0, bar);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) load(dst + j * 8192, &tm_a, kb * kOrthBK, m0 + 64 * j, bar);
-#pragma unroll
-                    for (int j = 0; j < (int)(kOrthBBytes<kBN, kPair> / 8192); ++j) {
-                        if constexpr (kSym) load(dst + kOrthABytes + j * 8192, &tm_b, kb * kOrthBK, row0 + n0 + 64 * j, bar);
-                        else load(dst + kOrthABytes + j * 8192, &tm_b, n0 + 64 * j, row0 + kb * kOrthBK, bar);
+                        for (int j = 0; j < (int)(kOrthBBytes<kBN, kPair> / 8192); ++j)
+                            load(dst + kOrthABytes + j * 8192, &tm_b, n0 + 64 * j, row0 + kb * kOrthBK, bar);
                     }
                     issued |= 1u << stage;
                     last_par = (last_par & ~(1u << stage)) | (phase << stage);

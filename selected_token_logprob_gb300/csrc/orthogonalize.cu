@@ -76,7 +76,7 @@ flp_status orth_tmap(CUtensorMap* map, const void* ptr, int64_t rows, int64_t co
 // A launch of one product: its kernel for this shape, once per device allowed
 // its shared memory.
 struct OrthMaps {
-    CUtensorMap a, b, in, lo, out;
+    CUtensorMap a, b, b64, in, lo, out;   // operands (b64: b in boxes of 64 rows), the epilogue's
 };
 
 template <int kMode, int kBN, bool kPair>
@@ -105,7 +105,8 @@ flp_status orth_launch(int dev, int fit, const OrthMaps& t, const flp::OrthArgs&
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kPair ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, t.a, t.b, t.in, t.lo, t.out, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, t.a, kBN == 64 || kMode >= flp::kOrthApply ? t.b64 : t.b, t.in,
+                                             t.lo, t.out, p);
     if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize product launch: %s", cudaGetErrorString(e));
     return FLP_OK;
 }
@@ -335,17 +336,19 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     __half* hi[2] = {reinterpret_cast<__half*>(ws + l.hi0), reinterpret_cast<__half*>(ws + l.hi1)};
     __half* lo = reinterpret_cast<__half*>(ws + l.lo);
 
-    // operands in boxes of 64 rows, the epilogues' reads and writes in boxes of 32
-    CUtensorMap op_x[2], op_a0, op_b0, ep_x[2], ep_lo, ep_a0, ep_b0;
+    // operands in boxes of 128 (and 64) rows, the epilogues' reads and writes of 32
+    CUtensorMap op_x[2], op_x64[2], op_a0, op_a064, op_b0, ep_x[2], ep_lo, ep_a0, ep_b0;
     const int64_t all_rows = batch * l.mp;
     for (int k = 0; k < 2; ++k) {
-        if ((st = orth_tmap(&op_x[k], hi[k], all_rows, l.np, 64)) != FLP_OK) return st;
+        if ((st = orth_tmap(&op_x[k], hi[k], all_rows, l.np, 128)) != FLP_OK) return st;
+        if ((st = orth_tmap(&op_x64[k], hi[k], all_rows, l.np, 64)) != FLP_OK) return st;
         if ((st = orth_tmap(&ep_x[k], hi[k], all_rows, l.np, 32, 32)) != FLP_OK) return st;
     }
     if ((st = orth_tmap(&ep_lo, lo, all_rows, l.np, 32, 32)) != FLP_OK) return st;
-    if ((st = orth_tmap(&op_a0, ws + l.a0, all_rows, l.mp, 64)) != FLP_OK) return st;
+    if ((st = orth_tmap(&op_a0, ws + l.a0, all_rows, l.mp, 128)) != FLP_OK) return st;
+    if ((st = orth_tmap(&op_a064, ws + l.a0, all_rows, l.mp, 64)) != FLP_OK) return st;
     if ((st = orth_tmap(&ep_a0, ws + l.a0, all_rows, l.mp, 32)) != FLP_OK) return st;
-    if ((st = orth_tmap(&op_b0, ws + l.b0, all_rows, l.mp, 64)) != FLP_OK) return st;
+    if ((st = orth_tmap(&op_b0, ws + l.b0, all_rows, l.mp, 128)) != FLP_OK) return st;
     if ((st = orth_tmap(&ep_b0, ws + l.b0, all_rows, l.mp, 32)) != FLP_OK) return st;
 
     flp::OrthInput in{};
@@ -403,12 +406,12 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
         p.b = coefficients[3 * k + 1];
         p.c = coefficients[3 * k + 2];
         p.mat_out = reinterpret_cast<__half*>(ws + l.a0);
-        OrthMaps t{op_x[cur], op_x[cur], ep_a0, ep_a0, ep_a0};   // Gram reads nothing beside its operands
+        OrthMaps t{op_x[cur], op_x[cur], op_x64[cur], ep_a0, ep_a0, ep_a0};   // Gram reads nothing beside its operands
         if ((st = orth_product<flp::kOrthGram>(dev, sms, pairs, batch, t, p, s)) != FLP_OK) return st;
         p.mat_out = reinterpret_cast<__half*>(ws + l.b0);
-        t = OrthMaps{op_a0, op_a0, ep_a0, ep_a0, ep_b0};
+        t = OrthMaps{op_a0, op_a0, op_a064, ep_a0, ep_a0, ep_b0};
         if ((st = orth_product<flp::kOrthPoly>(dev, sms, pairs, batch, t, p, s)) != FLP_OK) return st;
-        t = OrthMaps{op_b0, op_x[cur], ep_x[cur], ep_lo, ep_x[cur ^ 1]};
+        t = OrthMaps{op_b0, op_x[cur], op_x64[cur], ep_x[cur], ep_lo, ep_x[cur ^ 1]};
         if (k + 1 < steps) st = orth_product<flp::kOrthApply>(dev, sms, pairs, batch, t, p, s);
         else st = orth_product<flp::kOrthFinal>(dev, sms, pairs, batch, t, p, s);
         if (st != FLP_OK) return st;

@@ -676,8 +676,9 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
  * that out is within about 1e-3 (of its norm) of the result in 64 bits also
  * where G has few large singular values over a small floor.  The sum of squares
  * is FP32 within a row (entries between about 1e-19 and 1e17 in size).  A zero
- * matrix gives zeros; an infinity or NaN makes its matrix NaN.  Deterministic;
- * a matrix's bits do not depend on the rest of the batch.
+ * matrix gives zeros; an infinity or NaN makes its matrix NaN.  Deterministic:
+ * equal calls give equal bits (the order of the sums over K depends on the
+ * sizes and the batch).
  * Errors: FLP_EINVAL for a bad dtype, extent, stride, steps, coefficient, eps,
  * scale or workspace; FLP_EUNSUPPORTED for a smaller side above 65536 or sizes
  * beyond the 32-bit coordinates of the tensor maps.

@@ -59,12 +59,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
-__device__ __forceinline__ float4 dsm_ld(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
-}
 __device__ __forceinline__ void dsm_st2(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
@@ -91,11 +85,6 @@ __host__ __device__ constexpr uint32_t orth_idesc_n(int n, bool b_mn) {
 __device__ __forceinline__ uint32_t orth_block_piece(uint32_t block, int r, int j) {
     return block + (uint32_t)r * 128 + (uint32_t)((j ^ (r & 7)) * 16);
 }
-// Of 16-byte piece j (4 floats) of row r of the FP32 partials.
-__device__ __forceinline__ uint32_t orth_part_piece(uint32_t p, int r, int j) {
-    return p + (uint32_t)r * 512 + (uint32_t)((j ^ (r & 7)) * 16);
-}
-
 template <class T>
 __global__ void __launch_bounds__(kOrthCluThreads, 1)
 k_orth_cluster(const __grid_constant__ OrthCluArgs p) {

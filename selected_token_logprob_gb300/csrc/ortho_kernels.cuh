@@ -57,7 +57,10 @@ struct OrthArgs {
     int64_t units;            // over the batch
     int nkb;                  // K blocks of 64
     float a, b, c;            // this step's coefficients
-    __half* mat_out;          // Gram: A0, Poly: B0 (for the mirrored tiles)
+    __half* mat_out;          // Gram: A0, Poly: B0
+    const __half* mat_in;     // A0
+    const __half* x_hi;       // X; its next hi, and lo (in place)
+    __half *x_out, *x_lo;
     float *d, *e;             // [batch mp] diagonals
     void* out;                // Final
     int out_dtype, transposed, vec_out;
@@ -154,12 +157,12 @@ template <int kBN, bool kPair>
 constexpr uint32_t kOrthBBytes = (kPair ? kBN / 2 : kBN) * kOrthBK * 2;
 template <int kBN, bool kPair>
 constexpr uint32_t kOrthStageBytes = kOrthABytes + kOrthBBytes<kBN, kPair>;
-template <int kBN, bool kPair>
-constexpr int kOrthStages = 196608 / (int)kOrthStageBytes<kBN, kPair>;
 constexpr uint32_t kOrthBoxBytes = 4096;   // 32 rows x 64 columns of one matrix, or x 32 columns of hi and of lo
-template <int kBN, bool kPair>
-constexpr size_t kOrthSmemBytes =
-    1024 + (size_t)kOrthStages<kBN, kPair> * kOrthStageBytes<kBN, kPair> + 1024 + 4 * 2 * (size_t)kOrthBoxBytes;
+template <int kBN, bool kPair, int kBoxes>
+constexpr int kOrthStages = (229376 - 4 * kBoxes * (int)kOrthBoxBytes) / (int)kOrthStageBytes<kBN, kPair>;
+template <int kBN, bool kPair, int kBoxes>
+constexpr size_t kOrthSmemBytes = 1024 + (size_t)kOrthStages<kBN, kPair, kBoxes> * kOrthStageBytes<kBN, kPair> + 1024 +
+                                  4 * kBoxes * (size_t)kOrthBoxBytes;
 
 __device__ __forceinline__ uint32_t orth_pack(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -339,13 +342,15 @@ __device__ __forceinline__ void orth_write_out(const OrthArgs& p, const OrthRows
 // the epilogue boxes of 32 rows x 64 columns (Gram, Poly) or 32 columns (Apply,
 // Final): tm_in, tm_lo what it reads (Poly: A0; Apply, Final: hi and lo), tm_out
 // what it writes beside lo.
-template <int kMode, int kBN, bool kPair>
+// kBoxes: 2, or 4 (and a stage less) where the K loop is short: the epilogue then
+// reads two chunks ahead.
+template <int kMode, int kBN, bool kPair, int kBoxes>
 __global__ void __launch_bounds__(kOrthThreads, 1)
 k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_lo,
                const __grid_constant__ CUtensorMap tm_out, OrthArgs p) {
     constexpr bool kSym = kMode == kOrthGram || kMode == kOrthPoly;
-    constexpr int kBM = kPair ? 256 : 128, kStages = kOrthStages<kBN, kPair>;
+    constexpr int kBM = kPair ? 256 : 128, kStages = kOrthStages<kBN, kPair, kBoxes>;
     constexpr uint32_t kStageBytes = kOrthStageBytes<kBN, kPair>;
     extern __shared__ __align__(1024) unsigned char orth_smem_raw[];
     const uint32_t raw = smem_u32(orth_smem_raw);
@@ -354,8 +359,8 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
     const uint32_t full0 = bars, empty0 = bars + 8 * kStages;
     const uint32_t tfull0 = bars + 16 * kStages, tempty0 = tfull0 + 16;
     const uint32_t drain = tempty0 + 16;
-    const uint32_t in0 = drain + 8;   // 4 epilogue warps x 2 boxes
-    const uint32_t slot = in0 + 64;
+    const uint32_t in0 = drain + 8;   // 4 epilogue warps x kBoxes
+    const uint32_t slot = in0 + 32 * kBoxes;
     unsigned char* slot_gen = orth_smem_raw + (slot - raw);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(slot_gen);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(slot_gen + 4);
@@ -375,7 +380,7 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
             mbar_init(tempty0 + 8 * a, kPair ? 8 : 4);   // one arrival per epilogue warp
         }
         mbar_init(drain, 1);
-        for (int k = 0; k < 8; ++k) mbar_init(in0 + 8 * k, 1);
+        for (int k = 0; k < 4 * kBoxes; ++k) mbar_init(in0 + 8 * k, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_a);
@@ -507,9 +512,10 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t tempty = kPair ? map_to_rank(tempty0, 0) : tempty0;
         const int64_t cols = kSym ? p.mp : p.np;
-        const uint32_t my_boxes = boxes + (uint32_t)q * 2 * kOrthBoxBytes, my_in = in0 + (uint32_t)q * 16;
+        const uint32_t my_boxes = boxes + (uint32_t)q * kBoxes * kOrthBoxBytes, my_in = in0 + (uint32_t)q * 8 * kBoxes;
         constexpr bool kReads = kMode != kOrthGram;
         constexpr int kWide = kSym ? 64 : 32;   // columns of a chunk
+        constexpr int kAhead = kBoxes / 2;      // chunks read ahead
         int acc = 0, buf = 0;
         uint32_t acc_phase = 0, in_phase = 0, pending = 0;   // bit per box
         bool ok = true;
@@ -530,12 +536,16 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 tma_load_2d(box, &tm_in, (int)n0 + kWide * c, y, bar);
                 if constexpr (!kSym) tma_load_2d(box + kOrthBoxBytes / 2, &tm_lo, (int)n0 + kWide * c, y, bar);
             };
-            if (kReads && chunks > 0) {
-                if (lane == 0) {
-                    bulk_wait_read<0>();   // the stores out of these boxes have read them
-                    fetch(0, buf);
+            if (kReads) {
+                if (lane == 0 && chunks > 0) bulk_wait_read<0>();   // the stores out of the boxes have read them
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int b = (buf + k) % kBoxes;
+                    if (k < chunks) {
+                        if (lane == 0) fetch(k, b);
+                        pending |= 1u << b;
+                    }
                 }
-                pending |= 1u << buf;
             }
             ok = __all_sync(0xffffffffu, orth_wait(tfull0 + 8 * acc, acc_phase, abort_flag));
             if (!ok) break;
@@ -543,12 +553,13 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t box = my_boxes + (uint32_t)buf * kOrthBoxBytes;
                 if (kReads) {
-                    if (c + 1 < chunks) {
+                    if (c + kAhead < chunks) {
+                        const int b = (buf + kAhead) % kBoxes;
                         if (lane == 0) {
-                            bulk_wait_read<0>();
-                            fetch(c + 1, buf ^ 1);
+                            bulk_wait_read<kAhead - 1>();   // the store that last used this box
+                            fetch(c + kAhead, b);
                         }
-                        pending |= 1u << (buf ^ 1);
+                        pending |= 1u << b;
                     }
                     __syncwarp();
                     ok = __all_sync(0xffffffffu, orth_wait(my_in + 8 * buf, (in_phase >> buf) & 1u, abort_flag));
@@ -556,7 +567,7 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                     in_phase ^= 1u << buf;
                     pending &= ~(1u << buf);
                 } else if (lane == 0) {
-                    bulk_wait_read<1>();   // the store before last read this box
+                    bulk_wait_read<kBoxes - 1>();   // the store that last used this box
                 }
                 __syncwarp();
                 const int64_t c0 = n0 + kWide * c;
@@ -584,7 +595,7 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                         bulk_commit_group();
                     }
                 }
-                buf ^= 1;
+                buf = (buf + 1) % kBoxes;
             }
             if (!ok) break;
             tc_fence_before();
@@ -599,7 +610,7 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
             }
         }
         if (!ok && lane == 0) {   // the boxes' copies in flight
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < kBoxes; ++b)
                 if (pending & (1u << b)) mbar_wait(my_in + 8 * b, (in_phase >> b) & 1u, kOrthWaitCycles);
         }
         if (lane == 0) bulk_wait_read<0>();   // shared memory is read before the CTA exits
@@ -613,6 +624,353 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         if constexpr (kPair) tmem_dealloc_pair(tmem, 2 * kBN);
         else tmem_dealloc(tmem, 2 * kBN);
     }
+}
+
+// ---------------------------------------------------------------- few tiles
+
+// A product with fewer tiles than SMs is bound by the latencies of one tile: the
+// copy engine's rate (a 128 x 128 tile's K block of 32 KB takes about 500 cycles),
+// the first copy's 2000 and the epilogue.  Here a cluster of 1, 2 or 4 CTAs shares
+// a 128 x 128 tile, each taking a part of K.  A CTA puts its FP32 partial into
+// shared memory by column shares and pushes the others' into their CTAs with bulk
+// copies (reading them from there took 4000 cycles); each adds its share in CTA
+// order and finishes those columns straight from and to global memory, with what it
+// reads there loaded before the K loop.
+constexpr int kOrthSplitStages = 4;
+constexpr uint32_t kOrthSplitRecv = kOrthSplitStages * 32768;   // 64 KB of partials from the others
+constexpr size_t kOrthSplitSmem = 1024 + kOrthSplitRecv + 65536 + 256;
+static_assert(kOrthSplitSmem <= 232448, "shared memory per CTA");
+
+// Of 16-byte piece j (4 floats) of row r of 128 x 128 FP32 partials.
+__device__ __forceinline__ uint32_t orth_part_piece(uint32_t p, int r, int j) {
+    return p + (uint32_t)r * 512 + (uint32_t)((j ^ (r & 7)) * 16);
+}
+__device__ __forceinline__ float4 dsm_ld(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+// Shared memory of this CTA to another's, completing on a barrier there.
+__device__ __forceinline__ void dsm_push(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// What the columns c0 .. c0 + 31 of a row need beside the accumulators.
+struct OrthInputs {
+    uint4 a[4], b[4];   // Poly: A0 and d (two halves); Apply, Final: hi, lo
+    uint4 d[4];
+};
+template <int kMode>
+__device__ __forceinline__ void orth_inputs(const OrthArgs& p, int64_t batch, int64_t row, int64_t c0, OrthInputs& in) {
+    if constexpr (kMode == kOrthPoly) {
+        const uint4* a = reinterpret_cast<const uint4*>(p.mat_in + row * p.mp + c0);
+        const uint4* d = reinterpret_cast<const uint4*>(p.d + batch * p.mp + c0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            in.a[q] = a[q];
+            in.b[q] = d[q];
+            in.d[q] = d[4 + q];
+        }
+    } else if constexpr (kMode != kOrthGram) {
+        const uint4* h = reinterpret_cast<const uint4*>(p.x_hi + row * p.np + c0);
+        const uint4* l = reinterpret_cast<const uint4*>(p.x_lo + row * p.np + c0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            in.a[q] = h[q];
+            in.b[q] = l[q];
+        }
+    }
+}
+__device__ __forceinline__ float orth_word_f(const uint4& v, int k) {
+    return __uint_as_float(k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w);
+}
+__device__ __forceinline__ float orth_half_f(const uint4& v, int k) {
+    const uint32_t w = (k >> 1) == 0 ? v.x : (k >> 1) == 1 ? v.y : (k >> 1) == 2 ? v.z : v.w;
+    return (k & 1) ? h_hi(w) : h_lo(w);
+}
+
+// Columns c0 .. c0 + 31 of row `row` (i of its matrix): the accumulators v to the result.
+template <int kMode>
+__device__ __forceinline__ void orth_finish(const OrthArgs& p, int64_t batch, int64_t row, int64_t i, int64_t c0,
+                                            bool mirror, float side, const OrthInputs& in, float (&v)[32]) {
+    constexpr float kInv = 1.f / kOrthScale;
+    if constexpr (kMode == kOrthGram || kMode == kOrthPoly) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float s = v[j] * kInv;
+            if constexpr (kMode == kOrthGram) {
+                v[j] = s;
+                if (c0 + j == i) {
+                    p.d[row] = s * kInv;
+                    v[j] = 0.f;
+                }
+            } else {   // side = d_i
+                const float dj = orth_word_f(j < 16 ? in.b[j >> 2] : in.d[(j >> 2) - 4], j & 3);
+                v[j] = (p.b + p.c * (side + dj)) * orth_half_f(in.a[j >> 3], j & 7) + p.c * s;
+                if (c0 + j == i) {
+                    p.e[row] = p.b * side + p.c * (side * side) + p.c * (s * kInv);
+                    v[j] = 0.f;
+                }
+            }
+        }
+        uint4* o = reinterpret_cast<uint4*>(p.mat_out + row * p.mp + c0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            o[q] = make_uint4(orth_pack(v[8 * q], v[8 * q + 1]), orth_pack(v[8 * q + 2], v[8 * q + 3]),
+                              orth_pack(v[8 * q + 4], v[8 * q + 5]), orth_pack(v[8 * q + 6], v[8 * q + 7]));
+        if (mirror) {
+            __half* t = p.mat_out + (batch * p.mp + c0) * p.mp + i;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) t[j * p.mp] = __float2half_rn(v[j]);
+        }
+    } else {   // side = a + e_i
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = side * (orth_half_f(in.a[j >> 3], j & 7) + orth_half_f(in.b[j >> 3], j & 7) * (1.f / kOrthLoScale)) +
+                   v[j] * kInv;
+        if constexpr (kMode == kOrthApply) {
+            uint4* oh = reinterpret_cast<uint4*>(p.x_out + row * p.np + c0);
+            uint4* ol = reinterpret_cast<uint4*>(p.x_lo + row * p.np + c0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t hw[4], lw[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x0 = v[8 * q + 2 * k], x1 = v[8 * q + 2 * k + 1];
+                    hw[k] = orth_pack(x0, x1);
+                    lw[k] = orth_pack((x0 - h_lo(hw[k])) * kOrthLoScale, (x1 - h_hi(hw[k])) * kOrthLoScale);
+                }
+                oh[q] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+                ol[q] = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+            }
+        } else if (i < p.m) {
+            const float s = p.scale * kInv;
+            const int64_t base = batch * p.stride_out;
+            if (p.vec_out && !p.transposed && c0 + 32 <= p.n) {
+                if (p.out_dtype == 2) {
+                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + base + i * p.ld_out + c0);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        o[q] = make_float4(s * v[4 * q], s * v[4 * q + 1], s * v[4 * q + 2], s * v[4 * q + 3]);
+                } else {
+                    uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + base + i * p.ld_out + c0);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        o[q] = make_uint4(pack_bf16x2(s * v[8 * q], s * v[8 * q + 1]),
+                                          pack_bf16x2(s * v[8 * q + 2], s * v[8 * q + 3]),
+                                          pack_bf16x2(s * v[8 * q + 4], s * v[8 * q + 5]),
+                                          pack_bf16x2(s * v[8 * q + 6], s * v[8 * q + 7]));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    if (c0 + j < p.n) {
+                        const int64_t at = base + (p.transposed ? (c0 + j) * p.ld_out + i : i * p.ld_out + c0 + j);
+                        if (p.out_dtype == 2) static_cast<float*>(p.out)[at] = s * v[j];
+                        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(s * v[j]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kOrthThreads, 1)
+k_orth_split(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, OrthArgs p) {
+    constexpr bool kSym = kMode == kOrthGram || kMode == kOrthPoly;
+    constexpr int kStages = kOrthSplitStages;
+    constexpr uint32_t kStageBytes = 32768;
+    extern __shared__ __align__(1024) unsigned char orth_smem_raw[];
+    const uint32_t raw = smem_u32(orth_smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;   // the same offset in every CTA of the cluster
+    const uint32_t recv = base + kOrthSplitRecv, bars = recv + 65536;
+    const uint32_t full0 = bars, empty0 = bars + 8 * kStages, tfull = bars + 16 * kStages, got = tfull + 8, slot = got + 8;
+    unsigned char* slot_gen = orth_smem_raw + (slot - raw);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(slot_gen);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(slot_gen + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t split;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+    const uint32_t rank = cluster_rank();
+    const OrthUnit w = orth_unit<kSym, 128, 128>(blockIdx.x / split, p);
+    const int kb0 = (int)(p.nkb * rank / split), kb1 = (int)(p.nkb * (rank + 1) / split);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(got, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        if (split > 1) mbar_arrive_expect_tx(got, (split - 1) * (65536 / split));
+        prefetch_tmap(&tm_a);
+        prefetch_tmap(&tm_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(slot, 128);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (split > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // ready to receive
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    orth_dep_wait();
+
+    // the epilogue's share: 32 rows a warp, 128 / split columns of the tile
+    const int q = warp & 3, r = q * 32 + lane;
+    const bool epilogue = warp >= 2;
+    const int64_t cols = kSym ? p.mp : p.np;
+    const int64_t i_warp = (int64_t)w.mb * 128 + q * 32, i = i_warp + lane, row = w.batch * p.mp + i;
+    const int lw = split == 1 ? 7 : split == 2 ? 6 : 5;   // log2 of the columns
+    const int width = 1 << lw, from = (int)rank * width;   // of the tile's columns
+    const int64_t n0 = (int64_t)w.nb * 128;
+    int chunks = epilogue && i_warp < p.mp ? width / 32 : 0;
+    while (chunks > 0 && n0 + from + 32 * (chunks - 1) >= cols) --chunks;
+    OrthInputs in;
+    float side = 0.f;
+    if (warp == 0) {
+        if (lane == 0) {
+            const int row0 = (int)(w.batch * p.mp), m0 = row0 + w.mb * 128;
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, last_par = 0;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!orth_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = base + stage * kStageBytes, bar = full0 + 8 * stage;
+                mbar_arrive_expect_tx(bar, kStageBytes);
+                tma_load_2d(dst, &tm_a, kb * kOrthBK, m0, bar);
+                if constexpr (kSym) {
+                    tma_load_2d(dst + kOrthABytes, &tm_b, kb * kOrthBK, row0 + (int)n0, bar);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        tma_load_2d(dst + kOrthABytes + j * 8192, &tm_b, (int)n0 + 64 * j, row0 + kb * kOrthBK, bar);
+                }
+                issued |= 1u << stage;
+                last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) {
+                for (int s = 0; s < kStages; ++s)
+                    if (issued & (1u << s)) mbar_wait(full0 + 8 * s, (last_par >> s) & 1u, kOrthWaitCycles);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = orth_idesc<128, 128, !kSym>();
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!orth_wait(full0 + 8 * stage, phase, abort_flag)) break;
+                tc_fence_after();
+                const uint32_t addr = base + stage * kStageBytes;
+                const uint64_t a_desc = orth_desc_k(addr);
+                const uint64_t b_desc = kSym ? orth_desc_k(addr + kOrthABytes) : orth_desc_mn(addr + kOrthABytes);
+                constexpr uint64_t kBStep = kSym ? (32 >> 4) : (2048 >> 4);
+#pragma unroll
+                for (int k = 0; k < kOrthBK / 16; ++k)
+                    umma_bf16(tmem, a_desc + (32 >> 4) * k, b_desc + kBStep * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+                umma_commit(empty0 + 8 * stage);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            umma_commit(tfull);   // also after a wait that ran out: what was issued drains
+        }
+    } else if (chunks > 0) {
+        if constexpr (kMode == kOrthPoly) side = p.d[row];
+        else if constexpr (!kSym) side = p.a + p.e[row];
+        orth_inputs<kMode>(p, w.batch, row, n0 + from, in);
+    }
+    __syncwarp();
+    // Everyone waits for the MMAs: shared memory is free after them, and no CTA leaves
+    // before its own are done.
+    const bool ok = orth_wait(tfull, 0, abort_flag);
+    tc_fence_after();
+    const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+    __syncthreads();
+    const uint32_t share = (uint32_t)width * 512;              // bytes of a share of the partial tile
+    const uint32_t pitch = (uint32_t)width * 4;
+    auto piece = [&](uint32_t buf, int j) { return buf + (uint32_t)r * pitch + (uint32_t)((j ^ (r & 7)) * 16); };
+    if (split > 1) {
+        if (epilogue && i_warp < p.mp) {   // over the stages
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t t[32];
+                __syncwarp();
+                tmem_ld32(lane_addr + 32 * c, t);
+                const uint32_t buf = base + ((uint32_t)(32 * c) >> lw) * share;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    sts_v4(piece(buf, ((32 * c) & (width - 1)) / 4 + k), t[4 * k], t[4 * k + 1], t[4 * k + 2], t[4 * k + 3]);
+            }
+            fence_proxy_async_smem();
+        }
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the others can receive
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (uint32_t k = 0; k < split; ++k)
+                if (k != rank) dsm_push(map_to_rank(recv + rank * share, k), base + k * share, share, map_to_rank(got, k));
+        orth_wait(got, 0, abort_flag);
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // has the others' partials
+    }
+    const bool mirror = kSym && w.nb > w.mb;
+    for (int c = 0; c < chunks; ++c) {
+        float v[32];
+        OrthInputs ahead;
+        if (c + 1 < chunks) orth_inputs<kMode>(p, w.batch, row, n0 + from + 32 * (c + 1), ahead);
+        if (split > 1) {
+#pragma unroll
+            for (uint32_t s = 0; s < 4; ++s) {
+                if (s < split) {
+                    const uint32_t buf = s == rank ? base + rank * share : recv + s * share;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 t = lds_v4(piece(buf, 8 * c + k));
+                        const float f[4] = {__uint_as_float(t.x), __uint_as_float(t.y), __uint_as_float(t.z),
+                                            __uint_as_float(t.w)};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[4 * k + j] = s == 0 ? f[j] : v[4 * k + j] + f[j];
+                    }
+                }
+            }
+        } else {
+            uint32_t t[32];
+            __syncwarp();
+            tmem_ld32(lane_addr + 32 * c, t);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(t[j]);
+        }
+        orth_finish<kMode>(p, w.batch, row, i, n0 + from + 32 * c, mirror, side, in, v);
+        in = ahead;
+    }
+    tc_fence_before();
+    __syncwarp();
+    // the others have this CTA's partials
+    if (split > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128);
+    }
+    (void)ok;
 }
 
 // ---------------------------------------------------------------- the input

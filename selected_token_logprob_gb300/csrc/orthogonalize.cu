@@ -79,11 +79,11 @@ struct OrthMaps {
     CUtensorMap a, b, b64, in, lo, out;   // operands (b64: b in boxes of 64 rows), the epilogue's
 };
 
-template <int kMode, int kBN, bool kPair>
+template <int kMode, int kBN, bool kPair, int kBoxes = 2>
 flp_status orth_launch(int dev, int fit, const OrthMaps& t, const flp::OrthArgs& p, cudaStream_t s) {
     static std::atomic<bool> ready[kMaxDevices];
-    const auto kern = flp::k_orth_product<kMode, kBN, kPair>;
-    constexpr size_t smem = flp::kOrthSmemBytes<kBN, kPair>;
+    const auto kern = flp::k_orth_product<kMode, kBN, kPair, kBoxes>;
+    constexpr size_t smem = flp::kOrthSmemBytes<kBN, kPair, kBoxes>;
     static_assert(smem <= 232448, "shared memory per CTA");
     if (!ready[dev].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -120,13 +120,43 @@ int64_t orth_tiles(bool sym, int64_t rows, int64_t cols, int bm, int bn) {
     return t;
 }
 
+// A product whose 128 x 128 tiles leave SMs idle: a cluster of `split` CTAs a tile.
+template <int kMode>
+flp_status orth_split_launch(int dev, int split, const OrthMaps& t, const flp::OrthArgs& p, cudaStream_t s) {
+    static std::atomic<bool> ready[kMaxDevices];
+    const auto kern = flp::k_orth_split<kMode>;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)flp::kOrthSplitSmem);
+        if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize setup: %s", cudaGetErrorString(e));
+        ready[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.units * split));
+    cfg.blockDim = dim3(flp::kOrthThreads);
+    cfg.dynamicSmemBytes = flp::kOrthSplitSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, t.a, kMode >= flp::kOrthApply ? t.b64 : t.b, p);
+    if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize product launch: %s", cudaGetErrorString(e));
+    return FLP_OK;
+}
+
 // CTA pairs that can be resident at once on `dev` (cached; 0 if the query fails).
 int orth_pairs(int dev) {
     static std::atomic<int> count[kMaxDevices];
     int c = count[dev].load(std::memory_order_acquire);
     if (c == 0) {
-        const auto kern = flp::k_orth_product<flp::kOrthGram, 256, true>;
-        constexpr size_t smem = flp::kOrthSmemBytes<256, true>;
+        const auto kern = flp::k_orth_product<flp::kOrthGram, 256, true, 2>;
+        constexpr size_t smem = flp::kOrthSmemBytes<256, true, 2>;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(flp::kOrthThreads);
@@ -159,6 +189,15 @@ flp_status orth_product(int dev, int sms, int pairs, int64_t batch, const OrthMa
         p.per = orth_tiles(kSym, p.mp, cols, bm, bn);
         p.units = batch * p.per;
     };
+    // Fewer 128 x 128 tiles than SMs: a tile a cluster, its K loop and its epilogue
+    // split over up to 4 CTAs (a call on 1024 x 1024: 135 us with the tiles below, 152
+    // unsplit, 117 split; 200 x 400: 90, 117, 89; 512 x 4096: 188, 193, 128).
+    shape(128, 128);
+    if (p.units <= sms) {
+        int split = 1;
+        while (split < 4 && p.units * split * 2 <= sms && p.nkb >= 4) split *= 2;
+        return orth_split_launch<kMode>(dev, split, t, p, s);
+    }
     // Cycles of a launch by tile: a K block takes its MMAs' time or the copies'
     // turn-around over the stages, a tile some 5000 on top, a wave each.
     struct Tile { int bm, bn, kblock; int64_t slots; };
@@ -175,7 +214,13 @@ flp_status orth_product(int dev, int sms, int pairs, int64_t batch, const OrthMa
         }
     }
     shape(tiles[pick].bm, tiles[pick].bn);
-    if (pick == 0) return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
+    if (pick == 0) {
+        // 8 x 1024 x 4096 (16 K blocks): 726 us with 2 boxes, 711 with 4; 4 x 2048 x 2048
+        // (32): 617 and 622
+        if constexpr (!kSym)
+            if (p.nkb <= 16) return orth_launch<kMode, 256, true, 4>(dev, pairs, t, p, s);
+        return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
+    }
     if (pick == 1) return orth_launch<kMode, 128, false>(dev, sms, t, p, s);
     return orth_launch<kMode, 64, false>(dev, sms, t, p, s);
 }
@@ -393,6 +438,8 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     p.np = l.np;
     p.d = reinterpret_cast<float*>(ws + l.d);
     p.e = reinterpret_cast<float*>(ws + l.e);
+    p.mat_in = reinterpret_cast<const __half*>(ws + l.a0);
+    p.x_lo = lo;
     p.out = out;
     p.out_dtype = out_dtype;
     p.transposed = rows > cols ? 1 : 0;
@@ -405,6 +452,8 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
         p.a = coefficients[3 * k];
         p.b = coefficients[3 * k + 1];
         p.c = coefficients[3 * k + 2];
+        p.x_hi = hi[cur];
+        p.x_out = hi[cur ^ 1];
         p.mat_out = reinterpret_cast<__half*>(ws + l.a0);
         OrthMaps t{op_x[cur], op_x[cur], op_x64[cur], ep_a0, ep_a0, ep_a0};   // Gram reads nothing beside its operands
         if ((st = orth_product<flp::kOrthGram>(dev, sms, pairs, batch, t, p, s)) != FLP_OK) return st;

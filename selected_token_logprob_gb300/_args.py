@@ -22,9 +22,11 @@ def _rows(x: torch.Tensor, name: str):
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D [N, V], got shape {tuple(x.shape)}")
     n, v = x.shape
-    if v > 1 and x.stride(1) != 1:
+    ld, step = x.stride()
+    if v > 1 and step != 1:
         raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
-    ld = x.stride(0) if n > 1 else max(v, x.stride(0))
+    if n <= 1:
+        ld = max(v, ld)
     if ld < v:
         raise ValueError(f"{name} row stride {ld} is smaller than its width {v}")
     return n, v, ld
@@ -33,9 +35,9 @@ def _rows(x: torch.Tensor, name: str):
 def _vec(t: torch.Tensor, name: str, n: int, dtype: torch.dtype) -> None:
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError(f"{name} must have shape [{n}], got {tuple(t.shape)}")
-    if n > 1 and t.stride(0) != 1:
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 

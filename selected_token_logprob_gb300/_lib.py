@@ -106,6 +106,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = False):
     """The loaded library; raises if it is not built (no silent fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -122,10 +122,12 @@ flp_status launch_bwd_any(const flp::NormBwdArgs& a, cudaStream_t s, int* parts)
     return check_launch("norm backward");
 }
 
-// Launches the row kernel; *parts = its CTAs, one partial row each.
+// Launches the row kernel.  *parts = its CTAs, one partial row each, that are left
+// to fold; 0 where the kernel folds them itself.
 template <class T, class G, int V, int kTpr, bool kFull>
 flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
     static std::atomic<bool> ready[kMaxDevices];
+    static std::atomic<int> fits[kMaxDevices];   // CTAs that can be resident at once + 1, with the most shared memory
     constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr;
     static_assert(kNormSms * flp::kNormBwdCtas<kTpr> <= flp::kNormParts, "a partial row per CTA");
     const auto kern = flp::k_norm_bwd<T, G, V, kTpr, kFull>;
@@ -136,9 +138,39 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
         return a.mean ? launch_bwd_any<T, G, true>(a, s, parts) : launch_bwd_any<T, G, false>(a, s, parts);
     flp_status st;
     if ((st = norm_setup(kern, dev, ready)) != FLP_OK) return st;
-    *parts = row_ctas(a.n, kRows, kNormSms * flp::kNormBwdCtas<kTpr>);
-    kern<<<*parts, kThreads, smem, s>>>(a);
-    return check_launch("norm backward");
+    const int grid = row_ctas(a.n, kRows, kNormSms * flp::kNormBwdCtas<kTpr>);
+    int fit = fits[dev].load(std::memory_order_acquire);
+    if (fit == 0) {
+        // for the widest row of this kernel, so that one number serves all its calls
+        const int64_t most = (int64_t)kTpr * flp::kNormElems;
+        const size_t top = (V > 1 ? (size_t)kThreads * flp::kNormElems * (sizeof(T) + sizeof(G))
+                                  : (size_t)(flp::norm_pitch<T>(most) + flp::norm_pitch<G>(most)) * kRows) *
+                           flp::kNormBwdStages<T, G>;
+        int per_sm = 0;
+        const int sms = sm_count(dev);
+        if (top > kNormMaxSmem || sms <= 0 ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, top) != cudaSuccess) {
+            (void)cudaGetLastError();
+            per_sm = 0;
+        }
+        fit = per_sm * sms + 1;
+        fits[dev].store(fit, std::memory_order_release);
+    }
+    const bool sums = a.part_w != nullptr || a.part_b != nullptr, grid_fold = sums && grid < fit;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = grid_fold ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, grid_fold ? 1 : 0);
+    if (e != cudaSuccess) return fail(FLP_ECUDA, "norm backward launch: %s", cudaGetErrorString(e));
+    *parts = grid_fold || !sums ? 0 : grid;
+    return ok();
 }
 
 template <class T, class G, int V, bool kFull>
@@ -269,7 +301,7 @@ flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy
     float* ws = static_cast<float*>(workspace);
     const flp::NormBwdArgs a{dy, ld_dy, x, n, d, ld_x, {weight, weight_dtype}, center ? mean : nullptr, rstd,
                              1.f / (float)d, dx, ld_dx, dweight ? ws : nullptr,
-                             dbias ? ws + (int64_t)flp::kNormParts * d : nullptr};
+                             dbias ? ws + (int64_t)flp::kNormParts * d : nullptr, dweight, dbias, accumulate != 0};
     const bool wide = dy_dtype == FLP_DTYPE_F32;
     const bool vec = (d * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) && rows_aligned16(dx, ld_dx, dtype) &&
                      rows_aligned16(dy, ld_dy, dy_dtype) && aligned16(weight);
@@ -282,11 +314,9 @@ flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy
                   : launch_norm_bwd<__half, __half>(a, vec, dev, s, &parts);
     else
         st = launch_norm_bwd<float, float>(a, vec, dev, s, &parts);
-    if (st != FLP_OK || !sums) return st;
-    const flp::NormFoldArgs f{a.part_w, a.part_b, parts, d, dweight, dbias, accumulate != 0};
-    return launch_dependent("norm fold", flp::k_norm_fold,
-                            dim3((unsigned)ceil_div(d, flp::kNormFoldCols), dweight && dbias ? 2 : 1),
-                            flp::kNormFoldCols * flp::kNormFoldRows, (size_t)0, s, f);
+    if (st != FLP_OK || parts == 0) return st;
+    return launch_dependent("norm fold", flp::k_norm_fold, dim3((unsigned)(2 * ceil_div(d, 32))), flp::kNormFoldThreads,
+                            (size_t)0, s, a, parts);
 }
 
 }  // extern "C"

@@ -9,6 +9,7 @@
 // All sums are FP32; y and dx are rounded once to x's type.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -63,6 +64,8 @@ struct NormBwdArgs {
     int64_t ld_dx;
     float* part_w;   // [kNormParts, d] partial sums of dy xh, or null
     float* part_b;   // [kNormParts, d] partial sums of dy, or null
+    float *dweight, *dbias;   // what the partial rows are folded into
+    int accumulate;
 };
 
 // Rows of partial weight gradients: a constant, so that the order of the sum
@@ -159,6 +162,50 @@ k_norm_dw_any(NormBwdArgs a) {
     }
     if (a.part_w) a.part_w[(int64_t)p * a.d + c] = sw;
     if (a.part_b) a.part_b[(int64_t)p * a.d + c] = sb;
+}
+
+// ---------------------------------------------------------------- partial rows
+
+// out[c] (+)= sum over the partial rows in a fixed order, 32 columns a CTA and
+// turn: its kWarps warps take every kWarps-th row each.
+template <int kWarps>
+__device__ __forceinline__ void norm_fold(const NormBwdArgs& a, int rows, float (*red)[33]) {
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int groups = (int)((a.d + 31) / 32);
+    for (int g = blockIdx.x; g < 2 * groups; g += gridDim.x) {
+        const bool second = g >= groups;
+        const float* part = second ? a.part_b : a.part_w;
+        float* out = second ? a.dbias : a.dweight;
+        if (part == nullptr) continue;   // uniform over the CTA
+        const int64_t c = (int64_t)(second ? g - groups : g) * 32 + tx;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        if (c < a.d) {
+            for (int r = ty; r < rows; r += 8 * kWarps) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = r + k * kWarps < rows ? __ldcg(part + (int64_t)(r + k * kWarps) * a.d + c) : 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) s[k & 3] += v[k];
+            }
+        }
+        __syncthreads();   // the last turn's readers
+        red[ty][tx] = (s[0] + s[1]) + (s[2] + s[3]);
+        __syncthreads();
+        if (ty == 0 && c < a.d) {
+            float t = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) t += red[k][tx];
+            out[c] = a.accumulate ? out[c] + t : t;
+        }
+    }
+}
+
+constexpr int kNormFoldThreads = 1024;
+__global__ void __launch_bounds__(kNormFoldThreads)
+k_norm_fold(NormBwdArgs a, int rows) {
+    __shared__ float red[kNormFoldThreads / 32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    norm_fold<kNormFoldThreads / 32>(a, rows, red);
 }
 
 // ---------------------------------------------------------------- rows in registers
@@ -479,11 +526,13 @@ k_norm_fwd(NormFwdArgs a) {
     }
 }
 
-// dx and this CTA's partial row of dw (and db).  kFull: with centring (unless
-// a.mean is null) and db; else RMS norm without db.
+// dx and this CTA's partial row of dw (and db), which the CTAs fold after a
+// barrier of the grid (a cooperative launch; `grid_fold`), saving the launch of
+// k_norm_fold: it costs a caller as much as the kernel on small batches.  kFull: with
+// centring (unless a.mean is null) and db; else RMS norm without db.
 template <class T, class G, int V, int kTpr, bool kFull>
 __global__ void __launch_bounds__(kNormThreads<kTpr>, kNormBwdCtas<kTpr>)
-k_norm_bwd(NormBwdArgs a) {
+k_norm_bwd(NormBwdArgs a, int grid_fold) {
     constexpr int NV = kNormElems / V, kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr;
     constexpr int kStages = kNormBwdStages<T, G>;
     extern __shared__ __align__(16) unsigned char norm_smem[];
@@ -593,7 +642,6 @@ k_norm_bwd(NormBwdArgs a) {
             }
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the CTA's partial row
     if constexpr (kRows == 1) {
 #pragma unroll
@@ -640,42 +688,10 @@ k_norm_bwd(NormBwdArgs a) {
             if (kFull && a.part_b) a.part_b[(int64_t)blockIdx.x * d + i] = sum[kFull ? 1 : 0][i];
         }
     }
-}
-
-// ---------------------------------------------------------------- partial rows
-
-constexpr int kNormFoldCols = 32, kNormFoldRows = 32;
-
-struct NormFoldArgs {
-    const float *part_w, *part_b;   // [rows, d] or null
-    int rows;
-    int64_t d;
-    float *dweight, *dbias;
-    int accumulate;
-};
-
-// out[c] (+)= sum over the partial rows in a fixed order: kNormFoldRows
-// threads share a column, each taking every kNormFoldRows-th row.
-__global__ void __launch_bounds__(kNormFoldCols * kNormFoldRows)
-k_norm_fold(NormFoldArgs a) {
-    __shared__ float red[kNormFoldRows][kNormFoldCols + 1];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float* part = blockIdx.y == 0 && a.part_w ? a.part_w : a.part_b;
-    float* out = blockIdx.y == 0 && a.part_w ? a.dweight : a.dbias;
-    const int tx = threadIdx.x % kNormFoldCols, ty = threadIdx.x / kNormFoldCols;
-    const int64_t c = (int64_t)blockIdx.x * kNormFoldCols + tx;
-    float s = 0.f;
-    if (c < a.d) {
-#pragma unroll 10
-        for (int r = ty; r < a.rows; r += kNormFoldRows) s += __ldcg(part + (int64_t)r * a.d + c);
-    }
-    red[ty][tx] = s;
-    __syncthreads();
-    if (ty == 0 && c < a.d) {
-        float t = 0.f;
-#pragma unroll
-        for (int k = 0; k < kNormFoldRows; ++k) t += red[k][tx];
-        out[c] = a.accumulate ? out[c] + t : t;
+    if (grid_fold) {
+        __shared__ float fold[kThreads / 32][33];
+        cooperative_groups::this_grid().sync();
+        norm_fold<kThreads / 32>(a, (int)gridDim.x, fold);
     }
 }
 

@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -70,6 +71,7 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=ORTHOGONALIZE_CO
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def orthogonalize_workspace_size(batch: int, rows: int, cols: int) -> int:
     """Bytes of device scratch that orthogonalize needs."""
     b = ctypes.c_int64(0)

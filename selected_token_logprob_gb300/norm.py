@@ -4,6 +4,7 @@ norm; forward, backward with the weight's and bias's gradients, autograd."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -19,12 +20,12 @@ def _affine(weight, bias, x, d: int) -> int:
     dtype = first.dtype
     if dtype != x.dtype and dtype != torch.float32:
         raise TypeError(f"weight and bias must be {x.dtype} or torch.float32, got {dtype}")
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            if t.dtype != dtype:
-                raise TypeError("weight and bias must have the same dtype")
-            _vec(t, name, d, dtype)
-            _cuda(t)
+    if weight is not None:
+        _vec(weight, "weight", d, dtype)
+        _cuda(weight)
+    if bias is not None:
+        _vec(bias, "bias", d, dtype)
+        _cuda(bias)
     return _DTYPES[dtype]
 
 
@@ -42,22 +43,23 @@ def fused_layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None
     if not 0.0 <= eps < float("inf"):
         raise ValueError(f"eps must be finite and >= 0, got {eps}")
     _cuda(x)
+    dev = x.device
     if y is None:
-        y, ld_y = torch.empty((n, d), dtype=x.dtype, device=x.device), d
+        y, ld_y = torch.empty((n, d), dtype=x.dtype, device=dev), d
     else:
-        if y.dtype != x.dtype or tuple(y.shape) != (n, d):
+        if y.dtype != x.dtype or y.shape != x.shape:
             raise ValueError("y must have x's dtype and shape")
         _, _, ld_y = _rows(y, "y")
         _cuda(y)
     if rstd is None:
-        rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(n, dtype=torch.float32, device=dev)
     else:
         _vec(rstd, "rstd", n, torch.float32)
         _cuda(rstd)
     if not center:
         mean = None
     elif mean is None:
-        mean = torch.empty(n, dtype=torch.float32, device=x.device)
+        mean = torch.empty(n, dtype=torch.float32, device=dev)
     else:
         _vec(mean, "mean", n, torch.float32)
         _cuda(mean)
@@ -69,6 +71,7 @@ def fused_layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None
     return y, mean, rstd
 
 
+@functools.lru_cache(maxsize=256)
 def fused_layer_norm_backward_workspace_size(d: int) -> int:
     """Bytes of device scratch that fused_layer_norm_backward needs for the
     partial sums of the weight's and bias's gradients."""
@@ -76,6 +79,18 @@ def fused_layer_norm_backward_workspace_size(d: int) -> int:
     _lib.check("fused_layer_norm_backward_workspace_size",
                _lib.load().fused_layer_norm_backward_workspace_size(int(d), ctypes.byref(b)))
     return int(b.value)
+
+
+def _sum_output(name: str, t, wanted: bool, accumulate: bool, d: int, dev):
+    if not wanted:
+        return None
+    if t is None:
+        if accumulate:
+            raise ValueError(f"accumulate needs the {name} tensor to add to")
+        return torch.empty(d, dtype=torch.float32, device=dev)
+    _vec(t, name, d, torch.float32)
+    _cuda(t)
+    return t
 
 
 def fused_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None,
@@ -92,9 +107,10 @@ def fused_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.T
     n, d, ld = _rows(x, "x")
     dt = _dtype(x, "x")
     wdt = _affine(weight, None, x, d)
-    if dy.dtype != x.dtype and dy.dtype != torch.float32:
-        raise TypeError(f"dy must be {x.dtype} or torch.float32, got {dy.dtype}")
-    if tuple(dy.shape) != (n, d):
+    gdt = dy.dtype
+    if gdt != x.dtype and gdt != torch.float32:
+        raise TypeError(f"dy must be {x.dtype} or torch.float32, got {gdt}")
+    if dy.shape != x.shape:
         raise ValueError(f"dy must have x's shape {(n, d)}, got {tuple(dy.shape)}")
     _, _, ld_dy = _rows(dy, "dy")
     _vec(rstd, "rstd", n, torch.float32)
@@ -106,36 +122,26 @@ def fused_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.T
     else:
         _vec(mean, "mean", n, torch.float32)
         _cuda(mean)
+    dev = x.device
     if dx is None:
-        dx, ld_dx = torch.empty((n, d), dtype=x.dtype, device=x.device), d
+        dx, ld_dx = torch.empty((n, d), dtype=x.dtype, device=dev), d
     else:
-        if dx.dtype != x.dtype or tuple(dx.shape) != (n, d):
+        if dx.dtype != x.dtype or dx.shape != x.shape:
             raise ValueError("dx must have x's dtype and shape")
         _, _, ld_dx = _rows(dx, "dx")
         _cuda(dx)
-    sums = []
-    for name, t, wanted in (("dweight", dweight, with_dweight), ("dbias", dbias, with_dbias)):
-        if not wanted:
-            t = None
-        elif t is not None:
-            _vec(t, name, d, torch.float32)
-            _cuda(t)
-        elif accumulate:
-            raise ValueError(f"accumulate needs the {name} tensor to add to")
-        else:
-            t = torch.empty(d, dtype=torch.float32, device=x.device)
-        sums.append(t)
-    dweight, dbias = sums
+    dweight = _sum_output("dweight", dweight, with_dweight, accumulate, d, dev)
+    dbias = _sum_output("dbias", dbias, with_dbias, accumulate, d, dev)
     wptr, wbytes = None, 0
     if workspace is not None:
         _cuda(workspace)
         wptr, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif n > 0 and (with_dweight or with_dbias):
         wbytes = fused_layer_norm_backward_workspace_size(d)
-        workspace = torch.empty(wbytes, dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(wbytes, dtype=torch.uint8, device=dev)
         wptr = workspace.data_ptr()
     st = _lib.load().fused_layer_norm_backward(
-        dy.data_ptr(), _DTYPES[dy.dtype], ld_dy, x.data_ptr(), dt, n, d, ld, _opt_ptr(weight), wdt,
+        dy.data_ptr(), _DTYPES[gdt], ld_dy, x.data_ptr(), dt, n, d, ld, _opt_ptr(weight), wdt,
         _opt_ptr(mean), rstd.data_ptr(), 1 if center else 0, wptr, wbytes, dx.data_ptr(), ld_dx,
         _opt_ptr(dweight), _opt_ptr(dbias), 1 if accumulate else 0, _stream(x))
     _lib.check("fused_layer_norm_backward", st)

@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -65,6 +66,7 @@ def logp_preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, ref_logp:
     return loss, grad, rewards
 
 
+@functools.lru_cache(maxsize=256)
 def logp_preference_loss_workspace_size(n: int, num_seqs: int) -> int:
     """Bytes of device scratch that logp_preference_loss needs."""
     b = ctypes.c_int64(0)

@@ -73,13 +73,13 @@ flp_status launch_fwd_any(const flp::NormFwdArgs& a, cudaStream_t s) {
     return check_launch("norm forward");
 }
 
-template <class T, class W, int V, int kTpr, bool kCenter>
+template <class T, class W, int kTpr, bool kCenter, bool kAligned>
 flp_status launch_fwd_rows(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
     static std::atomic<bool> ready[kMaxDevices];
     constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = flp::kNormFwdStages<T>;
-    const auto kern = flp::k_norm_fwd<T, W, V, kTpr, kCenter>;
-    const size_t smem =
-        (V > 1 ? (size_t)kThreads * flp::kNormElems * sizeof(T) : (size_t)flp::norm_pitch<T>(a.d) * kRows) * kStages;
+    const auto kern = flp::k_norm_fwd<T, W, kTpr, kCenter, kAligned>;
+    const size_t smem = kAligned ? (size_t)kThreads * flp::kNormElems * sizeof(T) * kStages
+                                 : (size_t)flp::norm_pitch<T>(a.d) * kRows * (kStages + 1);
     if (smem > kNormMaxSmem) return launch_fwd_any<T, kCenter>(a, s);
     flp_status st;
     if ((st = norm_setup(kern, dev, ready)) != FLP_OK) return st;
@@ -87,22 +87,21 @@ flp_status launch_fwd_rows(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
     return check_launch("norm forward");
 }
 
-template <class T, class W, int V, bool kCenter>
+template <class T, class W, bool kCenter, bool kAligned>
 flp_status launch_fwd_v(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
     constexpr int E = flp::kNormElems;
-    if (a.d <= 32 * E) return launch_fwd_rows<T, W, V, 32, kCenter>(a, dev, s);
-    if (a.d <= 128 * E) return launch_fwd_rows<T, W, V, 128, kCenter>(a, dev, s);
-    if (a.d <= 256 * E) return launch_fwd_rows<T, W, V, 256, kCenter>(a, dev, s);
-    if (a.d <= 512 * E) return launch_fwd_rows<T, W, V, 512, kCenter>(a, dev, s);
-    if (a.d <= 1024 * E) return launch_fwd_rows<T, W, V, 1024, kCenter>(a, dev, s);
+    if (a.d <= 32 * E) return launch_fwd_rows<T, W, 32, kCenter, kAligned>(a, dev, s);
+    if (a.d <= 128 * E) return launch_fwd_rows<T, W, 128, kCenter, kAligned>(a, dev, s);
+    if (a.d <= 256 * E) return launch_fwd_rows<T, W, 256, kCenter, kAligned>(a, dev, s);
+    if (a.d <= 512 * E) return launch_fwd_rows<T, W, 512, kCenter, kAligned>(a, dev, s);
+    if (a.d <= 1024 * E) return launch_fwd_rows<T, W, 1024, kCenter, kAligned>(a, dev, s);
     return launch_fwd_any<T, kCenter>(a, s);
 }
 
 template <class T, class W>
 flp_status launch_fwd_w(const flp::NormFwdArgs& a, bool center, bool vec, int dev, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
-    if (vec) return center ? launch_fwd_v<T, W, V, true>(a, dev, s) : launch_fwd_v<T, W, V, false>(a, dev, s);
-    return center ? launch_fwd_v<T, W, 1, true>(a, dev, s) : launch_fwd_v<T, W, 1, false>(a, dev, s);
+    if (vec) return center ? launch_fwd_v<T, W, true, true>(a, dev, s) : launch_fwd_v<T, W, false, true>(a, dev, s);
+    return center ? launch_fwd_v<T, W, true, false>(a, dev, s) : launch_fwd_v<T, W, false, false>(a, dev, s);
 }
 
 template <class T>
@@ -124,16 +123,19 @@ flp_status launch_bwd_any(const flp::NormBwdArgs& a, cudaStream_t s, int* parts)
 
 // Launches the row kernel.  *parts = its CTAs, one partial row each, that are left
 // to fold; 0 where the kernel folds them itself.
-template <class T, class G, int V, int kTpr, bool kFull>
+template <class T, class G, int kTpr, bool kFull, bool kAligned>
 flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
     static std::atomic<bool> ready[kMaxDevices];
     static std::atomic<int> fits[kMaxDevices];   // CTAs that can be resident at once + 1, with the most shared memory
     constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr;
     static_assert(kNormSms * flp::kNormBwdCtas<kTpr> <= flp::kNormParts, "a partial row per CTA");
-    const auto kern = flp::k_norm_bwd<T, G, V, kTpr, kFull>;
-    const size_t smem = (V > 1 ? (size_t)kThreads * flp::kNormElems * (sizeof(T) + sizeof(G))
-                               : (size_t)(flp::norm_pitch<T>(a.d) + flp::norm_pitch<G>(a.d)) * kRows) *
-                        flp::kNormBwdStages<T, G>;
+    const auto kern = flp::k_norm_bwd<T, G, kTpr, kFull, kAligned>;
+    auto bytes = [](int64_t d) {
+        return kAligned ? (size_t)kThreads * flp::kNormElems * (sizeof(T) + sizeof(G)) * flp::kNormBwdStages<T, G>
+                        : ((size_t)(flp::norm_pitch<T>(d) + flp::norm_pitch<G>(d)) * flp::kNormBwdStages<T, G> +
+                           flp::norm_pitch<T>(d)) * kRows;
+    };
+    const size_t smem = bytes(a.d);
     if (smem > kNormMaxSmem)
         return a.mean ? launch_bwd_any<T, G, true>(a, s, parts) : launch_bwd_any<T, G, false>(a, s, parts);
     flp_status st;
@@ -142,10 +144,7 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
     int fit = fits[dev].load(std::memory_order_acquire);
     if (fit == 0) {
         // for the widest row of this kernel, so that one number serves all its calls
-        const int64_t most = (int64_t)kTpr * flp::kNormElems;
-        const size_t top = (V > 1 ? (size_t)kThreads * flp::kNormElems * (sizeof(T) + sizeof(G))
-                                  : (size_t)(flp::norm_pitch<T>(most) + flp::norm_pitch<G>(most)) * kRows) *
-                           flp::kNormBwdStages<T, G>;
+        const size_t top = bytes((int64_t)kTpr * flp::kNormElems);
         int per_sm = 0;
         const int sms = sm_count(dev);
         if (top > kNormMaxSmem || sms <= 0 ||
@@ -173,13 +172,13 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
     return ok();
 }
 
-template <class T, class G, int V, bool kFull>
+template <class T, class G, bool kFull, bool kAligned>
 flp_status launch_bwd_v(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
     constexpr int E = flp::kNormElems;
-    if (a.d <= 32 * E) return launch_bwd_rows<T, G, V, 32, kFull>(a, dev, s, parts);
-    if (a.d <= 128 * E) return launch_bwd_rows<T, G, V, 128, kFull>(a, dev, s, parts);
-    if (a.d <= 256 * E) return launch_bwd_rows<T, G, V, 256, kFull>(a, dev, s, parts);
-    return launch_bwd_rows<T, G, V, 512, kFull>(a, dev, s, parts);
+    if (a.d <= 32 * E) return launch_bwd_rows<T, G, 32, kFull, kAligned>(a, dev, s, parts);
+    if (a.d <= 128 * E) return launch_bwd_rows<T, G, 128, kFull, kAligned>(a, dev, s, parts);
+    if (a.d <= 256 * E) return launch_bwd_rows<T, G, 256, kFull, kAligned>(a, dev, s, parts);
+    return launch_bwd_rows<T, G, 512, kFull, kAligned>(a, dev, s, parts);
 }
 
 template <class T, class G>
@@ -187,14 +186,14 @@ flp_status launch_norm_bwd(const flp::NormBwdArgs& a, bool vec, int dev, cudaStr
     const bool center = a.mean != nullptr, full = center || a.part_b != nullptr;
     if (a.d > 512 * flp::kNormElems)
         return center ? launch_bwd_any<T, G, true>(a, s, parts) : launch_bwd_any<T, G, false>(a, s, parts);
-    constexpr int V = 16 / sizeof(G);   // of the wider of the two
-    if (vec) return full ? launch_bwd_v<T, G, V, true>(a, dev, s, parts) : launch_bwd_v<T, G, V, false>(a, dev, s, parts);
-    return full ? launch_bwd_v<T, G, 1, true>(a, dev, s, parts) : launch_bwd_v<T, G, 1, false>(a, dev, s, parts);
+    if (vec)
+        return full ? launch_bwd_v<T, G, true, true>(a, dev, s, parts) : launch_bwd_v<T, G, false, true>(a, dev, s, parts);
+    return full ? launch_bwd_v<T, G, true, false>(a, dev, s, parts) : launch_bwd_v<T, G, false, false>(a, dev, s, parts);
 }
 
 bool norm_workspace_bytes(int64_t d, int64_t* out) {
     int64_t b;
-    if (__builtin_mul_overflow(d, (int64_t)(2 * flp::kNormParts * 4), &b)) return false;
+    if (d > INT64_MAX - 4 || __builtin_mul_overflow((d + 3) / 4 * 4, (int64_t)(2 * flp::kNormParts * 4), &b)) return false;
     *out = ceil_div(b, 256) * 256;
     return true;
 }
@@ -299,9 +298,10 @@ flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy
     DeviceGuard guard;
     if ((st = guard.enter(dev)) != FLP_OK) return st;
     float* ws = static_cast<float*>(workspace);
+    const int64_t dp = ceil_div(d, 4) * 4;
     const flp::NormBwdArgs a{dy, ld_dy, x, n, d, ld_x, {weight, weight_dtype}, center ? mean : nullptr, rstd,
-                             1.f / (float)d, dx, ld_dx, dweight ? ws : nullptr,
-                             dbias ? ws + (int64_t)flp::kNormParts * d : nullptr, dweight, dbias, accumulate != 0};
+                             1.f / (float)d, dx, ld_dx, dp, dweight ? ws : nullptr,
+                             dbias ? ws + (int64_t)flp::kNormParts * dp : nullptr, dweight, dbias, accumulate != 0};
     const bool wide = dy_dtype == FLP_DTYPE_F32;
     const bool vec = (d * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) && rows_aligned16(dx, ld_dx, dtype) &&
                      rows_aligned16(dy, ld_dy, dy_dtype) && aligned16(weight);
@@ -315,7 +315,7 @@ flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy
     else
         st = launch_norm_bwd<float, float>(a, vec, dev, s, &parts);
     if (st != FLP_OK || parts == 0) return st;
-    return launch_dependent("norm fold", flp::k_norm_fold, dim3((unsigned)(2 * ceil_div(d, 32))), flp::kNormFoldThreads,
+    return launch_dependent("norm fold", flp::k_norm_fold, dim3((unsigned)(2 * ceil_div(d, 8))), flp::kNormFoldThreads,
                             (size_t)0, s, a, parts);
 }
 

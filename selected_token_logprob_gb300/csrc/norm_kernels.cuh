@@ -62,8 +62,9 @@ struct NormBwdArgs {
     float inv_d;
     void* dx;
     int64_t ld_dx;
-    float* part_w;   // [kNormParts, d] partial sums of dy xh, or null
-    float* part_b;   // [kNormParts, d] partial sums of dy, or null
+    int64_t dp;      // d rounded up to 4: a partial row
+    float* part_w;   // [kNormParts, dp] partial sums of dy xh, or null
+    float* part_b;   // [kNormParts, dp] partial sums of dy, or null
     float *dweight, *dbias;   // what the partial rows are folded into
     int accumulate;
 };
@@ -160,50 +161,58 @@ k_norm_dw_any(NormBwdArgs a) {
         sw += g * xh;
         sb += g;
     }
-    if (a.part_w) a.part_w[(int64_t)p * a.d + c] = sw;
-    if (a.part_b) a.part_b[(int64_t)p * a.d + c] = sb;
+    if (a.part_w) a.part_w[(int64_t)p * a.dp + c] = sw;
+    if (a.part_b) a.part_b[(int64_t)p * a.dp + c] = sb;
 }
 
 // ---------------------------------------------------------------- partial rows
 
-// out[c] (+)= sum over the partial rows in a fixed order, 32 columns a CTA and
-// turn: its kWarps warps take every kWarps-th row each.
+// out[c] (+)= sum over the partial rows in a fixed order, 8 columns (a sector) a
+// CTA and turn: a warp reads 4 rows at a time, 16 loads in flight a lane.  (With 32
+// columns a CTA most CTAs of a narrow norm had none, and the others read their 608
+// rows for 7 us.)
 template <int kWarps>
-__device__ __forceinline__ void norm_fold(const NormBwdArgs& a, int rows, float (*red)[33]) {
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int groups = (int)((a.d + 31) / 32);
+__device__ __forceinline__ void norm_fold(const NormBwdArgs& a, int rows, float (*red)[8]) {
+    const int col = threadIdx.x & 7, sub = (threadIdx.x >> 3) & 3, ty = threadIdx.x >> 5;
+    const int groups = (int)((a.d + 7) / 8);
     for (int g = blockIdx.x; g < 2 * groups; g += gridDim.x) {
         const bool second = g >= groups;
         const float* part = second ? a.part_b : a.part_w;
         float* out = second ? a.dbias : a.dweight;
         if (part == nullptr) continue;   // uniform over the CTA
-        const int64_t c = (int64_t)(second ? g - groups : g) * 32 + tx;
+        const int64_t c = (int64_t)(second ? g - groups : g) * 8 + col;
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         if (c < a.d) {
-            for (int r = ty; r < rows; r += 8 * kWarps) {
-                float v[8];
+            for (int r = ty * 4 + sub; r < rows; r += 64 * kWarps) {
+                float v[16];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = r + k * kWarps < rows ? __ldcg(part + (int64_t)(r + k * kWarps) * a.d + c) : 0.f;
+                for (int k = 0; k < 16; ++k) {
+                    const int q = r + 4 * k * kWarps;
+                    v[k] = q < rows ? __ldcg(part + (int64_t)q * a.dp + c) : 0.f;
+                }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) s[k & 3] += v[k];
+                for (int k = 0; k < 16; ++k) s[k & 3] += v[k];
             }
         }
+        float t = (s[0] + s[1]) + (s[2] + s[3]);
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+        t += __shfl_xor_sync(0xffffffffu, t, 16);
         __syncthreads();   // the last turn's readers
-        red[ty][tx] = (s[0] + s[1]) + (s[2] + s[3]);
+        if (sub == 0) red[ty][col] = t;
         __syncthreads();
-        if (ty == 0 && c < a.d) {
-            float t = 0.f;
+        if (threadIdx.x < 8 && c < a.d) {
+            t = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) t += red[k][tx];
+            for (int k = 0; k < kWarps; ++k) t += red[k][col];
             out[c] = a.accumulate ? out[c] + t : t;
         }
     }
 }
 
-constexpr int kNormFoldThreads = 1024;
+constexpr int kNormFoldThreads = 256;
 __global__ void __launch_bounds__(kNormFoldThreads)
 k_norm_fold(NormBwdArgs a, int rows) {
-    __shared__ float red[kNormFoldThreads / 32][33];
+    __shared__ float red[kNormFoldThreads / 32][8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     norm_fold<kNormFoldThreads / 32>(a, rows, red);
 }
@@ -216,13 +225,17 @@ k_norm_fold(NormBwdArgs a, int rows) {
 // into a ring in shared memory with cp.async, so that the loads of several
 // rows are in flight while one is reduced and written.
 //
-// V > 1 (16-byte aligned rows of whole vectors): a thread owns vectors of V
-// elements, copies only its own and reads back only its own; the ring needs no
-// barrier.  V is 16 bytes of the wider of x and dy, so that the lanes' copies
-// of both are contiguous (with 8 elements a lane the FP32 dy was fetched in
-// two halves of every sector: 217 instead of XXX us at 32768 x 4096).
-// V = 1 (any alignment, stride and width): the row's threads copy the aligned
-// 16-byte blocks that hold the row, and read elements at their offset.
+// A thread owns vectors of V elements, V being 16 bytes of the wider of x and dy,
+// so that the lanes' copies of both are contiguous (with 8 elements a lane the
+// FP32 dy was fetched in two halves of every sector: the backward kernel at
+// 32768 x 4096 took 217 us, now 150).
+// kAligned (16-byte aligned rows of whole vectors): a thread copies only its own
+// vectors and reads back only its own; the ring needs no barrier.
+// Otherwise (any alignment, stride and width): the row's threads copy the aligned
+// 16-byte blocks that hold the row and shift their vectors out of two neighbours;
+// results go back through shared memory as aligned blocks, the row's first and last
+// element by element.  (Element loads and stores, one value a lane, were bound by
+// their instructions: 5003 x 1031 FP16, forward and backward, 44 us.)
 constexpr int kNormElems = 16;
 template <int kTpr>
 constexpr int kNormThreads = kTpr < 128 ? 128 : kTpr;
@@ -321,12 +334,10 @@ __device__ __forceinline__ NormWords<V * (int)sizeof(T)> norm_pack(const float (
     return q;
 }
 
-// Elements [i, i + V) of a vector of type W (V > 1: in 16-byte loads at most).
+// Elements [i, i + V) of a vector of type W, in 16-byte loads at most.
 template <class W, int V>
 __device__ __forceinline__ void norm_vec_load(const W* p, int i, float (&o)[V]) {
-    if constexpr (V == 1) {
-        o[0] = to_f32(__ldg(p + i));
-    } else if constexpr (V * sizeof(W) <= 16) {
+    if constexpr (V * sizeof(W) <= 16) {
         norm_unpack<W, V>(norm_ldg<V * (int)sizeof(W)>(p + i), o);
     } else {
 #pragma unroll
@@ -372,14 +383,18 @@ template <class T>
 __host__ __device__ __forceinline__ uint32_t norm_pitch(int64_t d) {
     return (uint32_t)((d * (int64_t)sizeof(T) + 15) / 16 + 1) * 16;
 }
+template <class T>
+__device__ __forceinline__ uint32_t norm_misaligned(const T* p) {
+    return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+}
 
-// Copies row `r` of `base` (n rows of d elements, ld apart) into the ring: V > 1:
-// this thread's vectors, into its own places from `dst` on; V = 1: this thread's
+// Copies row `r` of `base` (rows of d elements, ld apart) into the ring: kAligned:
+// this thread's vectors, into its own places from `dst` on; else this thread's
 // blocks of the row, whose first byte comes to dst + (address mod 16).
-template <class T, int V, int kTpr>
+template <class T, int V, int kTpr, bool kAligned>
 __device__ __forceinline__ void norm_issue(const T* base, int64_t r, int64_t ld, int d, int t, uint32_t dst) {
     const T* p = base + r * ld;
-    if constexpr (V > 1) {
+    if constexpr (kAligned) {
         constexpr int NV = kNormElems / V, kBytes = V * (int)sizeof(T);
         const int nvec = d / V;
 #pragma unroll
@@ -388,7 +403,7 @@ __device__ __forceinline__ void norm_issue(const T* base, int64_t r, int64_t ld,
             if (v < nvec) cp_async<kBytes>(dst + k * kNormThreads<kTpr> * kBytes, p + v * V);
         }
     } else {
-        const int mis = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+        const int mis = (int)norm_misaligned(p);
         const int bytes = mis + d * (int)sizeof(T);
         const char* first = reinterpret_cast<const char*>(p) - mis;
         for (int b = t * 16; b < bytes; b += kTpr * 16) {
@@ -408,53 +423,111 @@ __device__ __forceinline__ void norm_issue(const T* base, int64_t r, int64_t ld,
         }
     }
 }
-// Values of vector k kTpr + t of the row copied to `src`; V = 1: of that
-// element, `src` being the row's first.
-template <class T, int V, int kTpr>
-__device__ __forceinline__ void norm_slot(uint32_t src, int k, int t, float (&o)[V]) {
-    if constexpr (V > 1) {
-        norm_unpack<T, V>(norm_lds<V * (int)sizeof(T)>(src + k * kNormThreads<kTpr> * V * (int)sizeof(T)), o);
-    } else if constexpr (sizeof(T) == 4) {
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(o[0]) : "r"(src + (k * kTpr + t) * 4) : "memory");
-    } else {
-        unsigned short h;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(src + (k * kTpr + t) * 2) : "memory");
-        o[0] = to_f32(*reinterpret_cast<const T*>(&h));
+// kBytes (8 or 16) bytes of shared memory from byte `at` on, an element's multiple:
+// two aligned pieces, shifted together.
+template <int kBytes>
+__device__ __forceinline__ NormWords<kBytes> norm_lds_shifted(uint32_t at) {
+    constexpr int N = kBytes / 4;
+    const uint32_t a = at & ~(uint32_t)(kBytes - 1);
+    const NormWords<kBytes> lo = norm_lds<kBytes>(a), hi = norm_lds<kBytes>(a + kBytes);
+    uint32_t w[2 * N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        w[k] = lo.w[k];
+        w[N + k] = hi.w[k];
     }
+    const uint32_t words = (at >> 2) & (N - 1), bits = (at & 3u) * 8;
+    // by whole words (the same for the whole row), then by half a word
+#pragma unroll
+    for (int s = N / 2; s >= 1; s >>= 1) {
+        if (words & s) {
+#pragma unroll
+            for (int k = 0; k + s < 2 * N; ++k) w[k] = w[k + s];
+        }
+    }
+    NormWords<kBytes> r;
+#pragma unroll
+    for (int k = 0; k < N; ++k) r.w[k] = __funnelshift_r(w[k], w[k + 1], bits);
+    return r;
 }
-template <class T>
-__device__ __forceinline__ uint32_t norm_misaligned(const T* p) {
-    return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+// Vector k kTpr + t of the row copied to `src`; !kAligned: `src` is the row's first byte.
+template <class T, int V, int kTpr, bool kAligned>
+__device__ __forceinline__ void norm_slot(uint32_t src, int k, int t, float (&o)[V]) {
+    constexpr int kBytes = V * (int)sizeof(T);
+    if constexpr (kAligned) norm_unpack<T, V>(norm_lds<kBytes>(src + k * kNormThreads<kTpr> * kBytes), o);
+    else norm_unpack<T, V>(norm_lds_shifted<kBytes>(src + (k * kTpr + t) * kBytes), o);
 }
 // After the wait for this thread's copies: those of the row's other threads.
-template <int V, int kTpr>
+template <int kTpr, bool kAligned>
 __device__ __forceinline__ void norm_copied() {
-    if constexpr (V == 1) {
+    if constexpr (!kAligned) {
         if constexpr (kTpr == 32) __syncwarp();
         else __syncthreads();
     }
 }
+// The row of d elements staged at `src` (16-byte aligned) to p, at any alignment.
+template <class T, int kTpr>
+__device__ __forceinline__ void norm_store_row(T* p, int d, int t, uint32_t src) {
+    const int mis = (int)norm_misaligned(p), bytes = mis + d * (int)sizeof(T);
+    char* first = reinterpret_cast<char*>(p) - mis;
+    for (int b = t * 16; b < bytes; b += kTpr * 16) {
+        if (b >= mis && b + 16 <= bytes) {
+            norm_stg<16>(first + b, norm_lds_shifted<16>(src + b - mis));
+        } else {
+            for (int o = b > mis ? b : mis; o < b + 16 && o < bytes; o += (int)sizeof(T)) {
+                if constexpr (sizeof(T) == 4) {
+                    uint32_t v;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(src + o - mis) : "memory");
+                    *reinterpret_cast<uint32_t*>(first + o) = v;
+                } else {
+                    unsigned short v;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(src + o - mis) : "memory");
+                    *reinterpret_cast<unsigned short*>(first + o) = v;
+                }
+            }
+        }
+    }
+}
+template <int kBytes>
+__device__ __forceinline__ void norm_sts(uint32_t a, const NormWords<kBytes>& r) {
+    if constexpr (kBytes == 16)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]),
+                     "r"(r.w[3]) : "memory");
+    else asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(r.w[0]), "r"(r.w[1]) : "memory");
+}
+// Vector i of a weight or bias vector of d elements; a vector that is cut by the end, or
+// a whole array that is not aligned for it, element by element (absent ones 0).
+template <class W, int V, bool kAligned>
+__device__ __forceinline__ void norm_vec_get(const W* p, bool aligned, int i, int d, float (&o)[V]) {
+    if (kAligned || (aligned && (i + 1) * V <= d)) {
+        norm_vec_load<W, V>(p, i * V, o);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = i * V + j < d ? to_f32(__ldg(p + i * V + j)) : 0.f;
+    }
+}
 
-template <class T, class W, int V, int kTpr, bool kCenter>
+template <class T, class W, int kTpr, bool kCenter, bool kAligned>
 __global__ void __launch_bounds__(kNormThreads<kTpr>, kNormFwdCtas<kTpr>)
 k_norm_fwd(NormFwdArgs a) {
-    constexpr int NV = kNormElems / V, kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr;
-    constexpr int kStages = kNormFwdStages<T>;
+    constexpr int V = 16 / (int)sizeof(T), NV = kNormElems / V;
+    constexpr int kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = kNormFwdStages<T>;
     extern __shared__ __align__(16) unsigned char norm_smem[];
     __shared__ float red[2 * 64];
     int turn = 0;
-    const int t = threadIdx.x % kTpr, d = (int)a.d, nvec = d / V;
+    const int t = threadIdx.x % kTpr, d = (int)a.d, nvec = (d + V - 1) / V;
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / kTpr;
-    // V > 1: the thread's places; V = 1: the row's slot
-    const uint32_t pitch = V > 1 ? kThreads * kNormElems * (uint32_t)sizeof(T) : norm_pitch<T>(d) * kRows;
+    // kAligned: the thread's places; else the row's slot, and after the ring its staged result
+    const uint32_t pitch = kAligned ? kThreads * kNormElems * (uint32_t)sizeof(T) : norm_pitch<T>(d) * kRows;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(norm_smem) +
-                          (V > 1 ? threadIdx.x * V * (uint32_t)sizeof(T) : threadIdx.x / kTpr * norm_pitch<T>(d));
+                          (kAligned ? threadIdx.x * 16 : threadIdx.x / kTpr * norm_pitch<T>(d));
     const T* x = static_cast<const T*>(a.x);
     const W *w = static_cast<const W*>(a.w.p), *b = static_cast<const W*>(a.b.p);
+    const bool w_al = norm_misaligned(w) == 0, b_al = norm_misaligned(b) == 0;
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) {
-        if (r + k * step < a.n) norm_issue<T, V, kTpr>(x, r + k * step, a.ld_x, d, t, ring + k * pitch);
+        if (r + k * step < a.n) norm_issue<T, V, kTpr, kAligned>(x, r + k * step, a.ld_x, d, t, ring + k * pitch);
         cp_async_commit();
     }
     int stage = 0;
@@ -462,17 +535,26 @@ k_norm_fwd(NormFwdArgs a) {
         float v[NV][V];
         const int64_t ahead = r + (kStages - 1) * step;
         const int into = stage == 0 ? kStages - 1 : stage - 1;
-        if (ahead < a.n) norm_issue<T, V, kTpr>(x, ahead, a.ld_x, d, t, ring + into * pitch);
+        if (ahead < a.n) norm_issue<T, V, kTpr, kAligned>(x, ahead, a.ld_x, d, t, ring + into * pitch);
         cp_async_commit();
         cp_async_wait<kStages - 1>();
-        norm_copied<V, kTpr>();
-        const uint32_t src = ring + stage * pitch + (V > 1 ? 0 : norm_misaligned(x + r * a.ld_x));
+        norm_copied<kTpr, kAligned>();
+        const uint32_t src = ring + stage * pitch + (kAligned ? 0 : norm_misaligned(x + r * a.ld_x));
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (k * kTpr + t < nvec) norm_slot<T, V, kTpr>(src, k, t, v[k]);
-            else
+            const int i = k * kTpr + t;
+            if (i < nvec) {
+                norm_slot<T, V, kTpr, kAligned>(src, k, t, v[k]);
+                if constexpr (!kAligned) {
+                    if ((i + 1) * V > d) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) v[k][j] = i * V + j < d ? v[k][j] : 0.f;
+                    }
+                }
+            } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j) v[k][j] = 0.f;
+            }
         }
         stage = stage == kStages - 1 ? 0 : stage + 1;
         float mu = 0.f;
@@ -488,16 +570,20 @@ k_norm_fwd(NormFwdArgs a) {
         float q[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (!kCenter || k * kTpr + t < nvec)
+            const int i = k * kTpr + t;
+            if (!kCenter || i < nvec) {
+                const int have = kAligned || !kCenter ? V : d - i * V;   // what lies past the row is not mu away
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float c = v[k][j] - mu;
-                    q[0] += c * c;
+                    if (kAligned || !kCenter || j < have) q[0] += c * c;
                 }
+            }
         }
         norm_row_sum<kTpr, 1>(q, red, turn);
         const float rstd = __frsqrt_rn(q[0] * a.inv_d + a.eps);
         T* y = static_cast<T*>(a.y) + r * a.ld_y;
+        const uint32_t out = ring + kStages * pitch;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
@@ -506,18 +592,22 @@ k_norm_fwd(NormFwdArgs a) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) v[k][j] = (v[k][j] - mu) * rstd;
                 if (w != nullptr) {
-                    norm_vec_load<W, V>(w, i * V, f);
+                    norm_vec_get<W, V, kAligned>(w, w_al, i, d, f);
 #pragma unroll
                     for (int j = 0; j < V; ++j) v[k][j] *= f[j];
                 }
                 if (b != nullptr) {
-                    norm_vec_load<W, V>(b, i * V, f);
+                    norm_vec_get<W, V, kAligned>(b, b_al, i, d, f);
 #pragma unroll
                     for (int j = 0; j < V; ++j) v[k][j] += f[j];
                 }
-                if constexpr (V > 1) norm_stg(y + i * V, norm_pack<T, V>(v[k]));
-                else y[i] = from_f32<T>(v[k][0]);
+                if constexpr (kAligned) norm_stg(y + i * V, norm_pack<T, V>(v[k]));
+                else norm_sts(out + i * 16, norm_pack<T, V>(v[k]));
             }
+        }
+        if constexpr (!kAligned) {
+            norm_copied<kTpr, kAligned>();   // the whole row is staged
+            norm_store_row<T, kTpr>(y, d, t, out);
         }
         if (t == 0) {
             if (kCenter && a.mean) a.mean[r] = mu;
@@ -530,32 +620,33 @@ k_norm_fwd(NormFwdArgs a) {
 // barrier of the grid (a cooperative launch; `grid_fold`), saving the launch of
 // k_norm_fold: it costs a caller as much as the kernel on small batches.  kFull: with
 // centring (unless a.mean is null) and db; else RMS norm without db.
-template <class T, class G, int V, int kTpr, bool kFull>
+template <class T, class G, int kTpr, bool kFull, bool kAligned>
 __global__ void __launch_bounds__(kNormThreads<kTpr>, kNormBwdCtas<kTpr>)
 k_norm_bwd(NormBwdArgs a, int grid_fold) {
-    constexpr int NV = kNormElems / V, kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr;
-    constexpr int kStages = kNormBwdStages<T, G>;
+    constexpr int V = 16 / (int)sizeof(G), NV = kNormElems / V;
+    constexpr int kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = kNormBwdStages<T, G>;
     extern __shared__ __align__(16) unsigned char norm_smem[];
     __shared__ float red[2 * 64];
     int turn = 0;
-    const int t = threadIdx.x % kTpr, d = (int)a.d, nvec = d / V;
+    const int t = threadIdx.x % kTpr, d = (int)a.d, nvec = (d + V - 1) / V;
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / kTpr;
-    const uint32_t xpitch = V > 1 ? kThreads * kNormElems * (uint32_t)sizeof(T) : norm_pitch<T>(d) * kRows;
-    const uint32_t pitch = xpitch + (V > 1 ? kThreads * kNormElems * (uint32_t)sizeof(G) : norm_pitch<G>(d) * kRows);
+    // kAligned: the thread's places; else the rows' slots, and after the ring the staged dx
+    const uint32_t xpitch = kAligned ? kThreads * kNormElems * (uint32_t)sizeof(T) : norm_pitch<T>(d) * kRows;
+    const uint32_t pitch = xpitch + (kAligned ? kThreads * kNormElems * (uint32_t)sizeof(G) : norm_pitch<G>(d) * kRows);
     const uint32_t smem = (uint32_t)__cvta_generic_to_shared(norm_smem);
     const uint32_t ring_x =
-        smem + (V > 1 ? threadIdx.x * V * (uint32_t)sizeof(T) : threadIdx.x / kTpr * norm_pitch<T>(d));
+        smem + (kAligned ? threadIdx.x * V * (uint32_t)sizeof(T) : threadIdx.x / kTpr * norm_pitch<T>(d));
     const uint32_t ring_g =
-        smem + xpitch + (V > 1 ? threadIdx.x * V * (uint32_t)sizeof(G) : threadIdx.x / kTpr * norm_pitch<G>(d));
+        smem + xpitch + (kAligned ? threadIdx.x * V * (uint32_t)sizeof(G) : threadIdx.x / kTpr * norm_pitch<G>(d));
     const T* x = static_cast<const T*>(a.x);
     const G* dy = static_cast<const G*>(a.dy);
     const bool center = kFull && a.mean != nullptr;
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) {
         if (r + k * step < a.n) {
-            norm_issue<T, V, kTpr>(x, r + k * step, a.ld_x, d, t, ring_x + k * pitch);
-            norm_issue<G, V, kTpr>(dy, r + k * step, a.ld_dy, d, t, ring_g + k * pitch);
+            norm_issue<T, V, kTpr, kAligned>(x, r + k * step, a.ld_x, d, t, ring_x + k * pitch);
+            norm_issue<G, V, kTpr, kAligned>(dy, r + k * step, a.ld_dy, d, t, ring_g + k * pitch);
         }
         cp_async_commit();
     }
@@ -571,12 +662,14 @@ k_norm_bwd(NormBwdArgs a, int grid_fold) {
         }
     }
     if (a.w.p != nullptr) {
+        const bool al = norm_misaligned(static_cast<const char*>(a.w.p)) == 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
             if (i < nvec) {
-                if (sizeof(T) == 4 || a.w.dtype == 2) norm_vec_load<float, V>(static_cast<const float*>(a.w.p), i * V, w[k]);
-                else norm_vec_load<T, V>(static_cast<const T*>(a.w.p), i * V, w[k]);
+                if (sizeof(T) == 4 || a.w.dtype == 2)
+                    norm_vec_get<float, V, kAligned>(static_cast<const float*>(a.w.p), al, i, d, w[k]);
+                else norm_vec_get<T, V, kAligned>(static_cast<const T*>(a.w.p), al, i, d, w[k]);
             }
         }
     }
@@ -595,21 +688,31 @@ k_norm_bwd(NormBwdArgs a, int grid_fold) {
         const int64_t ahead = r + (kStages - 1) * step;
         const int into = stage == 0 ? kStages - 1 : stage - 1;
         if (ahead < a.n) {
-            norm_issue<T, V, kTpr>(x, ahead, a.ld_x, d, t, ring_x + into * pitch);
-            norm_issue<G, V, kTpr>(dy, ahead, a.ld_dy, d, t, ring_g + into * pitch);
+            norm_issue<T, V, kTpr, kAligned>(x, ahead, a.ld_x, d, t, ring_x + into * pitch);
+            norm_issue<G, V, kTpr, kAligned>(dy, ahead, a.ld_dy, d, t, ring_g + into * pitch);
         }
         cp_async_commit();
         cp_async_wait<kStages - 1>();
-        norm_copied<V, kTpr>();
-        const uint32_t sx = ring_x + stage * pitch + (V > 1 ? 0 : norm_misaligned(x + r * a.ld_x));
-        const uint32_t sg = ring_g + stage * pitch + (V > 1 ? 0 : norm_misaligned(dy + r * a.ld_dy));
+        norm_copied<kTpr, kAligned>();
+        const uint32_t sx = ring_x + stage * pitch + (kAligned ? 0 : norm_misaligned(x + r * a.ld_x));
+        const uint32_t sg = ring_g + stage * pitch + (kAligned ? 0 : norm_misaligned(dy + r * a.ld_dy));
         float xh[NV][V], g[NV][V];   // xh, then dx; dy, then dy w
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (k * kTpr + t < nvec) {
-                norm_slot<T, V, kTpr>(sx, k, t, xh[k]);
-                norm_slot<G, V, kTpr>(sg, k, t, g[k]);
+            const int i = k * kTpr + t;
+            if (i < nvec) {
+                norm_slot<T, V, kTpr, kAligned>(sx, k, t, xh[k]);
+                norm_slot<G, V, kTpr, kAligned>(sg, k, t, g[k]);
+                if constexpr (!kAligned) {
+                    if ((i + 1) * V > d) {   // past the row: nothing
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            xh[k][j] = i * V + j < d ? xh[k][j] : mu;
+                            g[k][j] = i * V + j < d ? g[k][j] : 0.f;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     xh[k][j] = (xh[k][j] - mu) * rstd;
@@ -631,15 +734,20 @@ k_norm_bwd(NormBwdArgs a, int grid_fold) {
         }
         const float c2 = s[0] * a.inv_d, c1 = center ? s[1] * a.inv_d : 0.f;
         T* dx = static_cast<T*>(a.dx) + r * a.ld_dx;
+        const uint32_t out = smem + kStages * pitch + threadIdx.x / kTpr * norm_pitch<T>(d);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
             if (i < nvec) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) xh[k][j] = (g[k][j] - c1 - xh[k][j] * c2) * rstd;
-                if constexpr (V > 1) norm_stg(dx + i * V, norm_pack<T, V>(xh[k]));
-                else dx[i] = from_f32<T>(xh[k][0]);
+                if constexpr (kAligned) norm_stg(dx + i * V, norm_pack<T, V>(xh[k]));
+                else norm_sts(out + i * V * (uint32_t)sizeof(T), norm_pack<T, V>(xh[k]));
             }
+        }
+        if constexpr (!kAligned) {
+            norm_copied<kTpr, kAligned>();   // the whole row is staged
+            norm_store_row<T, kTpr>(dx, d, t, out);
         }
     }
     // the CTA's partial row
@@ -648,21 +756,17 @@ k_norm_bwd(NormBwdArgs a, int grid_fold) {
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
             if (i < nvec) {
-                const int64_t at = (int64_t)blockIdx.x * d + i * V;
-                if constexpr (V > 1) {
+                const int64_t at = (int64_t)blockIdx.x * a.dp + i * V;
 #pragma unroll
-                    for (int h = 0; h < V; h += 4) {
-                        if (a.part_w)
-                            *reinterpret_cast<float4*>(a.part_w + at + h) =
-                                make_float4(dw[k][h], dw[k][h + 1], dw[k][h + 2], dw[k][h + 3]);
-                        if constexpr (kFull)
-                            if (a.part_b)
-                                *reinterpret_cast<float4*>(a.part_b + at + h) =
-                                    make_float4(db[k][h], db[k][h + 1], db[k][h + 2], db[k][h + 3]);
-                    }
-                } else {
-                    if (a.part_w) a.part_w[at] = dw[k][0];
-                    if (kFull && a.part_b) a.part_b[at] = db[k][0];
+                for (int h = 0; h < V; h += 4) {   // past the row, but inside its padding: zeros
+                    if (!kAligned && i * V + h >= d) break;
+                    if (a.part_w)
+                        *reinterpret_cast<float4*>(a.part_w + at + h) =
+                            make_float4(dw[k][h], dw[k][h + 1], dw[k][h + 2], dw[k][h + 3]);
+                    if constexpr (kFull)
+                        if (a.part_b)
+                            *reinterpret_cast<float4*>(a.part_b + at + h) =
+                                make_float4(db[k][h], db[k][h + 1], db[k][h + 2], db[k][h + 3]);
                 }
             }
         }
@@ -684,12 +788,12 @@ k_norm_bwd(NormBwdArgs a, int grid_fold) {
             __syncthreads();
         }
         for (int i = threadIdx.x; i < d; i += kThreads) {
-            if (a.part_w) a.part_w[(int64_t)blockIdx.x * d + i] = sum[0][i];
-            if (kFull && a.part_b) a.part_b[(int64_t)blockIdx.x * d + i] = sum[kFull ? 1 : 0][i];
+            if (a.part_w) a.part_w[(int64_t)blockIdx.x * a.dp + i] = sum[0][i];
+            if (kFull && a.part_b) a.part_b[(int64_t)blockIdx.x * a.dp + i] = sum[kFull ? 1 : 0][i];
         }
     }
     if (grid_fold) {
-        __shared__ float fold[kThreads / 32][33];
+        __shared__ float fold[kThreads / 32][8];
         cooperative_groups::this_grid().sync();
         norm_fold<kThreads / 32>(a, (int)gridDim.x, fold);
     }

@@ -42,6 +42,10 @@ constexpr float kOrthScale = 256.f;          // of every FP16 operand
 constexpr float kOrthLoScale = 2048.f;       // of lo, on top: hi's rounding is below 2^-11
 constexpr long long kOrthWaitCycles = 4000000000LL;
 constexpr int kOrthThreads = 192;
+// The persistent kernel's epilogue: two warps per 32 rows, each with half of a tile's
+// columns (with one, a chunk of 32 columns took 1350 cycles, the latencies of its own
+// instructions, and 8 x 1024 x 4096's products waited for it).
+constexpr int kOrthEpiWarps = 8, kOrthProductThreads = 64 + 32 * kOrthEpiWarps;
 constexpr int kOrthBK = 64;
 constexpr int kOrthParts = 256;              // most partial sums of squares per matrix
 
@@ -157,12 +161,17 @@ template <int kBN, bool kPair>
 constexpr uint32_t kOrthBBytes = (kPair ? kBN / 2 : kBN) * kOrthBK * 2;
 template <int kBN, bool kPair>
 constexpr uint32_t kOrthStageBytes = kOrthABytes + kOrthBBytes<kBN, kPair>;
-constexpr uint32_t kOrthBoxBytes = 4096;   // 32 rows x 64 columns of one matrix, or x 32 columns of hi and of lo
-template <int kBN, bool kPair, int kBoxes>
-constexpr int kOrthStages = (229376 - 4 * kBoxes * (int)kOrthBoxBytes) / (int)kOrthStageBytes<kBN, kPair>;
-template <int kBN, bool kPair, int kBoxes>
-constexpr size_t kOrthSmemBytes = 1024 + (size_t)kOrthStages<kBN, kPair, kBoxes> * kOrthStageBytes<kBN, kPair> + 1024 +
-                                  4 * kBoxes * (size_t)kOrthBoxBytes;
+// 32 rows x 32 columns of one matrix (Gram, Poly), or of hi and of lo
+constexpr uint32_t kOrthSquareBytes = 32 * 32 * 2;
+template <bool kSym>
+constexpr uint32_t kOrthBoxBytes = kSym ? kOrthSquareBytes : 2 * kOrthSquareBytes;
+constexpr int kOrthBoxes = 2;              // a warp
+template <int kBN, bool kPair, bool kSym>
+constexpr int kOrthStages =
+    (229376 - kOrthEpiWarps * kOrthBoxes * (int)kOrthBoxBytes<kSym>) / (int)kOrthStageBytes<kBN, kPair>;
+template <int kBN, bool kPair, bool kSym>
+constexpr size_t kOrthSmemBytes = 1024 + (size_t)kOrthStages<kBN, kPair, kSym> * kOrthStageBytes<kBN, kPair> + 1024 +
+                                  kOrthEpiWarps * kOrthBoxes * (size_t)kOrthBoxBytes<kSym>;
 
 __device__ __forceinline__ uint32_t orth_pack(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -185,13 +194,11 @@ struct OrthRows {
 };
 
 // 32 accumulators of row w.i, columns c0 .. c0 + 31 (c0 a multiple of 32, all
-// inside the padded output), with the boxes of the 64-column chunk they lie in;
-// the results go back into the boxes.  `diag`: these columns meet the warp's rows.
+// inside the padded output), with their box; the results go back into it.  `diag`: these columns meet the warp's rows.
 template <int kMode>
 __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows& w, bool diag, bool mirror,
                                               int64_t batch, int64_t c0, uint32_t box, int lane, uint32_t (&r)[32]) {
     constexpr float kInv = 1.f / kOrthScale;
-    const int half = (int)((c0 >> 5) & 1) * 4;   // first 16-byte piece of these columns
     float v[32];
     if constexpr (kMode == kOrthGram || kMode == kOrthPoly) {
         if constexpr (kMode == kOrthGram) {
@@ -212,7 +219,7 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
             float sq = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint4 x = lds_v4(orth_piece(box, lane, half + q));
+                const uint4 x = lds_v4(orth_piece64(box, lane, q));
                 const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
@@ -237,7 +244,7 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            sts_v4(orth_piece(box, lane, half + q), orth_pack(v[8 * q], v[8 * q + 1]),
+            sts_v4(orth_piece64(box, lane, q), orth_pack(v[8 * q], v[8 * q + 1]),
                    orth_pack(v[8 * q + 2], v[8 * q + 3]), orth_pack(v[8 * q + 4], v[8 * q + 5]),
                    orth_pack(v[8 * q + 6], v[8 * q + 7]));
         if (mirror) {
@@ -247,7 +254,7 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
         }
     } else {
         const float ai = p.a + p.e[w.row];
-        const uint32_t lo_box = box + kOrthBoxBytes / 2;
+        const uint32_t lo_box = box + kOrthSquareBytes;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const uint4 h = lds_v4(orth_piece64(box, lane, q)), l = lds_v4(orth_piece64(lo_box, lane, q));
@@ -339,18 +346,16 @@ __device__ __forceinline__ void orth_write_out(const OrthArgs& p, const OrthRows
 // D tiles = A B^T (Gram, Poly; both operands K-major rows) or A B (Apply, Final;
 // B read MN-major).  tm_a, tm_b: operands, boxes of 64 columns x the CTA's rows of
 // a K block (MN-major: x 64 rows).  For
-// the epilogue boxes of 32 rows x 64 columns (Gram, Poly) or 32 columns (Apply,
-// Final): tm_in, tm_lo what it reads (Poly: A0; Apply, Final: hi and lo), tm_out
+// the epilogue boxes of 32 rows x 32 columns: tm_in, tm_lo what it reads (Poly: A0; Apply, Final: hi and lo), tm_out
 // what it writes beside lo.
-// kBoxes: 2, or 4 (and a stage less) where the K loop is short: the epilogue then
-// reads two chunks ahead.
-template <int kMode, int kBN, bool kPair, int kBoxes>
-__global__ void __launch_bounds__(kOrthThreads, 1)
+template <int kMode, int kBN, bool kPair>
+__global__ void __launch_bounds__(kOrthProductThreads, 1)
 k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_lo,
                const __grid_constant__ CUtensorMap tm_out, OrthArgs p) {
     constexpr bool kSym = kMode == kOrthGram || kMode == kOrthPoly;
-    constexpr int kBM = kPair ? 256 : 128, kStages = kOrthStages<kBN, kPair, kBoxes>;
+    constexpr int kBM = kPair ? 256 : 128, kStages = kOrthStages<kBN, kPair, kSym>, kBoxes = kOrthBoxes;
+    constexpr uint32_t kBoxBytes = kOrthBoxBytes<kSym>;
     constexpr uint32_t kStageBytes = kOrthStageBytes<kBN, kPair>;
     extern __shared__ __align__(1024) unsigned char orth_smem_raw[];
     const uint32_t raw = smem_u32(orth_smem_raw);
@@ -359,8 +364,8 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
     const uint32_t full0 = bars, empty0 = bars + 8 * kStages;
     const uint32_t tfull0 = bars + 16 * kStages, tempty0 = tfull0 + 16;
     const uint32_t drain = tempty0 + 16;
-    const uint32_t in0 = drain + 8;   // 4 epilogue warps x kBoxes
-    const uint32_t slot = in0 + 32 * kBoxes;
+    const uint32_t in0 = drain + 8;   // the epilogue warps' boxes
+    const uint32_t slot = in0 + 8 * kOrthEpiWarps * kBoxes;
     unsigned char* slot_gen = orth_smem_raw + (slot - raw);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(slot_gen);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(slot_gen + 4);
@@ -377,10 +382,10 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull0 + 8 * a, 1);
-            mbar_init(tempty0 + 8 * a, kPair ? 8 : 4);   // one arrival per epilogue warp
+            mbar_init(tempty0 + 8 * a, (kPair ? 2 : 1) * kOrthEpiWarps);   // one arrival per epilogue warp
         }
         mbar_init(drain, 1);
-        for (int k = 0; k < 4 * kBoxes; ++k) mbar_init(in0 + 8 * k, 1);
+        for (int k = 0; k < kOrthEpiWarps * kBoxes; ++k) mbar_init(in0 + 8 * k, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_a);
@@ -507,15 +512,14 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
         }
         __syncwarp();
     } else {
-        // ---------------- epilogue: 32 rows a warp, 64 columns at a time
-        const int q = warp & 3;
+        // ---------------- epilogue: 32 rows and half of the columns a warp
+        const int q = warp & 3, e = warp - 2;   // tensor memory's lanes go by warp mod 4
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t tempty = kPair ? map_to_rank(tempty0, 0) : tempty0;
         const int64_t cols = kSym ? p.mp : p.np;
-        const uint32_t my_boxes = boxes + (uint32_t)q * kBoxes * kOrthBoxBytes, my_in = in0 + (uint32_t)q * 8 * kBoxes;
+        const uint32_t my_boxes = boxes + (uint32_t)e * kBoxes * kBoxBytes, my_in = in0 + (uint32_t)e * 8 * kBoxes;
         constexpr bool kReads = kMode != kOrthGram;
-        constexpr int kWide = kSym ? 64 : 32;   // columns of a chunk
-        constexpr int kAhead = kBoxes / 2;      // chunks read ahead
+        constexpr int kWide = 32;   // columns of a chunk
         int acc = 0, buf = 0;
         uint32_t acc_phase = 0, in_phase = 0, pending = 0;   // bit per box
         bool ok = true;
@@ -530,34 +534,33 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
             const bool mirror = kSym && n0 >= (int64_t)(w.mb + 1) * kBM;
             int chunks = o.i_warp < p.mp ? (int)((cols - n0) / kWide) : 0;   // cols and n0 are multiples of 64
             if (chunks > kBN / kWide) chunks = kBN / kWide;
+            const int part = (chunks + 1) / 2, c_from = e < 4 ? 0 : part, c_to = e < 4 ? part : chunks;
             auto fetch = [&](int c, int b) {   // lane 0: what chunk c reads
-                const uint32_t box = my_boxes + (uint32_t)b * kOrthBoxBytes, bar = my_in + 8 * b;
-                mbar_arrive_expect_tx(bar, kOrthBoxBytes);
+                const uint32_t box = my_boxes + (uint32_t)b * kBoxBytes, bar = my_in + 8 * b;
+                mbar_arrive_expect_tx(bar, kBoxBytes);
                 tma_load_2d(box, &tm_in, (int)n0 + kWide * c, y, bar);
-                if constexpr (!kSym) tma_load_2d(box + kOrthBoxBytes / 2, &tm_lo, (int)n0 + kWide * c, y, bar);
+                if constexpr (!kSym) tma_load_2d(box + kOrthSquareBytes, &tm_lo, (int)n0 + kWide * c, y, bar);
             };
             if (kReads) {
-                if (lane == 0 && chunks > 0) bulk_wait_read<0>();   // the stores out of the boxes have read them
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const int b = (buf + k) % kBoxes;
-                    if (k < chunks) {
-                        if (lane == 0) fetch(k, b);
-                        pending |= 1u << b;
+                if (c_from < c_to) {
+                    if (lane == 0) {
+                        bulk_wait_read<0>();   // the stores out of the boxes have read them
+                        fetch(c_from, buf);
                     }
+                    pending |= 1u << buf;
                 }
             }
             ok = __all_sync(0xffffffffu, orth_wait(tfull0 + 8 * acc, acc_phase, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            for (int c = 0; c < chunks; ++c) {
-                const uint32_t box = my_boxes + (uint32_t)buf * kOrthBoxBytes;
+            for (int c = c_from; c < c_to; ++c) {
+                const uint32_t box = my_boxes + (uint32_t)buf * kBoxBytes;
                 if (kReads) {
-                    if (c + kAhead < chunks) {
-                        const int b = (buf + kAhead) % kBoxes;
+                    if (c + 1 < c_to) {
+                        const int b = (buf + 1) % kBoxes;
                         if (lane == 0) {
-                            bulk_wait_read<kAhead - 1>();   // the store that last used this box
-                            fetch(c + kAhead, b);
+                            bulk_wait_read<0>();   // the store that last used this box
+                            fetch(c + 1, b);
                         }
                         pending |= 1u << b;
                     }
@@ -572,12 +575,9 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                 __syncwarp();
                 const int64_t c0 = n0 + kWide * c;
                 const bool diag = kSym && c0 < o.i_warp + 32 && o.i_warp < c0 + kWide;
-#pragma unroll
-                for (int h = 0; h < kWide / 32; ++h) {
-                    uint32_t r[32];
-                    tmem_ld32(lane_addr + (uint32_t)(acc * kBN + kWide * c + 32 * h), r);
-                    orth_epilogue<kMode>(p, o, diag, mirror, w.batch, c0 + 32 * h, box, lane, r);
-                }
+                uint32_t r[32];
+                tmem_ld32(lane_addr + (uint32_t)(acc * kBN + kWide * c), r);
+                orth_epilogue<kMode>(p, o, diag, mirror, w.batch, c0, box, lane, r);
                 if constexpr (kMode == kOrthFinal) {
                     if (!p.transposed) {
                         __syncwarp();
@@ -591,7 +591,7 @@ k_orth_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) {
                         tma_store_2d(&tm_out, (int)c0, y, box);
-                        if constexpr (!kSym) tma_store_2d(&tm_lo, (int)c0, y, box + kOrthBoxBytes / 2);
+                        if constexpr (!kSym) tma_store_2d(&tm_lo, (int)c0, y, box + kOrthSquareBytes);
                         bulk_commit_group();
                     }
                 }

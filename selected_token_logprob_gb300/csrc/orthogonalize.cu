@@ -79,11 +79,11 @@ struct OrthMaps {
     CUtensorMap a, b, b64, in, lo, out;   // operands (b64: b in boxes of 64 rows), the epilogue's
 };
 
-template <int kMode, int kBN, bool kPair, int kBoxes = 2>
+template <int kMode, int kBN, bool kPair>
 flp_status orth_launch(int dev, int fit, const OrthMaps& t, const flp::OrthArgs& p, cudaStream_t s) {
     static std::atomic<bool> ready[kMaxDevices];
-    const auto kern = flp::k_orth_product<kMode, kBN, kPair, kBoxes>;
-    constexpr size_t smem = flp::kOrthSmemBytes<kBN, kPair, kBoxes>;
+    const auto kern = flp::k_orth_product<kMode, kBN, kPair>;
+    constexpr size_t smem = flp::kOrthSmemBytes<kBN, kPair, kMode == flp::kOrthGram || kMode == flp::kOrthPoly>;
     static_assert(smem <= 232448, "shared memory per CTA");
     if (!ready[dev].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -93,7 +93,7 @@ flp_status orth_launch(int dev, int fit, const OrthMaps& t, const flp::OrthArgs&
     const int64_t ctas = (p.units < fit ? p.units : fit) * (kPair ? 2 : 1);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(flp::kOrthThreads);
+    cfg.blockDim = dim3(flp::kOrthProductThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -155,11 +155,11 @@ int orth_pairs(int dev) {
     static std::atomic<int> count[kMaxDevices];
     int c = count[dev].load(std::memory_order_acquire);
     if (c == 0) {
-        const auto kern = flp::k_orth_product<flp::kOrthGram, 256, true, 2>;
-        constexpr size_t smem = flp::kOrthSmemBytes<256, true, 2>;
+        const auto kern = flp::k_orth_product<flp::kOrthGram, 256, true>;
+        constexpr size_t smem = flp::kOrthSmemBytes<256, true, true>;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(flp::kOrthThreads);
+        cfg.blockDim = dim3(flp::kOrthProductThreads);
         cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -214,13 +214,7 @@ flp_status orth_product(int dev, int sms, int pairs, int64_t batch, const OrthMa
         }
     }
     shape(tiles[pick].bm, tiles[pick].bn);
-    if (pick == 0) {
-        // 8 x 1024 x 4096 (16 K blocks): 726 us with 2 boxes, 711 with 4; 4 x 2048 x 2048
-        // (32): 617 and 622
-        if constexpr (!kSym)
-            if (p.nkb <= 16) return orth_launch<kMode, 256, true, 4>(dev, pairs, t, p, s);
-        return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
-    }
+    if (pick == 0) return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
     if (pick == 1) return orth_launch<kMode, 128, false>(dev, sms, t, p, s);
     return orth_launch<kMode, 64, false>(dev, sms, t, p, s);
 }
@@ -392,9 +386,9 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     if ((st = orth_tmap(&ep_lo, lo, all_rows, l.np, 32, 32)) != FLP_OK) return st;
     if ((st = orth_tmap(&op_a0, ws + l.a0, all_rows, l.mp, 128)) != FLP_OK) return st;
     if ((st = orth_tmap(&op_a064, ws + l.a0, all_rows, l.mp, 64)) != FLP_OK) return st;
-    if ((st = orth_tmap(&ep_a0, ws + l.a0, all_rows, l.mp, 32)) != FLP_OK) return st;
+    if ((st = orth_tmap(&ep_a0, ws + l.a0, all_rows, l.mp, 32, 32)) != FLP_OK) return st;
     if ((st = orth_tmap(&op_b0, ws + l.b0, all_rows, l.mp, 128)) != FLP_OK) return st;
-    if ((st = orth_tmap(&ep_b0, ws + l.b0, all_rows, l.mp, 32)) != FLP_OK) return st;
+    if ((st = orth_tmap(&ep_b0, ws + l.b0, all_rows, l.mp, 32, 32)) != FLP_OK) return st;
 
     flp::OrthInput in{};
     in.x = x;

@@ -22,14 +22,24 @@
 // A and B are symmetric: only tiles on and above the diagonal are computed, and
 // each is written to both places.
 //
-// Each product is one launch of persistent CTAs (or CTA pairs) with six warps:
-// one TMA producer, one MMA issuer, four epilogue warps (one accumulator row a
-// thread).  The epilogue of a tile overlaps the next tile's MMAs; what it reads
-// beside the accumulators (X's hi and lo, or A0) comes by TMA into boxes of 32
-// rows x 64 columns a warp, which it rewrites in place and stores by TMA.
-// Every wait is bounded: a wait that runs out sets the error word and the CTA's
-// abort flag, the copies and MMAs in flight are waited for, TMEM is freed and
+// Each product is one launch: persistent CTAs or CTA pairs (k_orth_product), or,
+// where a product has fewer 128 x 128 tiles than the GPU has SMs, a cluster a tile
+// (k_orth_split); a matrix with a side of at most 128 takes one launch in all
+// (ortho_cluster.cuh).  The persistent form has ten warps: one TMA producer, one MMA
+// issuer, eight epilogue warps (one accumulator row a thread, half of a tile's
+// columns).  The epilogue of a tile overlaps the next tile's MMAs; what it reads
+// beside the accumulators (X's hi and lo, or A0) comes by TMA into boxes of 32 rows
+// x 32 columns a warp, which it rewrites in place and stores by TMA (by way of
+// registers and plain loads and stores: 78 instead of 65 us for Apply at 8 x 1024 x
+// 4096).  Every wait is bounded: a wait that runs out sets the error word and the
+// CTA's abort flag, the copies and MMAs in flight are waited for, TMEM is freed and
 // the kernel returns.
+//
+// What bounds it (4096 x 4096, 1025 us): the tensor cores and the copies that feed
+// them, 585 cycles a K block of a 256 x 256 tile (512 being the MMAs' own), in 2, 2
+// and 4 waves a step where 1.8, 1.8 and 3.4 would hold the work.  Cutting the K
+// blocks of all tiles into equal runs, one a pair, did not pay: the same 1046 us,
+// and 644 instead of 617 at 4 x 2048 x 2048.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -76,7 +76,7 @@ flp_status orth_tmap(CUtensorMap* map, const void* ptr, int64_t rows, int64_t co
 // A launch of one product: its kernel for this shape, once per device allowed
 // its shared memory.
 struct OrthMaps {
-    CUtensorMap a, b, b64, in, lo, out;   // operands (b64: b in boxes of 64 rows), the epilogue's
+    CUtensorMap a, b, in, lo, out;   // operands, what the epilogue reads and writes
 };
 
 template <int kMode, int kBN, bool kPair>
@@ -105,8 +105,7 @@ flp_status orth_launch(int dev, int fit, const OrthMaps& t, const flp::OrthArgs&
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kPair ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, t.a, kBN == 64 || kMode >= flp::kOrthApply ? t.b64 : t.b, t.in,
-                                             t.lo, t.out, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, t.a, t.b, t.in, t.lo, t.out, p);
     if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize product launch: %s", cudaGetErrorString(e));
     return FLP_OK;
 }
@@ -145,7 +144,7 @@ flp_status orth_split_launch(int dev, int split, const OrthMaps& t, const flp::O
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, t.a, kMode >= flp::kOrthApply ? t.b64 : t.b, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, t.a, t.b, p);
     if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize product launch: %s", cudaGetErrorString(e));
     return FLP_OK;
 }
@@ -198,25 +197,15 @@ flp_status orth_product(int dev, int sms, int pairs, int64_t batch, const OrthMa
         while (split < 4 && p.units * split * 2 <= sms && p.nkb >= 4) split *= 2;
         return orth_split_launch<kMode>(dev, split, t, p, s);
     }
-    // Cycles of a launch by tile: a K block takes its MMAs' time or the copies'
-    // turn-around over the stages, a tile some 5000 on top, a wave each.
-    struct Tile { int bm, bn, kblock; int64_t slots; };
-    const Tile tiles[] = {{256, 256, 540, pairs}, {128, 128, 420, sms}, {128, 64, 320, sms}};
-    int64_t best = -1;
-    int pick = 1;
-    for (int k = 0; k < 3; ++k) {
-        if (tiles[k].slots <= 0) continue;
-        const int64_t units = batch * orth_tiles(kSym, p.mp, cols, tiles[k].bm, tiles[k].bn);
-        const int64_t c = ceil_div(units, tiles[k].slots) * ((int64_t)p.nkb * tiles[k].kblock) + 5000;
-        if (best < 0 || c < best) {
-            best = c;
-            pick = k;
-        }
-    }
-    shape(tiles[pick].bm, tiles[pick].bn);
-    if (pick == 0) return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
-    if (pick == 1) return orth_launch<kMode, 128, false>(dev, sms, t, p, s);
-    return orth_launch<kMode, 64, false>(dev, sms, t, p, s);
+    // Else by the waves: 256 x 256 tiles a pair or 128 x 128 a CTA, a K block taking
+    // about 540 and 420 cycles (8 x 1024 x 4096: Gram's 80 pair tiles 68 us, its 288
+    // small ones 43; 4096 x 4096 in all 1064 and 1482 us).
+    const int64_t small = ceil_div(p.units, sms) * 420;
+    const int64_t wide = batch * orth_tiles(kSym, p.mp, cols, 256, 256);
+    if (pairs <= 0 || small <= ceil_div(wide, pairs) * 540)
+        return orth_launch<kMode, 128, false>(dev, sms, t, p, s);
+    shape(256, 256);
+    return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
 }
 
 // CTAs of the cluster that holds a matrix with m <= 128 in one launch (0: the
@@ -375,8 +364,8 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     __half* hi[2] = {reinterpret_cast<__half*>(ws + l.hi0), reinterpret_cast<__half*>(ws + l.hi1)};
     __half* lo = reinterpret_cast<__half*>(ws + l.lo);
 
-    // operands in boxes of 128 (and 64) rows, the epilogues' reads and writes of 32
-    CUtensorMap op_x[2], op_x64[2], op_a0, op_a064, op_b0, ep_x[2], ep_lo, ep_a0, ep_b0;
+    // operands in boxes of 128 rows (MN-major: 64), the epilogues' reads and writes of 32
+    CUtensorMap op_x[2], op_x64[2], op_a0, op_b0, ep_x[2], ep_lo, ep_a0, ep_b0;
     const int64_t all_rows = batch * l.mp;
     for (int k = 0; k < 2; ++k) {
         if ((st = orth_tmap(&op_x[k], hi[k], all_rows, l.np, 128)) != FLP_OK) return st;
@@ -385,7 +374,6 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     }
     if ((st = orth_tmap(&ep_lo, lo, all_rows, l.np, 32, 32)) != FLP_OK) return st;
     if ((st = orth_tmap(&op_a0, ws + l.a0, all_rows, l.mp, 128)) != FLP_OK) return st;
-    if ((st = orth_tmap(&op_a064, ws + l.a0, all_rows, l.mp, 64)) != FLP_OK) return st;
     if ((st = orth_tmap(&ep_a0, ws + l.a0, all_rows, l.mp, 32, 32)) != FLP_OK) return st;
     if ((st = orth_tmap(&op_b0, ws + l.b0, all_rows, l.mp, 128)) != FLP_OK) return st;
     if ((st = orth_tmap(&ep_b0, ws + l.b0, all_rows, l.mp, 32, 32)) != FLP_OK) return st;
@@ -449,12 +437,12 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
         p.x_hi = hi[cur];
         p.x_out = hi[cur ^ 1];
         p.mat_out = reinterpret_cast<__half*>(ws + l.a0);
-        OrthMaps t{op_x[cur], op_x[cur], op_x64[cur], ep_a0, ep_a0, ep_a0};   // Gram reads nothing beside its operands
+        OrthMaps t{op_x[cur], op_x[cur], ep_a0, ep_a0, ep_a0};   // Gram reads nothing beside its operands
         if ((st = orth_product<flp::kOrthGram>(dev, sms, pairs, batch, t, p, s)) != FLP_OK) return st;
         p.mat_out = reinterpret_cast<__half*>(ws + l.b0);
-        t = OrthMaps{op_a0, op_a0, op_a064, ep_a0, ep_a0, ep_b0};
+        t = OrthMaps{op_a0, op_a0, ep_a0, ep_a0, ep_b0};
         if ((st = orth_product<flp::kOrthPoly>(dev, sms, pairs, batch, t, p, s)) != FLP_OK) return st;
-        t = OrthMaps{op_b0, op_x[cur], op_x64[cur], ep_x[cur], ep_lo, ep_x[cur ^ 1]};
+        t = OrthMaps{op_b0, op_x64[cur], ep_x[cur], ep_lo, ep_x[cur ^ 1]};
         if (k + 1 < steps) st = orth_product<flp::kOrthApply>(dev, sms, pairs, batch, t, p, s);
         else st = orth_product<flp::kOrthFinal>(dev, sms, pairs, batch, t, p, s);
         if (st != FLP_OK) return st;

@@ -209,17 +209,25 @@ __device__ __forceinline__ void pref_run(const PrefArgs& a, int64_t w, int64_t w
 // a lane copies and reads back only its own tokens, so no barrier is needed).
 constexpr int kPrefStages = 2;
 constexpr uint32_t kPrefStageBytes = kPrefThreads * kPrefQuads * (16 + 16 + 4);
-__device__ __forceinline__ void pref_ring_issue(const PrefArgs& a, int64_t t0, uint32_t stage) {
+// logp and ref are read once: first out of the L2 cache, so that the mask stays for
+// the gradients' pass.
+__device__ __forceinline__ uint64_t pref_read_once() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void pref_ring_issue(const PrefArgs& a, int64_t t0, uint32_t stage, uint64_t once) {
     const int lane = threadIdx.x & 31;
     const float *p = a.logp + t0 + lane * 4, *q = a.ref + t0 + lane * 4;
     const uint8_t* m = a.mask + t0 + lane * 4;
 #pragma unroll
     for (int h = 0; h < kPrefQuads; ++h) {
         const uint32_t at = stage + (h * kPrefThreads + threadIdx.x) * 16;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(p + 128 * h) : "memory");
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(at), "l"(p + 128 * h), "l"(once)
+                     : "memory");
         if (a.ref)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + kPrefQuads * kPrefThreads * 16),
-                         "l"(q + 128 * h) : "memory");
+            asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
+                             at + kPrefQuads * kPrefThreads * 16), "l"(q + 128 * h), "l"(once) : "memory");
         if (a.mask)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
                              stage + kPrefQuads * kPrefThreads * 32 + (h * kPrefThreads + threadIdx.x) * 4),
@@ -256,10 +264,11 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, int64_t w, int64_t 
     if (c0 >= c1) return;
     const int64_t base = c0 * kPrefChunk, len = (c1 - c0) * kPrefChunk;
     const int64_t full = a.n / kPrefChunk;   // chunks before this are whole
+    const uint64_t once = pref_read_once();
     if constexpr (kRing) {
 #pragma unroll
         for (int k = 0; k < kPrefStages - 1; ++k) {
-            if (c0 + k < c1 && c0 + k < full) pref_ring_issue(a, base + k * kPrefChunk, ring + k * kPrefStageBytes);
+            if (c0 + k < c1 && c0 + k < full) pref_ring_issue(a, base + k * kPrefChunk, ring + k * kPrefStageBytes, once);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     }
@@ -271,7 +280,7 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, int64_t w, int64_t 
         if constexpr (kRing) {
             const int64_t ahead = c + kPrefStages - 1;
             const int into = stage == 0 ? kPrefStages - 1 : stage - 1;
-            if (ahead < c1 && ahead < full) pref_ring_issue(a, ahead * kPrefChunk, ring + into * kPrefStageBytes);
+            if (ahead < c1 && ahead < full) pref_ring_issue(a, ahead * kPrefChunk, ring + into * kPrefStageBytes, once);
             asm volatile("cp.async.commit_group;" ::: "memory");
             asm volatile("cp.async.wait_group %0;" ::"n"(kPrefStages - 1) : "memory");
             if (c < full) pref_ring_read(a, ring + stage * kPrefStageBytes, r);

@@ -675,7 +675,7 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
  * two FP16 numbers (22 bits) and the diagonals of A and b A + c A^2 in FP32, so
  * that out is within about 1e-3 (of its norm) of the result in 64 bits also
  * where G has few large singular values over a small floor.  The sum of squares
- * is FP32 within a row (entries between about 1e-19 and 1e17 in size).  A zero
+ * is FP32 (entries between about 1e-19 and 1e17 in size).  A zero
  * matrix gives zeros; an infinity or NaN makes its matrix NaN.  Deterministic:
  * equal calls give equal bits (the order of the sums over K depends on the
  * sizes and the batch).

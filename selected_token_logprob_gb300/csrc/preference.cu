@@ -11,16 +11,15 @@ namespace {
 
 // Byte offsets of the workspace's parts; false when they overflow.
 struct PrefLayout {
-    int64_t part_loss, part_live, slots, coef, total;
+    int64_t part_loss, slots, coef, total;
 };
 
 bool pref_layout(int64_t n, int64_t nseq, PrefLayout* l) {
     const int64_t nchunks = n / flp::kPrefChunk + (n % flp::kPrefChunk != 0);
     int64_t slots, b;
     if (__builtin_add_overflow(nchunks, nseq, &slots) || slots > INT64_MAX / 32) return false;
-    l->part_loss = 256;   // the ticket and 1 / D
-    l->part_live = l->part_loss + 8 * flp::kPrefPairCtas;
-    l->slots = l->part_live + 8 * flp::kPrefPairCtas;
+    l->part_loss = 256;   // the live pairs
+    l->slots = l->part_loss + 8 * flp::kPrefMaxCtas;
     l->coef = l->slots + 8 * slots;
     if (__builtin_add_overflow(l->coef, 4 * nseq + 255, &b)) return false;
     l->total = b / 256 * 256;
@@ -107,52 +106,48 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
     a.grad = grad;
     a.rewards = rewards;
     char* base = static_cast<char*>(workspace);
-    a.ticket = reinterpret_cast<unsigned*>(base);
-    a.inv_den = reinterpret_cast<float*>(base + 16);
+    a.live = reinterpret_cast<int*>(base);
     a.part_loss = reinterpret_cast<flp::PrefTwo*>(base + l.part_loss);
-    a.part_live = reinterpret_cast<int*>(base + l.part_live);
     a.slots = reinterpret_cast<flp::PrefSlot*>(base + l.slots);
     a.coef = reinterpret_cast<float*>(base + l.coef);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool vec = aligned16(logp) && aligned16(ref_logp) && aligned16(grad) &&
                      (reinterpret_cast<uintptr_t>(active_mask) & 3u) == 0;
-    // A batch that leaves a cluster's warps a few chunks and pairs each runs in
-    // one launch; above that the whole GPU's bandwidth is worth two more launches.
-    constexpr int64_t kClusterWarps = flp::kPrefClusterCtas * flp::kPrefClusterThreads / 32;
-    if (a.nchunks <= 8 * kClusterWarps && num_seqs <= 16 * kClusterWarps) {
-        (vec ? flp::k_pref_cluster<true> : flp::k_pref_cluster<false>)<<<flp::kPrefClusterCtas,
-                                                                         flp::kPrefClusterThreads, 0, s>>>(a);
-        return check_launch("preference loss");
-    }
-    // Token passes: a run of chunks per warp.
-    constexpr int kWarps = flp::kPrefThreads / 32;
-    const int64_t ctas = a.nchunks <= kWarps ? 1 : ceil_div(a.nchunks, kWarps);
-    auto token_grid = [&](int per_sm) { return (int)(ctas < (int64_t)sms * per_sm ? ctas : (int64_t)sms * per_sm); };
-    if (vec) {
-        constexpr int kRing = flp::kPrefStages * (int)flp::kPrefStageBytes;
-        static std::atomic<bool> ready[kMaxDevices];
-        if (!ready[dev].load(std::memory_order_acquire)) {
-            const cudaError_t e = cudaFuncSetAttribute(flp::k_pref_sums<true>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
-            if (e != cudaSuccess) return fail(FLP_ECUDA, "preference setup: %s", cudaGetErrorString(e));
-            ready[dev].store(true, std::memory_order_release);
-        }
-        flp::k_pref_sums<true><<<token_grid(flp::kPrefSumCtas), flp::kPrefThreads, kRing, s>>>(a);
-    } else {
-        flp::k_pref_sums<false><<<token_grid(flp::kPrefSumCtas), flp::kPrefThreads, 0, s>>>(a);
-    }
-    if ((st = check_launch("preference sums")) != FLP_OK) return st;
-    // 8 lanes per pair while a sequence has a few slots, a warp beyond that
+    // 8 lanes per pair while a sequence has a few slots, a warp beyond that (8192 pairs
+    // x 1024 tokens: 50 and 60 us; 501 x 5000: 22 and 21; 64 x 60000: 32 and 28)
     const bool narrow = a.nchunks <= 16 * num_seqs;
-    int64_t pgrid = ceil_div(num_seqs / 2, flp::kPrefThreads / (narrow ? 8 : 32));
-    pgrid = pgrid < 1 ? 1 : (pgrid > flp::kPrefPairCtas ? flp::kPrefPairCtas : pgrid);
-    if ((st = launch_dependent("preference pairs", narrow ? flp::k_pref_pairs<8> : flp::k_pref_pairs<32>, (int)pgrid,
-                               flp::kPrefThreads, (size_t)0, s, a)) != FLP_OK)
-        return st;
-    if (n == 0) return ok();
-    return launch_dependent("preference grad", vec ? flp::k_pref_grad<true> : flp::k_pref_grad<false>,
-                            token_grid(flp::kPrefGradCtas),
-                            flp::kPrefThreads, (size_t)0, s, a);
+    // A chunk a warp, a pair a group of lanes, up to the CTAs that can be resident.
+    constexpr int kRing = flp::kPrefStages * (int)flp::kPrefStageBytes;
+    const auto kern = vec ? flp::k_pref<true> : flp::k_pref<false>;
+    static std::atomic<int> fits[2][kMaxDevices];
+    int fit = fits[vec][dev].load(std::memory_order_acquire);
+    if (fit == 0) {
+        int per_sm = 0;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, flp::kPrefThreads, kRing);
+        if (e != cudaSuccess) return fail(FLP_ECUDA, "preference setup: %s", cudaGetErrorString(e));
+        if (per_sm < 1) return fail(FLP_ECUDA, "preference setup: device %d cannot hold the kernel", dev);
+        fit = per_sm * sms < flp::kPrefMaxCtas ? per_sm * sms : flp::kPrefMaxCtas;
+        fits[vec][dev].store(fit, std::memory_order_release);
+    }
+    const int64_t by_tokens = ceil_div(a.nchunks, flp::kPrefThreads / 32);
+    const int64_t by_pairs = ceil_div(num_seqs / 2, flp::kPrefThreads / (narrow ? 8 : 32));
+    int64_t ctas = by_tokens > by_pairs ? by_tokens : by_pairs;
+    ctas = ctas < 1 ? 1 : (ctas > fit ? fit : ctas);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(flp::kPrefThreads);
+    cfg.dynamicSmemBytes = kRing;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, narrow ? 1 : 0);
+    if (e != cudaSuccess) return fail(FLP_ECUDA, "preference launch: %s", cudaGetErrorString(e));
+    return ok();
 }
 
 }  // extern "C"

@@ -10,22 +10,30 @@
 // token) divided by their number D.  The gradient of token t of sequence s is
 // +-(dl/dh) / D, divided by n_s when averaging.
 //
-// Three phases.  Sums: the batch is cut into fixed chunks of 512 tokens; a warp
-// takes a run of consecutive chunks and writes, for every sequence that a chunk
-// meets, the sum and the active count into slot (chunk + sequence).  Along the
-// packed batch each next piece moves to the next chunk, the next sequence or
-// both, so slots never collide and a sequence's pieces lie side by side.  Pairs:
-// 8 (or 32) lanes per pair add both sides' slots in FP64 and form the loss and
-// the sequences' coefficients; the loss and D are folded in a fixed order.
-// Grad: the warps write their chunks' gradients.  A large batch runs them as
-// three dependent launches, a small one in a single cluster of 8 CTAs with
-// cluster barriers between them.  Nothing depends on timing or on the grid.
+// One cooperative launch, three phases with a barrier of the grid between them.
+// Sums: the batch is cut into fixed chunks of 512 tokens; a warp takes a run of
+// consecutive chunks and writes, for every sequence that a chunk meets, the sum and
+// the active count into slot (chunk + sequence).  Along the packed batch each next
+// piece moves to the next chunk, the next sequence or both, so slots never collide and
+// a sequence's pieces lie side by side.  Pairs: 8 (or 32) lanes per pair add both
+// sides' slots as two-float sums and form the loss and the sequences' coefficients;
+// the loss and D are folded in a fixed order.  Grad: the warps write their chunks'
+// gradients.  Nothing depends on timing.
 //
-// A run's cursor holds the bounds (and coefficients) of 32 sequences, one a
-// lane, so that a chunk reads no bounds from memory; the next chunk's tokens are
-// copied into shared memory while this one's are summed.
+// A run's window holds the bounds (and coefficients) of 31 sequences, one a lane, so
+// that a chunk reads no bounds from memory.  The whole warp takes a long piece, one
+// after the other; short ones (32 tokens at most) are taken by a lane each, all at
+// once, out of shared memory.  The next chunk's tokens are copied into shared memory
+// while this one's are summed.
+//
+// What bounds it: at 16.8 M tokens in 16384 sequences (218 MB in 50 us, 4.4 TB/s) the
+// sums 28 us, by instructions and memory alike, the pairs 7, a chain of latencies, the
+// gradients 16, out of L2; small batches take 13 us, latencies.  As three dependent
+// launches these took 49.5 and 11, but a caller's queue of calls was bound by the
+// launches (31 us a call on 2.5 M tokens, now 25).
 #pragma once
 
+#include <cooperative_groups.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -34,8 +42,12 @@ namespace flp {
 constexpr int kPrefChunk = 512;        // tokens per warp and step
 constexpr int kPrefQuads = kPrefChunk / 128;   // groups of four neighbouring tokens a lane holds of it
 constexpr int kPrefThreads = 256;
-constexpr int kPrefSumCtas = 3, kPrefGradCtas = 4;   // CTAs per SM of the token passes
-constexpr int kPrefPairCtas = 304;     // most CTAs of the pair kernel (the fold's shape)
+constexpr int kPrefCtas = 3;           // per SM
+constexpr int kPrefMaxCtas = 608;      // most CTAs of a launch
+// A window with at least kPrefBriefs pieces of at most kPrefShort tokens has them taken
+// by a lane each (8192 pairs x 4 tokens: 113 us by whole warps, now 21; taking every short
+// piece so, the odd cut end of a long sequence too, cost 3 us on long batches).
+constexpr int kPrefShort = 32, kPrefBriefs = 4;
 
 enum PrefKind { kPrefSigmoid = 0, kPrefHinge = 1, kPrefIpo = 2 };
 
@@ -75,15 +87,11 @@ struct PrefArgs {
     float target_hi, target_lo;   // 1 / (2 beta) as two floats
     float *loss, *grad, *rewards;
     // workspace
-    unsigned* ticket;
-    float* inv_den;
-    PrefTwo* part_loss;           // [kPrefPairCtas]
-    int* part_live;               // [kPrefPairCtas]
+    int* live;                    // live pairs
+    PrefTwo* part_loss;           // [kPrefMaxCtas]
     PrefSlot* slots;              // [nchunks + nseq]
     float* coef;                  // [nseq] dl/dr before the division by D
 };
-
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Sequence bounds, clamped to the batch.
 __device__ __forceinline__ int64_t pref_cu(const PrefArgs& a, int64_t i) {
@@ -108,40 +116,53 @@ __device__ __forceinline__ int64_t pref_first_seq(const PrefArgs& a, int64_t pos
     return lo;
 }
 
-// Walks the sequences that a run of tokens [base, base + len) meets.  Bounds are
-// held relative to base, clamped to [-1, len + 1].
-struct PrefCursor {
-    int64_t s0;       // sequence of lane 0's bound
+// The bounds of the sequences s0 .. s0 + 30 that a run of tokens [base, base + len)
+// meets, relative to base and clamped to [-1, len + 1].
+struct PrefWindow {
+    int64_t s0;
     int32_t bound;    // lane l: start of sequence s0 + l
     float coef;       // lane l: coefficient of sequence s0 + l (grad phase)
-    int k;            // current sequence - s0
 };
 template <bool kCoef>
 __device__ __forceinline__ void pref_window(const PrefArgs& a, int64_t base, int64_t len, int64_t s, float inv_den,
-                                            PrefCursor& c) {
+                                            PrefWindow& c) {
     const int lane = threadIdx.x & 31;
     const int64_t i = s + lane;
-    int64_t v = (i <= a.nseq ? pref_cu(a, i) : a.n) - base;
+    int64_t v = (a.nseq > 0 && i <= a.nseq ? pref_cu(a, i) : a.n) - base;   // no sequences: cu may be null
     v = v < -1 ? -1 : (v > len + 1 ? len + 1 : v);
     c.s0 = s;
     c.bound = (int32_t)v;
     c.coef = kCoef && i < a.nseq ? __ldcg(a.coef + i) * inv_den : 0.f;
-    c.k = 0;
 }
-// Calls piece(sequence, lo, hi, coefficient) for every sequence with tokens in the chunk
-// [t, t + size) of the run, lo and hi relative to the chunk; advances the cursor.
-template <bool kCoef, class F>
-__device__ __forceinline__ void pref_walk(const PrefArgs& a, int64_t base, int64_t len, float inv_den, PrefCursor& c,
-                                          int32_t t, int32_t size, F piece) {
-    while (c.s0 + c.k < a.nseq) {
-        if (c.k == 31) pref_window<kCoef>(a, base, len, c.s0 + c.k, inv_den, c);
-        const int32_t b = __shfl_sync(0xffffffffu, c.bound, c.k), e = __shfl_sync(0xffffffffu, c.bound, c.k + 1);
-        if (b >= t + size) break;
-        const int32_t lo = b > t ? b - t : 0, hi = e < t + size ? e - t : size;
-        const float g = kCoef ? __shfl_sync(0xffffffffu, c.coef, c.k) : 0.f;
-        if (hi > lo) piece(c.s0 + c.k, lo, hi, g);
-        if (e > t + size) break;   // goes on in the next chunk
-        ++c.k;
+// The pieces of the chunk [t, t + kPrefChunk) of the run, bounds relative to the chunk:
+// every lane with a short one calls brief(sequence, lo, hi, coefficient) at the same
+// time, the whole warp calls piece(sequence, lo, hi, coefficient) for every long one.
+// `any_brief` runs in the whole warp before the lanes' calls.
+template <bool kCoef, class A, class B, class F>
+__device__ __forceinline__ void pref_walk(const PrefArgs& a, int64_t base, int64_t len, float inv_den, PrefWindow& c,
+                                          int32_t t, A any_brief, B brief, F piece) {
+    const int lane = threadIdx.x & 31;
+    for (;;) {
+        const int32_t end = __shfl_down_sync(0xffffffffu, c.bound, 1);
+        const int32_t lo = c.bound > t ? c.bound - t : 0, hi = end < t + kPrefChunk ? end - t : kPrefChunk;
+        const bool real = lane < 31 && c.s0 + lane < a.nseq && hi > lo;
+        uint32_t left = __ballot_sync(0xffffffffu, real);
+        const uint32_t briefs = __ballot_sync(0xffffffffu, real && hi - lo <= kPrefShort);
+        if (__popc(briefs) >= kPrefBriefs) {
+            any_brief();
+            if ((briefs >> lane) & 1u) brief(c.s0 + lane, lo, hi, c.coef);
+            __syncwarp();
+            left &= ~briefs;
+        }
+        for (; left != 0; left &= left - 1) {
+            const int k = __ffs(left) - 1;
+            piece(c.s0 + k, __shfl_sync(0xffffffffu, lo, k), __shfl_sync(0xffffffffu, hi, k),
+                  kCoef ? __shfl_sync(0xffffffffu, c.coef, k) : 0.f);
+        }
+        // on to the next window while this one ends inside the chunk
+        const int32_t last = __shfl_sync(0xffffffffu, c.bound, 31);
+        if (last >= t + kPrefChunk || c.s0 + 31 >= a.nseq) break;
+        pref_window<kCoef>(a, base, len, c.s0 + 31, inv_den, c);
     }
 }
 
@@ -172,31 +193,19 @@ __device__ __forceinline__ void pref_mask(const PrefArgs& a, int64_t t0, uint32_
         }
     }
 }
-template <bool kVec>
 __device__ __forceinline__ void pref_tokens(const float* x, int64_t t0, int64_t n, float (&v)[4 * kPrefQuads]) {
     const int64_t i0 = t0 + (threadIdx.x & 31) * 4;
-    if (kVec && t0 + kPrefChunk <= n) {
 #pragma unroll
-        for (int h = 0; h < kPrefQuads; ++h) {
-            const float4 q = __ldcs(reinterpret_cast<const float4*>(x + i0) + 32 * h);
-            v[4 * h] = q.x;
-            v[4 * h + 1] = q.y;
-            v[4 * h + 2] = q.z;
-            v[4 * h + 3] = q.w;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4 * kPrefQuads; ++j) {
-            const int64_t i = i0 + (j >> 2) * 128 + (j & 3);
-            v[j] = i < n ? __ldcs(x + i) : 0.f;
-        }
+    for (int j = 0; j < 4 * kPrefQuads; ++j) {
+        const int64_t i = i0 + (j >> 2) * 128 + (j & 3);
+        v[j] = i < n ? __ldcs(x + i) : 0.f;
     }
 }
-template <bool kVec>
+// A chunk that the ring does not hold: the batch's last, or any of unaligned arrays.
 __device__ __forceinline__ void pref_load(const PrefArgs& a, int64_t t0, PrefRaw& r) {
-    pref_tokens<kVec>(a.logp, t0, a.n, r.p);
-    if (a.ref) pref_tokens<kVec>(a.ref, t0, a.n, r.q);
-    pref_mask<kVec>(a, t0, r.m);
+    pref_tokens(a.logp, t0, a.n, r.p);
+    if (a.ref) pref_tokens(a.ref, t0, a.n, r.q);
+    pref_mask<false>(a, t0, r.m);
 }
 
 // Chunks [c0, c1) of warp `w` of `warps`.
@@ -255,40 +264,50 @@ __device__ __forceinline__ void pref_ring_read(const PrefArgs& a, uint32_t stage
 __device__ __forceinline__ int pref_bytes_set(uint32_t m) {
     return __popc((m | ((m & 0x7f7f7f7fu) + 0x7f7f7f7fu)) & 0x80808080u);
 }
+// Addresses in a stage of the warp's token q of a chunk (its value) and of its mask byte.
+__device__ __forceinline__ uint32_t pref_token_at(uint32_t stage, int q) {
+    return stage + ((q >> 7) * kPrefThreads + (threadIdx.x & ~31u) + ((q >> 2) & 31)) * 16 + (q & 3) * 4;
+}
+__device__ __forceinline__ uint32_t pref_mask_at(uint32_t stage, int q) {
+    return stage + kPrefQuads * kPrefThreads * 32 + ((q >> 7) * kPrefThreads + (threadIdx.x & ~31u) + ((q >> 2) & 31)) * 4 +
+           (q & 3);
+}
+// This lane's tokens to the stage, at their places.
+__device__ __forceinline__ void pref_stage_tokens(uint32_t stage, const float (&v)[4 * kPrefQuads]) {
+#pragma unroll
+    for (int h = 0; h < kPrefQuads; ++h)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + (h * kPrefThreads + threadIdx.x) * 16),
+                     "f"(v[4 * h]), "f"(v[4 * h + 1]), "f"(v[4 * h + 2]), "f"(v[4 * h + 3]) : "memory");
+}
 
-template <bool kVec, bool kRing>
+template <bool kVec>
 __device__ __forceinline__ void pref_sums(const PrefArgs& a, int64_t w, int64_t warps, uint32_t ring) {
     const int lane = threadIdx.x & 31;
     int64_t c0, c1;
     pref_run(a, w, warps, c0, c1);
     if (c0 >= c1) return;
     const int64_t base = c0 * kPrefChunk, len = (c1 - c0) * kPrefChunk;
-    const int64_t full = a.n / kPrefChunk;   // chunks before this are whole
+    const int64_t full = kVec ? a.n / kPrefChunk : 0;   // chunks before this are whole and copied ahead
     const uint64_t once = pref_read_once();
-    if constexpr (kRing) {
 #pragma unroll
-        for (int k = 0; k < kPrefStages - 1; ++k) {
-            if (c0 + k < c1 && c0 + k < full) pref_ring_issue(a, base + k * kPrefChunk, ring + k * kPrefStageBytes, once);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
+    for (int k = 0; k < kPrefStages - 1; ++k) {
+        if (c0 + k < c1 && c0 + k < full) pref_ring_issue(a, base + k * kPrefChunk, ring + k * kPrefStageBytes, once);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    PrefCursor cur;
+    PrefWindow cur;
     pref_window<false>(a, base, len, pref_first_seq(a, base), 0.f, cur);
     int stage = 0;
     for (int64_t c = c0; c < c1; ++c) {
         PrefRaw r;
-        if constexpr (kRing) {
-            const int64_t ahead = c + kPrefStages - 1;
-            const int into = stage == 0 ? kPrefStages - 1 : stage - 1;
-            if (ahead < c1 && ahead < full) pref_ring_issue(a, ahead * kPrefChunk, ring + into * kPrefStageBytes, once);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            asm volatile("cp.async.wait_group %0;" ::"n"(kPrefStages - 1) : "memory");
-            if (c < full) pref_ring_read(a, ring + stage * kPrefStageBytes, r);
-            else pref_load<false>(a, c * kPrefChunk, r);
-            stage = stage == kPrefStages - 1 ? 0 : stage + 1;
-        } else {
-            pref_load<kVec>(a, c * kPrefChunk, r);
-        }
+        const int64_t ahead = c + kPrefStages - 1;
+        const int into = stage == 0 ? kPrefStages - 1 : stage - 1;
+        if (ahead < c1 && ahead < full) pref_ring_issue(a, ahead * kPrefChunk, ring + into * kPrefStageBytes, once);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kPrefStages - 1) : "memory");
+        const uint32_t slot = ring + stage * kPrefStageBytes;
+        if (c < full) pref_ring_read(a, slot, r);
+        else pref_load(a, c * kPrefChunk, r);
+        stage = stage == kPrefStages - 1 ? 0 : stage + 1;
         // a masked value is not used
         float v[4 * kPrefQuads], quad[kPrefQuads];
 #pragma unroll
@@ -298,35 +317,67 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, int64_t w, int64_t 
                 v[j] = pref_active(r.m, j) ? (a.ref ? r.p[j] - r.q[j] : r.p[j]) : 0.f;
             quad[h] = (v[4 * h] + v[4 * h + 1]) + (v[4 * h + 2] + v[4 * h + 3]);
         }
-        pref_walk<false>(a, base, len, 0.f, cur, (int32_t)((c - c0) * kPrefChunk), kPrefChunk,
-                         [&](int64_t s, int32_t lo, int32_t hi, float) {
-            float sum = 0.f;
-            int cnt = 0;
+        bool staged = false;
+        pref_walk<false>(
+            a, base, len, 0.f, cur, (int32_t)((c - c0) * kPrefChunk),
+            [&] {
+                if (staged) return;
+                staged = true;
+                pref_stage_tokens(slot, v);
 #pragma unroll
-            for (int h = 0; h < kPrefQuads; ++h) {
-                const int q = h * 128 + lane * 4;
-                if (q >= lo && q + 4 <= hi) {
-                    sum += quad[h];
-                    cnt += pref_bytes_set(r.m[h]);
-                } else if (q + 4 > lo && q < hi) {   // a bound inside the quad: one lane or two
+                for (int h = 0; h < kPrefQuads; ++h)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + kPrefQuads * kPrefThreads * 32 +
+                                                                 (h * kPrefThreads + threadIdx.x) * 4),
+                                 "r"(r.m[h]) : "memory");
+                __syncwarp();
+            },
+            [&](int64_t s, int32_t lo, int32_t hi, float) {
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                int cnt = 0;
+                for (int q = lo; q < hi; q += 4) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (q + j >= lo && q + j < hi) {
-                            sum += v[4 * h + j];
-                            cnt += pref_active(r.m, 4 * h + j) ? 1 : 0;
+                    for (int j = 0; j < 4; ++j) {
+                        if (q + j < hi) {
+                            float x;
+                            unsigned short m;
+                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(pref_token_at(slot, q + j)) : "memory");
+                            asm volatile("ld.shared.u8 %0, [%1];" : "=h"(m) : "r"(pref_mask_at(slot, q + j)) : "memory");
+                            part[j] += x;
+                            cnt += m != 0 ? 1 : 0;
                         }
+                    }
                 }
-            }
+                a.slots[c + s] = PrefSlot{(part[0] + part[1]) + (part[2] + part[3]), cnt};
+            },
+            [&](int64_t s, int32_t lo, int32_t hi, float) {
+                float sum = 0.f;
+                int cnt = 0;
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            cnt = __reduce_add_sync(0xffffffffu, cnt);
-            if (lane == 0) a.slots[c + s] = PrefSlot{sum, cnt};
-        });
+                for (int h = 0; h < kPrefQuads; ++h) {
+                    const int q = h * 128 + lane * 4;
+                    if (q >= lo && q + 4 <= hi) {
+                        sum += quad[h];
+                        cnt += pref_bytes_set(r.m[h]);
+                    } else if (q + 4 > lo && q < hi) {   // a bound inside the quad: one lane or two
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (q + j >= lo && q + j < hi) {
+                                sum += v[4 * h + j];
+                                cnt += pref_active(r.m, 4 * h + j) ? 1 : 0;
+                            }
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                cnt = __reduce_add_sync(0xffffffffu, cnt);
+                if (lane == 0) a.slots[c + s] = PrefSlot{sum, cnt};
+            });
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <int kLanes>
-__device__ __forceinline__ int pref_group_sum(int v) {
+template <int kLanes, class T>
+__device__ __forceinline__ T pref_group_sum(T v) {
 #pragma unroll
     for (int o = kLanes / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
@@ -342,10 +393,11 @@ __device__ __forceinline__ PrefTwo pref_group_sum(PrefTwo v) {
     return v;
 }
 
-// This lane's share of the sum and active tokens of the sequence [b, e).
+// This lane's share of the sum and active tokens (a sequence may have more than 2^31)
+// of the sequence [b, e).
 template <int kLanes>
 __device__ __forceinline__ void pref_sequence(const PrefArgs& a, int64_t s, int64_t b, int64_t e, PrefTwo& sum,
-                                              int& cnt) {
+                                              int64_t& cnt) {
     sum = {0.f, 0.f};
     cnt = 0;
     if (e > b) {
@@ -372,7 +424,7 @@ __device__ __forceinline__ void pref_pairs(const PrefArgs& a, int64_t first, int
         const int64_t sc = a.halves ? p : 2 * p, sj = a.halves ? p + pairs : 2 * p + 1;
         const int64_t bc = pref_cu(a, sc), ec = pref_cu(a, sc + 1), bj = pref_cu(a, sj), ej = pref_cu(a, sj + 1);
         PrefTwo rc, rj;
-        int nc, nj;
+        int64_t nc, nj;
         pref_sequence<kLanes>(a, sc, bc, ec, rc, nc);
         pref_sequence<kLanes>(a, sj, bj, ej, rj, nj);
         rc = pref_settle(pref_group_sum<kLanes>(rc));
@@ -449,20 +501,20 @@ __device__ __forceinline__ float pref_loss(const PrefArgs& a, PrefTwo loss, int 
 // The gradients of warp w's chunks; `wait` returns 1 / D once it and the
 // coefficients are there.
 template <bool kVec, class F>
-__device__ __forceinline__ void pref_grad(const PrefArgs& a, int64_t w, int64_t warps, F wait) {
+__device__ __forceinline__ void pref_grad(const PrefArgs& a, int64_t w, int64_t warps, uint32_t slot, F wait) {
     const int lane = threadIdx.x & 31;
     int64_t c0, c1;
     pref_run(a, w, warps, c0, c1);
-    if (c0 >= c1) {
-        wait();
-        return;
-    }
     const int64_t base = c0 * kPrefChunk, len = (c1 - c0) * kPrefChunk;
     uint32_t next[kPrefQuads];
-    pref_mask<kVec>(a, base, next);
-    const int64_t s = pref_first_seq(a, base);
+    int64_t s = 0;
+    if (c0 < c1) {
+        pref_mask<kVec>(a, base, next);
+        s = pref_first_seq(a, base);
+    }
     const float inv_den = wait();
-    PrefCursor cur;
+    if (c0 >= c1) return;
+    PrefWindow cur;
     pref_window<true>(a, base, len, s, inv_den, cur);
     for (int64_t c = c0; c < c1; ++c) {
         const int64_t t0 = c * kPrefChunk;
@@ -471,20 +523,45 @@ __device__ __forceinline__ void pref_grad(const PrefArgs& a, int64_t w, int64_t 
         for (int h = 0; h < kPrefQuads; ++h) m[h] = next[h];
         if (c + 1 < c1) pref_mask<kVec>(a, t0 + kPrefChunk, next);
         float v[4 * kPrefQuads] = {};
-        pref_walk<true>(a, base, len, inv_den, cur, (int32_t)((c - c0) * kPrefChunk), kPrefChunk,
-                        [&](int64_t, int32_t lo, int32_t hi, float g) {
+        bool staged = false;
+        pref_walk<true>(
+            a, base, len, inv_den, cur, (int32_t)((c - c0) * kPrefChunk),
+            [&] {
+                if (staged) return;
+                staged = true;
+                const float zeros[4 * kPrefQuads] = {};
+                pref_stage_tokens(slot, zeros);
+                __syncwarp();
+            },
+            [&](int64_t, int32_t lo, int32_t hi, float g) {
+                for (int q = lo; q < hi; ++q)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(pref_token_at(slot, q)), "f"(g) : "memory");
+            },
+            [&](int64_t, int32_t lo, int32_t hi, float g) {
+#pragma unroll
+                for (int h = 0; h < kPrefQuads; ++h) {
+                    const int q = h * 128 + lane * 4;
+                    if (q >= lo && q + 4 <= hi) {
+                        v[4 * h] = v[4 * h + 1] = v[4 * h + 2] = v[4 * h + 3] = g;
+                    } else if (q + 4 > lo && q < hi) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (q + j >= lo && q + j < hi) v[4 * h + j] = g;
+                    }
+                }
+            });
+        if (staged) {   // a token is in a short piece, a long one or none
 #pragma unroll
             for (int h = 0; h < kPrefQuads; ++h) {
-                const int q = h * 128 + lane * 4;
-                if (q >= lo && q + 4 <= hi) {
-                    v[4 * h] = v[4 * h + 1] = v[4 * h + 2] = v[4 * h + 3] = g;
-                } else if (q + 4 > lo && q < hi) {
+                float x[4];
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                             : "r"(slot + (h * kPrefThreads + threadIdx.x) * 16) : "memory");
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (q + j >= lo && q + j < hi) v[4 * h + j] = g;
-                }
+                for (int j = 0; j < 4; ++j) v[4 * h + j] += x[j];
             }
-        });
+            __syncwarp();
+        }
 #pragma unroll
         for (int j = 0; j < 4 * kPrefQuads; ++j) v[j] = pref_active(m, j) ? v[j] : 0.f;
         const int64_t i0 = t0 + lane * 4;
@@ -503,103 +580,46 @@ __device__ __forceinline__ void pref_grad(const PrefArgs& a, int64_t w, int64_t 
     }
 }
 
-// ---------------------------------------------------------------- three launches
-
 template <bool kVec>
-__global__ void __launch_bounds__(kPrefThreads, kPrefSumCtas)
-k_pref_sums(PrefArgs a) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-    extern __shared__ __align__(16) unsigned char pref_smem[];
-    pref_sums<kVec, kVec>(a, (int64_t)blockIdx.x * (kPrefThreads / 32) + (threadIdx.x >> 5),
-                          (int64_t)gridDim.x * (kPrefThreads / 32), (uint32_t)__cvta_generic_to_shared(pref_smem));
-}
-
-template <int kLanes>
-__global__ void __launch_bounds__(kPrefThreads)
-k_pref_pairs(PrefArgs a) {
+__global__ void __launch_bounds__(kPrefThreads, kPrefCtas)
+k_pref(PrefArgs a, int narrow) {
     __shared__ PrefTwo sl[kPrefThreads / 32];
     __shared__ int sk[kPrefThreads / 32];
-    __shared__ bool s_last;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    grid_dep_wait();
-    constexpr int kGroups = kPrefThreads / kLanes;
+    extern __shared__ __align__(16) unsigned char pref_smem[];
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(pref_smem);
+    const auto grid = cooperative_groups::this_grid();
+    const int64_t w = (int64_t)blockIdx.x * (kPrefThreads / 32) + (threadIdx.x >> 5);
+    const int64_t warps = (int64_t)gridDim.x * (kPrefThreads / 32);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.live = 0;
+    pref_sums<kVec>(a, w, warps, ring);
+    grid.sync();
     PrefTwo l;
     int k;
-    pref_pairs<kLanes>(a, (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes, (int64_t)gridDim.x * kGroups, l, k);
+    if (narrow) {
+        constexpr int kGroups = kPrefThreads / 8;
+        pref_pairs<8>(a, (int64_t)blockIdx.x * kGroups + threadIdx.x / 8, (int64_t)gridDim.x * kGroups, l, k);
+    } else {
+        pref_pairs<32>(a, w, warps, l, k);
+    }
     pref_cta_sum<kPrefThreads>(l, k, sl, sk);
     if (threadIdx.x == 0) {
         a.part_loss[blockIdx.x] = l;
-        a.part_live[blockIdx.x] = k;
-        __threadfence();
-        s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
-        __threadfence();
+        if (k > 0) atomicAdd(a.live, k);   // whole numbers: any order gives the same sum
     }
-    __syncthreads();
-    if (!s_last) return;
-    // the last CTA: fold in an order fixed by the grid
-    l = {0.f, 0.f};
-    k = 0;
-    for (int i = threadIdx.x; i < (int)gridDim.x; i += kPrefThreads) {
-        const float2 q = __ldcg(reinterpret_cast<const float2*>(a.part_loss + i));
-        l = pref_add(l, PrefTwo{q.x, q.y});
-        k += __ldcg(a.part_live + i);
-    }
-    pref_cta_sum<kPrefThreads>(l, k, sl, sk);
-    if (threadIdx.x == 0) {
-        *a.inv_den = pref_inv_den(a, k);
-        *a.loss = pref_loss(a, l, k);
-    }
-}
-
-template <bool kVec>
-__global__ void __launch_bounds__(kPrefThreads, kPrefGradCtas)
-k_pref_grad(PrefArgs a) {
-    pref_grad<kVec>(a, (int64_t)blockIdx.x * (kPrefThreads / 32) + (threadIdx.x >> 5),
-                    (int64_t)gridDim.x * (kPrefThreads / 32), [&] {
-        grid_dep_wait();
-        return __ldcg(a.inv_den);
+    pref_grad<kVec>(a, w, warps, ring, [&] {
+        grid.sync();
+        return pref_inv_den(a, __ldcg(a.live));
     });
-}
-
-// ---------------------------------------------------------------- one cluster
-
-constexpr int kPrefClusterCtas = 8, kPrefClusterThreads = 512;
-
-__device__ __forceinline__ void pref_cluster_sync() {
-    __threadfence();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-template <bool kVec>
-__global__ void __cluster_dims__(kPrefClusterCtas, 1, 1) __launch_bounds__(kPrefClusterThreads)
-k_pref_cluster(PrefArgs a) {
-    constexpr int kWarps = kPrefClusterThreads / 32, kGroups = kPrefClusterThreads / 8;
-    __shared__ PrefTwo sl[kWarps];
-    __shared__ int sk[kWarps];
-    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * kWarps;
-    pref_sums<kVec, false>(a, w, warps, 0);
-    pref_cluster_sync();
-    PrefTwo l;
-    int k;
-    pref_pairs<8>(a, (int64_t)blockIdx.x * kGroups + threadIdx.x / 8, (int64_t)gridDim.x * kGroups, l, k);
-    pref_cta_sum<kPrefClusterThreads>(l, k, sl, sk);
-    if (threadIdx.x == 0) {
-        a.part_loss[blockIdx.x] = l;
-        a.part_live[blockIdx.x] = k;
+    if (blockIdx.x == gridDim.x - 1) {   // the loss, in an order fixed by the grid
+        l = {0.f, 0.f};
+        for (int i = threadIdx.x; i < (int)gridDim.x; i += kPrefThreads) {
+            const float2 q = __ldcg(reinterpret_cast<const float2*>(a.part_loss + i));
+            l = pref_add(l, PrefTwo{q.x, q.y});
+        }
+        k = 0;
+        pref_cta_sum<kPrefThreads>(l, k, sl, sk);
+        if (threadIdx.x == 0) *a.loss = pref_loss(a, l, __ldcg(a.live));
     }
-    pref_cluster_sync();
-    l = {0.f, 0.f};
-    k = 0;
-#pragma unroll
-    for (int i = 0; i < kPrefClusterCtas; ++i) {
-        const float2 q = __ldcg(reinterpret_cast<const float2*>(a.part_loss + i));
-        l = pref_add(l, PrefTwo{q.x, q.y});
-        k += __ldcg(a.part_live + i);
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.loss = pref_loss(a, l, k);
-    const float inv_den = pref_inv_den(a, k);
-    pref_grad<kVec>(a, w, warps, [&] { return inv_den; });
 }
 
 }  // namespace flp

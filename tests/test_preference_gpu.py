@@ -1,8 +1,8 @@
 """GPU tests of the preference loss against plain formulas in 64 bits.
 
-Tolerances, u = 2^-24.  A sequence's sum over 256-token chunks rounds each
-difference once and adds at most 8 + 5 times in FP32 (the rest is FP64), so
-its log-ratio is within e_s = 16 u sum|logp - ref| (/ n_s when averaging) and
+Tolerances, u = 2^-24.  A sequence's sum over 512-token chunks rounds each
+difference once and adds at most 2 + 4 + 5 times in FP32 (the rest is a sum of two
+floats), so its log-ratio is within e_s = 16 u sum|logp - ref| (/ n_s when averaging) and
 h within e = e_c + e_j.  u = beta h - margin is rounded once.
   rewards |err| <= beta e_s + u |reward|
   pair    sigmoid, hinge: beta e + 8 u (1 + |u| + l); ipo: (2 |t| + e) e + 4 u l
@@ -290,6 +290,52 @@ def test_batch_larger_than_one_wave():
     assert (rewards.double() - 0.1 * torch.stack([r[0::2], r[1::2]], 1)).abs().max() <= 1e-4
     dr = torch.stack([2 * t, -2 * t], 1).reshape(-1) / live.sum()
     assert (grad.double() - torch.repeat_interleave(dr, lens)).abs().max() <= 1e-4 * dr.abs().max()
+
+
+def test_tokens_without_sequences():
+    """No sequences: cu_seqlens and rewards may be null at the C entry."""
+    n = 1500
+    logp, grad, loss = torch.zeros(n, device=DEV), torch.full((n,), 7.0, device=DEV), torch.full((1,), 7.0, device=DEV)
+    size = flp.logp_preference_loss_workspace_size(n, 0)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    st = flp._lib.load().logp_preference_loss(logp.data_ptr(), None, None, None, 0, n, 0, 0, 0, 0.1, 0.0, 0.0, 0.0,
+                                              ws.data_ptr(), size, loss.data_ptr(), grad.data_ptr(), None,
+                                              torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert float(loss) == 0 and torch.count_nonzero(grad) == 0
+
+
+@pytest.mark.parametrize("mean", [1, 3, 9, 31, 40, 70])
+def test_many_short_sequences(mean):
+    rng = np.random.default_rng(mean)
+    lens = [int(v) for v in rng.integers(0, 2 * mean + 1, 700)] + [2000, 5, 0, 33]
+    logp, ref, mask, cu = _case(lens, 40 + mean)
+    _check(*_both(logp, ref, mask, cu))
+    logp, ref, _, cu = _case(lens, 50 + mean, junk=False)
+    _check(*_both(logp, ref, None, cu, average=True, kind="ipo", layout="halves"))
+
+
+def test_one_sequence_of_more_than_2_31_tokens():
+    """Token offsets and a sequence's count past 32 bits.  The chosen answer's
+    logp is -2^-10 everywhere and the rejected one's -2^-9 (exact in every
+    partial sum up to the chunks'), so h = 2^-10 up to the mean's rounding."""
+    long, short = (1 << 31) + 777, 1000
+    n = long + short
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of free device memory")
+    logp = torch.full((n,), -2.0 ** -10, device=DEV)
+    logp[long:] = -2.0 ** -9
+    cu = torch.tensor([0, long, n], device=DEV)
+    loss, grad, rewards = flp.logp_preference_loss(logp, cu, beta=0.5, average=True)
+    u = 0.5 * 2.0 ** -10
+    dh = -0.5 / (1 + math.exp(u))
+    assert abs(float(loss) - math.log1p(math.exp(-u))) < 1e-6
+    assert rewards[0].tolist() == pytest.approx([-u, -2 * u], rel=1e-6)
+    at = torch.tensor([0, 12345, (1 << 31) - 1, 1 << 31, long - 1], device=DEV)
+    assert grad[at].tolist() == pytest.approx([dh / long] * 5, rel=1e-6)
+    assert grad[long:].tolist() == pytest.approx([-dh / short] * short, rel=1e-6)
+    del logp, grad
+    torch.cuda.empty_cache()
 
 
 def test_refusals():

@@ -140,7 +140,7 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
         return a.mean ? launch_bwd_any<T, G, true>(a, s, parts) : launch_bwd_any<T, G, false>(a, s, parts);
     flp_status st;
     if ((st = norm_setup(kern, dev, ready)) != FLP_OK) return st;
-    const int grid = row_ctas(a.n, kRows, kNormSms * flp::kNormBwdCtas<kTpr>);
+    const int rows = row_ctas(a.n, kRows, kNormSms * flp::kNormBwdCtas<kTpr>);
     int fit = fits[dev].load(std::memory_order_acquire);
     if (fit == 0) {
         // for the widest row of this kernel, so that one number serves all its calls
@@ -155,7 +155,14 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
         fit = per_sm * sms + 1;
         fits[dev].store(fit, std::memory_order_release);
     }
-    const bool sums = a.part_w != nullptr || a.part_b != nullptr, grid_fold = sums && grid < fit;
+    const bool sums = a.part_w != nullptr || a.part_b != nullptr, grid_fold = sums && rows < fit;
+    // with a few rows more CTAs, so that the fold takes one turn
+    int grid = rows;
+    if (grid_fold) {
+        const int teams = kThreads / 32 / flp::norm_fold_team(rows, kThreads / 32);
+        const int64_t want = ceil_div(ceil_div(a.d, 8) * ((a.part_w != nullptr) + (a.part_b != nullptr)), teams);
+        if (grid < want) grid = (int)(want < fit - 1 ? want : fit - 1);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
@@ -166,9 +173,9 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = grid_fold ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, grid_fold ? 1 : 0);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, rows, grid_fold ? 1 : 0);
     if (e != cudaSuccess) return fail(FLP_ECUDA, "norm backward launch: %s", cudaGetErrorString(e));
-    *parts = grid_fold || !sums ? 0 : grid;
+    *parts = grid_fold || !sums ? 0 : rows;
     return ok();
 }
 

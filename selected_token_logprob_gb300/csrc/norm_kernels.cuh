@@ -167,27 +167,35 @@ k_norm_dw_any(NormBwdArgs a) {
 
 // ---------------------------------------------------------------- partial rows
 
-// out[c] (+)= sum over the partial rows in a fixed order, 8 columns (a sector) a
-// CTA and turn: a warp reads 4 rows at a time, 16 loads in flight a lane.  (With 32
-// columns a CTA most CTAs of a narrow norm had none, and the others read their 608
-// rows for 7 us.)
+// out[c] (+)= sum over the partial rows in an order fixed by their number, 8
+// columns (a sector) a team of warps and turn.  A warp reads 4 rows at a time, 16
+// loads in flight a lane, so a team has a warp per 64 rows.  (With the whole CTA on
+// each 8 columns, a few rows' sums took 27 us at 7 x 1024 and 17 at 64 x 4096, now
+// 4.6 and 6.2; with 32 columns a CTA most CTAs of a narrow norm had none.)
+__host__ __device__ __forceinline__ int norm_fold_team(int rows, int warps) {
+    int w = 1;
+    while (w < warps && 64 * w < rows) w *= 2;
+    return w;
+}
 template <int kWarps>
 __device__ __forceinline__ void norm_fold(const NormBwdArgs& a, int rows, float (*red)[8]) {
-    const int col = threadIdx.x & 7, sub = (threadIdx.x >> 3) & 3, ty = threadIdx.x >> 5;
-    const int groups = (int)((a.d + 7) / 8);
-    for (int g = blockIdx.x; g < 2 * groups; g += gridDim.x) {
-        const bool second = g >= groups;
+    const int col = threadIdx.x & 7, sub = (threadIdx.x >> 3) & 3, warp = threadIdx.x >> 5;
+    const int w = norm_fold_team(rows, kWarps), teams = kWarps / w, team = warp / w, ty = warp % w;
+    const int groups = (int)((a.d + 7) / 8), in_w = a.part_w ? groups : 0, all = in_w + (a.part_b ? groups : 0);
+    for (int g0 = blockIdx.x * teams; g0 < all; g0 += gridDim.x * teams) {
+        const int g = g0 + team;
+        const bool second = g >= in_w;
         const float* part = second ? a.part_b : a.part_w;
         float* out = second ? a.dbias : a.dweight;
-        if (part == nullptr) continue;   // uniform over the CTA
-        const int64_t c = (int64_t)(second ? g - groups : g) * 8 + col;
+        const int64_t c = (int64_t)(second ? g - in_w : g) * 8 + col;
+        const bool mine = g < all && c < a.d;
         float s[4] = {0.f, 0.f, 0.f, 0.f};
-        if (c < a.d) {
-            for (int r = ty * 4 + sub; r < rows; r += 64 * kWarps) {
+        if (mine) {
+            for (int r = ty * 4 + sub; r < rows; r += 64 * w) {
                 float v[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const int q = r + 4 * k * kWarps;
+                    const int q = r + 4 * k * w;
                     v[k] = q < rows ? __ldcg(part + (int64_t)q * a.dp + c) : 0.f;
                 }
 #pragma unroll
@@ -197,15 +205,15 @@ __device__ __forceinline__ void norm_fold(const NormBwdArgs& a, int rows, float 
         float t = (s[0] + s[1]) + (s[2] + s[3]);
         t += __shfl_xor_sync(0xffffffffu, t, 8);
         t += __shfl_xor_sync(0xffffffffu, t, 16);
-        __syncthreads();   // the last turn's readers
-        if (sub == 0) red[ty][col] = t;
-        __syncthreads();
-        if (threadIdx.x < 8 && c < a.d) {
+        if (w > 1) {   // alike in the whole CTA
+            __syncthreads();   // the last turn's readers
+            if (sub == 0) red[warp][col] = t;
+            __syncthreads();
             t = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) t += red[k][col];
-            out[c] = a.accumulate ? out[c] + t : t;
+            for (int k = 0; k < kWarps; ++k) t += k < w ? red[team * w + k][col] : 0.f;
         }
+        if (ty == 0 && sub == 0 && mine) out[c] = a.accumulate ? out[c] + t : t;
     }
 }
 
@@ -616,13 +624,13 @@ k_norm_fwd(NormFwdArgs a) {
     }
 }
 
-// dx and this CTA's partial row of dw (and db), which the CTAs fold after a
-// barrier of the grid (a cooperative launch; `grid_fold`), saving the launch of
-// k_norm_fold: it costs a caller as much as the kernel on small batches.  kFull: with
-// centring (unless a.mean is null) and db; else RMS norm without db.
+// dx and this CTA's partial row of dw (and db): `parts` CTAs have rows.  They are
+// folded after a barrier of the grid (a cooperative launch; `grid_fold`), saving the
+// launch of k_norm_fold: it costs a caller as much as the kernel on small batches.
+// kFull: with centring (unless a.mean is null) and db; else RMS norm without db.
 template <class T, class G, int kTpr, bool kFull, bool kAligned>
 __global__ void __launch_bounds__(kNormThreads<kTpr>, kNormBwdCtas<kTpr>)
-k_norm_bwd(NormBwdArgs a, int grid_fold) {
+k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
     constexpr int V = 16 / (int)sizeof(G), NV = kNormElems / V;
     constexpr int kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = kNormBwdStages<T, G>;
     extern __shared__ __align__(16) unsigned char norm_smem[];
@@ -751,7 +759,9 @@ k_norm_bwd(NormBwdArgs a, int grid_fold) {
         }
     }
     // the CTA's partial row
-    if constexpr (kRows == 1) {
+    if ((int)blockIdx.x >= parts) {
+        // only here to fold
+    } else if constexpr (kRows == 1) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
@@ -795,7 +805,7 @@ k_norm_bwd(NormBwdArgs a, int grid_fold) {
     if (grid_fold) {
         __shared__ float fold[kThreads / 32][8];
         cooperative_groups::this_grid().sync();
-        norm_fold<kThreads / 32>(a, (int)gridDim.x, fold);
+        norm_fold<kThreads / 32>(a, parts, fold);
     }
 }
 

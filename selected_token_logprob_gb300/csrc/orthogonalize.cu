@@ -208,36 +208,32 @@ flp_status orth_product(int dev, int sms, int pairs, int64_t batch, const OrthMa
     return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
 }
 
-// CTAs of the cluster that holds a matrix with m <= 128 in one launch (0: the
-// tiled kernels): at most 4 blocks of 64 columns a CTA, 6 with the most CTAs.
-int orth_cluster_ctas(int64_t m, int64_t blocks) {
-    if (m > 128) return 0;
-    for (int c = 1; c <= flp::kOrthCluMaxCtas; c *= 2)
-        if (ceil_div(blocks, c) <= (c == flp::kOrthCluMaxCtas ? flp::kOrthCluMaxBlocks : 4)) return c;
-    return 0;
-}
-
-// Launches the one-cluster form; *done = false where the device cannot hold the cluster.
-template <class T>
-flp_status orth_cluster_launch(int dev, int ctas, int64_t batch, const flp::OrthCluArgs& p, cudaStream_t s, bool* done) {
-    static std::atomic<int> fits[kMaxDevices][5];   // by log2 of the CTAs: 0 unknown, 1 yes, 2 no
-    const auto kern = flp::k_orth_cluster<T>;
+cudaLaunchConfig_t orth_cluster_config(int ctas, int64_t batch, cudaStream_t s, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(batch * ctas));
     cfg.blockDim = dim3(flp::kOrthCluThreads);
     cfg.dynamicSmemBytes = flp::kOrthCluSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = (unsigned)ctas;
+    attr->val.clusterDim.y = 1;
+    attr->val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Clusters of `ctas` CTAs (a power of two) that can be resident at once (0: none).
+template <class T>
+int orth_cluster_fit(int dev, int ctas) {
+    static std::atomic<int> fits[kMaxDevices][5];   // by log2 of the CTAs; + 1
+    const auto kern = flp::k_orth_cluster<T>;
     int log = 0;
     while ((1 << log) < ctas) ++log;
     int f = fits[dev][log].load(std::memory_order_acquire);
     if (f == 0) {
+        cudaLaunchAttribute attr;
+        const cudaLaunchConfig_t cfg = orth_cluster_config(ctas, 1, nullptr, &attr);
         int n = 0;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)flp::kOrthCluSmem) !=
                 cudaSuccess ||
@@ -246,12 +242,52 @@ flp_status orth_cluster_launch(int dev, int ctas, int64_t batch, const flp::Orth
             (void)cudaGetLastError();
             n = 0;
         }
-        f = n > 0 ? 1 : 2;
+        f = n + 1;
         fits[dev][log].store(f, std::memory_order_release);
     }
-    *done = f == 1;
-    if (f != 1) return FLP_OK;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    return f - 1;
+}
+
+// CTAs of the cluster that holds a matrix with m <= 128 in one launch (0: the tiled
+// kernels).
+template <class T>
+int orth_cluster_ctas(int dev, int64_t batch, int64_t m, int64_t blocks) {
+    if (m > 128) return 0;
+    auto fewest = [&](int per) {   // CTAs that hold `per` blocks of 64 columns each
+        for (int c = 1; c <= flp::kOrthCluMaxCtas; c *= 2)
+            if (ceil_div(blocks, c) <= per) return c;
+        return 0;
+    };
+    // Few columns: one CTA, without exchanges (64 x 256: 22.7 us; in 4 CTAs 23.3, in 2 26.4).
+    if (blocks <= 4) return orth_cluster_fit<T>(dev, 1) > 0 ? 1 : 0;
+    // Two blocks a CTA while all clusters run at once (64 x 512: 25.8 us, four blocks
+    // 31.2; 128 x 512: 43, 55; 64 x 1024: 27.9, 30.6), else four, or six with the most
+    // CTAs (16 x 128 x 1024: two 90.7, four 50.8).
+    int c = fewest(2);
+    if (c == 0 || batch > orth_cluster_fit<T>(dev, c)) {
+        c = fewest(4);
+        if (c == 0) c = ceil_div(blocks, flp::kOrthCluMaxCtas) <= flp::kOrthCluMaxBlocks ? flp::kOrthCluMaxCtas : 0;
+        if (c == 0) return 0;
+    }
+    const int fit = orth_cluster_fit<T>(dev, c);
+    if (fit <= 0) return 0;
+    // Large clusters leave SMs idle: over 64 rows the tiled kernels win from the third
+    // wave on (128 x 4096, 16 CTAs: a batch of 12 121 against 142 us, of 16 181 against
+    // 164; 128 x 2048, 8 CTAs: of 24 109 against 133, of 32 163 against 151); smaller
+    // clusters and fewer rows stay ahead (200 x 64 x 1024: 191 against 275).
+    if (m > 64 && c >= 8 && batch > 2 * (int64_t)fit) return 0;
+    return c;
+}
+
+// The one-cluster form; *done = false where the tiled kernels have to serve.
+template <class T>
+flp_status orth_cluster_launch(int dev, int64_t batch, const flp::OrthCluArgs& p, cudaStream_t s, bool* done) {
+    const int ctas = orth_cluster_ctas<T>(dev, batch, p.m, p.blocks);
+    *done = ctas > 0 && batch * ctas < kMaxGrid;
+    if (!*done) return FLP_OK;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = orth_cluster_config(ctas, batch, s, &attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, flp::k_orth_cluster<T>, p);
     if (e != cudaSuccess) return fail(FLP_ECUDA, "orthogonalize cluster launch: %s", cudaGetErrorString(e));
     return ok();
 }
@@ -332,8 +368,7 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     const bool vec_in = (cols * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) &&
                         (batch == 1 || (stride_x * eb) % 16 == 0);
     const bool vec_out = aligned16(out) && (ld_out * ob) % 16 == 0 && (batch == 1 || (stride_out * ob) % 16 == 0);
-    const int ctas = orth_cluster_ctas(l.m, l.np / 64);
-    if (ctas > 0 && batch * ctas < kMaxGrid) {
+    if (l.m <= 128) {
         flp::OrthCluArgs c{};
         c.x = x;
         c.ld = ld_x;
@@ -354,9 +389,9 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
         c.stride_out = stride_out;
         for (int k = 0; k < 3 * steps; ++k) c.coef[k] = coefficients[k];
         bool done = false;
-        st = dtype == FLP_DTYPE_BF16 ? orth_cluster_launch<__nv_bfloat16>(dev, ctas, batch, c, s, &done)
-             : dtype == FLP_DTYPE_F16 ? orth_cluster_launch<__half>(dev, ctas, batch, c, s, &done)
-                                      : orth_cluster_launch<float>(dev, ctas, batch, c, s, &done);
+        st = dtype == FLP_DTYPE_BF16 ? orth_cluster_launch<__nv_bfloat16>(dev, batch, c, s, &done)
+             : dtype == FLP_DTYPE_F16 ? orth_cluster_launch<__half>(dev, batch, c, s, &done)
+                                      : orth_cluster_launch<float>(dev, batch, c, s, &done);
         if (st != FLP_OK || done) return st;
     }
     const int pairs = orth_pairs(dev);

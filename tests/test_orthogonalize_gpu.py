@@ -111,6 +111,16 @@ def test_stacks_and_types(dtype, shape):
         _check(x[k], flp.orthogonalize(x[k], out_dtype=torch.float32), [ABC] * 5)
 
 
+@pytest.mark.parametrize("shape", [(26, 100, 4000), (26, 4100, 128), (40, 127, 2000), (30, 64, 1500), (9, 128, 520),
+                                   (300, 24, 130), (14, 100, 900)])
+def test_stacks_of_small_matrices(shape):
+    """More matrices than clusters that run at once, and few enough for smaller slices."""
+    x = _gradient(shape, 5)
+    got = flp.orthogonalize(x, out_dtype=torch.float32)
+    _check(x, got, [ABC] * 5)
+    assert torch.equal(got, flp.orthogonalize(x, out_dtype=torch.float32))
+
+
 @pytest.mark.parametrize("kind", ["gauss", "low_rank", "one_direction", "decaying", "orthogonal"])
 @pytest.mark.parametrize("shape", [(256, 256), (512, 1500), (700, 128)])
 def test_spectra(kind, shape):

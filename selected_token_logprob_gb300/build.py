@@ -16,10 +16,12 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfused_logp.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fused_logp.cu", "norm.cu", "orthogonalize.cu", "preference.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fused_logp.cu", "norm_backward.cu", "norm_forward.cu",
+                                                     "orthogonalize.cu", "preference.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("logp_kernels.cuh", "logp_prims.cuh",
                                                   "grpo_kernels.cuh", "linear_logp.cuh", "gemm_bf16.cuh",
-                                                  "host_common.h", "norm_kernels.cuh", "ortho_cluster.cuh", "ortho_kernels.cuh",
+                                                  "host_common.h", "norm_host.h", "norm_kernels.cuh", "ortho_cluster.cuh",
+                                                  "ortho_kernels.cuh",
                                                   "preference_kernels.cuh", "tc_prims.cuh")] + [os.path.join(INCLUDE, "fused_logp.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

@@ -1,114 +1,12 @@
-// Host side of the norm in front of the LM head (fused_layer_norm_forward,
-// fused_layer_norm_backward): argument checks and launches.
+// Host side of the norm's backward (fused_layer_norm_backward): argument checks and
+// launches.
 #include <math.h>
 
-#include "host_common.h"
-#include "norm_kernels.cuh"
+#include "norm_host.h"
 
 using namespace flp_host;
 
 namespace {
-
-constexpr int64_t kNormMaxDim = ((int64_t)1 << 31) - 1;
-
-flp_status check_norm_shape(int64_t n, int64_t d, int dtype) {
-    flp_status st;
-    if ((st = check_dtype(dtype)) != FLP_OK) return st;
-    if (n < 0) return fail(FLP_EINVAL, "n must be >= 0 (got %lld)", (long long)n);
-    if (d < 1) return fail(FLP_EINVAL, "d must be >= 1 (got %lld)", (long long)d);
-    if (d > kNormMaxDim) return fail(FLP_EUNSUPPORTED, "d must be below 2^31 (got %lld)", (long long)d);
-    return FLP_OK;
-}
-
-// A vector's or gradient's dtype: the rows' own or FP32.
-flp_status check_side_dtype(const char* name, int side, int dtype) {
-    if (side != dtype && side != FLP_DTYPE_F32)
-        return fail(FLP_EINVAL, "%s dtype must be x's (%d) or FLP_DTYPE_F32 (got %d)", name, dtype, side);
-    return FLP_OK;
-}
-
-struct Extent {
-    const char* name;
-    const void* p;
-    int64_t bytes;
-};
-
-// The output `o` must not share bytes with the input `i`, unless it lies on
-// it exactly and `same` allows that.
-flp_status check_apart(const Extent& o, const Extent& i, bool same) {
-    if (o.p == nullptr || i.p == nullptr || (same && o.p == i.p)) return FLP_OK;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(o.p), b = reinterpret_cast<uintptr_t>(i.p);
-    if (a < b + (uintptr_t)i.bytes && b < a + (uintptr_t)o.bytes)
-        return fail(FLP_EINVAL, "%s overlaps %s", o.name, i.name);
-    return FLP_OK;
-}
-
-// Allows a kernel its ring of shared memory, once per device.
-template <class K>
-flp_status norm_setup(K kern, int dev, std::atomic<bool>* ready) {
-    if (ready[dev].load(std::memory_order_acquire)) return FLP_OK;
-    cudaFuncAttributes f;
-    cudaError_t e = cudaFuncGetAttributes(&f, kern);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - (int)f.sharedSizeBytes);
-    if (e != cudaSuccess) return fail(FLP_ECUDA, "norm setup: %s", cudaGetErrorString(e));
-    ready[dev].store(true, std::memory_order_release);
-    return FLP_OK;
-}
-
-// SMs that the persistent grids are sized for: a constant, so that the order
-// of the weight's gradient depends on the problem alone.
-constexpr int kNormSms = 152;
-
-int row_ctas(int64_t n, int rows, int most) {
-    const int64_t c = ceil_div(n, rows);
-    return (int)(c < most ? c : most);
-}
-
-constexpr size_t kNormMaxSmem = 232448 - 8192;   // of a CTA, beside the static arrays
-
-template <class T, bool kCenter>
-flp_status launch_fwd_any(const flp::NormFwdArgs& a, cudaStream_t s) {
-    flp::k_norm_fwd_any<T, kCenter><<<row_ctas(a.n, 1, kNormSms * 8), flp::kNormAnyThreads, 0, s>>>(a);
-    return check_launch("norm forward");
-}
-
-template <class T, class W, int kTpr, bool kCenter, bool kAligned>
-flp_status launch_fwd_rows(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
-    static std::atomic<bool> ready[kMaxDevices];
-    constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = flp::kNormFwdStages<T>;
-    const auto kern = flp::k_norm_fwd<T, W, kTpr, kCenter, kAligned>;
-    const size_t smem = kAligned ? (size_t)kThreads * flp::kNormElems * sizeof(T) * kStages
-                                 : (size_t)flp::norm_pitch<T>(a.d) * kRows * (kStages + 1);
-    if (smem > kNormMaxSmem) return launch_fwd_any<T, kCenter>(a, s);
-    flp_status st;
-    if ((st = norm_setup(kern, dev, ready)) != FLP_OK) return st;
-    kern<<<row_ctas(a.n, kRows, kNormSms * flp::kNormFwdCtas<kTpr>), kThreads, smem, s>>>(a);
-    return check_launch("norm forward");
-}
-
-template <class T, class W, bool kCenter, bool kAligned>
-flp_status launch_fwd_v(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
-    constexpr int E = flp::kNormElems;
-    if (a.d <= 32 * E) return launch_fwd_rows<T, W, 32, kCenter, kAligned>(a, dev, s);
-    if (a.d <= 128 * E) return launch_fwd_rows<T, W, 128, kCenter, kAligned>(a, dev, s);
-    if (a.d <= 256 * E) return launch_fwd_rows<T, W, 256, kCenter, kAligned>(a, dev, s);
-    if (a.d <= 512 * E) return launch_fwd_rows<T, W, 512, kCenter, kAligned>(a, dev, s);
-    if (a.d <= 1024 * E) return launch_fwd_rows<T, W, 1024, kCenter, kAligned>(a, dev, s);
-    return launch_fwd_any<T, kCenter>(a, s);
-}
-
-template <class T, class W>
-flp_status launch_fwd_w(const flp::NormFwdArgs& a, bool center, bool vec, int dev, cudaStream_t s) {
-    if (vec) return center ? launch_fwd_v<T, W, true, true>(a, dev, s) : launch_fwd_v<T, W, false, true>(a, dev, s);
-    return center ? launch_fwd_v<T, W, true, false>(a, dev, s) : launch_fwd_v<T, W, false, false>(a, dev, s);
-}
-
-template <class T>
-flp_status launch_norm_fwd(const flp::NormFwdArgs& a, bool center, bool vec, int dev, cudaStream_t s) {
-    return a.w.dtype == FLP_DTYPE_F32 ? launch_fwd_w<T, float>(a, center, vec, dev, s)
-                                      : launch_fwd_w<T, T>(a, center, vec, dev, s);
-}
 
 template <class T, class G, bool kCenter>
 flp_status launch_bwd_any(const flp::NormBwdArgs& a, cudaStream_t s, int* parts) {
@@ -181,7 +79,12 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
 
 template <class T, class G, bool kFull, bool kAligned>
 flp_status launch_bwd_v(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
+    // As in the forward, the fewest threads that hold a row (2 M rows of 64 BF16: by a warp
+    // each 515 us, 160 here; 65536 x 512 with 128 threads 69, 42 here; 32768 x 2048 with 256
+    // 83, 69 here), but for two warps a row (131072 x 1024: 168 us, with four 153).
     constexpr int E = flp::kNormElems;
+    if (a.d <= 8 * E) return launch_bwd_rows<T, G, 8, kFull, kAligned>(a, dev, s, parts);
+    if (a.d <= 16 * E) return launch_bwd_rows<T, G, 16, kFull, kAligned>(a, dev, s, parts);
     if (a.d <= 32 * E) return launch_bwd_rows<T, G, 32, kFull, kAligned>(a, dev, s, parts);
     if (a.d <= 128 * E) return launch_bwd_rows<T, G, 128, kFull, kAligned>(a, dev, s, parts);
     if (a.d <= 256 * E) return launch_bwd_rows<T, G, 256, kFull, kAligned>(a, dev, s, parts);
@@ -208,42 +111,6 @@ bool norm_workspace_bytes(int64_t d, int64_t* out) {
 }  // namespace
 
 extern "C" {
-
-flp_status fused_layer_norm_forward(const void* x, int dtype, int64_t n, int64_t d, int64_t ld_x,
-                                    const void* weight, const void* bias, int weight_dtype, float eps, int center,
-                                    void* y, int64_t ld_y, float* mean, float* rstd, flp_stream_t stream) {
-    flp_status st;
-    if ((st = check_norm_shape(n, d, dtype)) != FLP_OK) return st;
-    if ((st = check_side_dtype("weight", weight_dtype, dtype)) != FLP_OK) return st;
-    if (ld_x < d || ld_y < d)
-        return fail(FLP_EINVAL, "ld_x (%lld) and ld_y (%lld) must be >= d (%lld)", (long long)ld_x, (long long)ld_y,
-                    (long long)d);
-    if (!(eps >= 0.f) || !isfinite(eps)) return fail(FLP_EINVAL, "eps must be finite and >= 0 (got %g)", (double)eps);
-    if (n == 0) return ok();
-    const int eb = elem_bytes(dtype);
-    int64_t bx, by;
-    if (!span_bytes(n, d, ld_x, eb, &bx) || !span_bytes(n, d, ld_y, eb, &by))
-        return fail(FLP_EINVAL, "x or y extent overflows int64");
-    const Extent ey{"y", y, by};
-    if ((st = check_apart(ey, {"x", x, bx}, ld_x == ld_y)) != FLP_OK) return st;
-    const void* ptrs[] = {x, y, weight, bias, mean, rstd};
-    const char* names[] = {"x", "y", "weight", "bias", "mean", "rstd"};
-    const bool optional[] = {false, false, true, true, true, true};
-    int dev;
-    if ((st = common_device(6, ptrs, names, optional, &dev)) != FLP_OK) return st;
-    if (dev < 0 || dev >= kMaxDevices) return fail(FLP_ECUDA, "device index %d out of range", dev);
-    DeviceGuard guard;
-    if ((st = guard.enter(dev)) != FLP_OK) return st;
-    const flp::NormFwdArgs a{x, n, d, ld_x, {weight, weight_dtype}, {bias, weight_dtype}, eps, 1.f / (float)d,
-                             y, ld_y, mean, rstd};
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // 16-byte vectors need whole, aligned ones in every row and vector
-    const bool vec = (d * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) && rows_aligned16(y, ld_y, dtype) &&
-                     aligned16(weight) && aligned16(bias);
-    if (dtype == FLP_DTYPE_BF16) return launch_norm_fwd<__nv_bfloat16>(a, center != 0, vec, dev, s);
-    if (dtype == FLP_DTYPE_F16) return launch_norm_fwd<__half>(a, center != 0, vec, dev, s);
-    return launch_norm_fwd<float>(a, center != 0, vec, dev, s);
-}
 
 flp_status fused_layer_norm_backward_workspace_size(int64_t d, int64_t* bytes) {
     if (bytes == nullptr) return fail(FLP_EINVAL, "bytes is a null pointer");
@@ -322,7 +189,7 @@ flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy
     else
         st = launch_norm_bwd<float, float>(a, vec, dev, s, &parts);
     if (st != FLP_OK || parts == 0) return st;
-    return launch_dependent("norm fold", flp::k_norm_fold, dim3((unsigned)(2 * ceil_div(d, 8))), flp::kNormFoldThreads,
+    return launch_dependent("norm fold", flp::k_norm_fold<flp::kNormFoldThreads>, dim3((unsigned)(2 * ceil_div(d, 8))), flp::kNormFoldThreads,
                             (size_t)0, s, a, parts);
 }
 

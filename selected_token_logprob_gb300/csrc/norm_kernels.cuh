@@ -218,19 +218,20 @@ __device__ __forceinline__ void norm_fold(const NormBwdArgs& a, int rows, float 
 }
 
 constexpr int kNormFoldThreads = 256;
-__global__ void __launch_bounds__(kNormFoldThreads)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
 k_norm_fold(NormBwdArgs a, int rows) {
-    __shared__ float red[kNormFoldThreads / 32][8];
+    __shared__ float red[kThreads / 32][8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    norm_fold<kNormFoldThreads / 32>(a, rows, red);
+    norm_fold<kThreads / 32>(a, rows, red);
 }
 
 // ---------------------------------------------------------------- rows in registers
 
-// A row is held by kTpr threads, kNormElems elements each: kTpr = 32 (a warp
-// per row, four rows a CTA, no block-wide sums) up to 512 columns, then one
-// CTA per row.  Persistent CTAs step through the rows and copy the next ones
-// into a ring in shared memory with cp.async, so that the loads of several
+// A row is held by kTpr threads, at most kNormElems elements each: part of a warp
+// up to 256 columns, a warp up to 512, in the forward two up to 1024 (no block-wide sums,
+// several rows a CTA), then one CTA per row.  Persistent CTAs step through the rows and copy the
+// next ones into a ring in shared memory with cp.async, so that the loads of several
 // rows are in flight while one is reduced and written.
 //
 // A thread owns vectors of V elements, V being 16 bytes of the wider of x and dy,
@@ -243,7 +244,12 @@ k_norm_fold(NormBwdArgs a, int rows) {
 // 16-byte blocks that hold the row and shift their vectors out of two neighbours;
 // results go back through shared memory as aligned blocks, the row's first and last
 // element by element.  (Element loads and stores, one value a lane, were bound by
-// their instructions: 5003 x 1031 FP16, forward and backward, 44 us.)
+// their instructions: 5003 x 1031 FP16, forward and backward, 44 us, now 36.  Aligned
+// rows by blocks: the backward at 16384 x 4096 120 us, 69 by vectors.)
+//
+// What bounds it: memory (32768 x 4096 BF16: forward 88 us, 6.1 TB/s, backward with FP32
+// dy 150 us, 7.1 TB/s; 2 M rows of 64: 5.2 and 5.0 TB/s), but for the instructions of the
+// shifted rows (130182 x 1031: 2.3 and 2.1 TB/s).
 constexpr int kNormElems = 16;
 template <int kTpr>
 constexpr int kNormThreads = kTpr < 128 ? 128 : kTpr;
@@ -358,28 +364,37 @@ __device__ __forceinline__ void norm_vec_load(const W* p, int i, float (&o)[V]) 
     }
 }
 
+// Barrier of a row's threads.
+template <int kTpr>
+__device__ __forceinline__ void norm_row_sync() {
+    if constexpr (kTpr <= 32) __syncwarp();
+    else if constexpr (kTpr == kNormThreads<kTpr>) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / kTpr), "n"(kTpr) : "memory");
+}
+
 // Sums of kCount values over the threads of a row, the same in each of them.
 // `red` holds two buffers of 32 x kCount floats used in turn (`turn`), so one
 // barrier per sum is enough.
 template <int kTpr, int kCount>
 __device__ __forceinline__ void norm_row_sum(float (&v)[kCount], float* red, int& turn) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
+    for (int o = (kTpr < 32 ? kTpr : 32) / 2; o >= 1; o >>= 1)
 #pragma unroll
         for (int c = 0; c < kCount; ++c) v[c] += __shfl_xor_sync(0xffffffffu, v[c], o);
     if constexpr (kTpr > 32) {
         constexpr int kWarps = kTpr / 32;
+        const int warp = threadIdx.x >> 5, first = warp / kWarps * kWarps;   // of the row
         float* buf = red + turn * 64;
         turn ^= 1;
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int c = 0; c < kCount; ++c) buf[c * 32 + (threadIdx.x >> 5)] = v[c];
-        __syncthreads();
+            for (int c = 0; c < kCount; ++c) buf[c * 32 + warp] = v[c];
+        norm_row_sync<kTpr>();
 #pragma unroll
         for (int c = 0; c < kCount; ++c) {
             float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) s += buf[c * 32 + k];
+            for (int k = 0; k < kWarps; ++k) s += buf[c * 32 + first + k];
             v[c] = s;
         }
     }
@@ -468,10 +483,7 @@ __device__ __forceinline__ void norm_slot(uint32_t src, int k, int t, float (&o)
 // After the wait for this thread's copies: those of the row's other threads.
 template <int kTpr, bool kAligned>
 __device__ __forceinline__ void norm_copied() {
-    if constexpr (!kAligned) {
-        if constexpr (kTpr == 32) __syncwarp();
-        else __syncthreads();
-    }
+    if constexpr (!kAligned) norm_row_sync<kTpr>();
 }
 // The row of d elements staged at `src` (16-byte aligned) to p, at any alignment.
 template <class T, int kTpr>
@@ -539,7 +551,10 @@ k_norm_fwd(NormFwdArgs a) {
         cp_async_commit();
     }
     int stage = 0;
-    for (; r < a.n; r += step) {
+    // the rows of a warp take their turns together, the last of them without a row
+    const int64_t before = kTpr < 32 ? (threadIdx.x & 31) / kTpr : 0;
+    for (; r - before < a.n; r += step) {
+        const bool live = kTpr >= 32 || r < a.n;
         float v[NV][V];
         const int64_t ahead = r + (kStages - 1) * step;
         const int into = stage == 0 ? kStages - 1 : stage - 1;
@@ -551,7 +566,7 @@ k_norm_fwd(NormFwdArgs a) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
-            if (i < nvec) {
+            if (i < nvec && live) {
                 norm_slot<T, V, kTpr, kAligned>(src, k, t, v[k]);
                 if constexpr (!kAligned) {
                     if ((i + 1) * V > d) {
@@ -595,7 +610,7 @@ k_norm_fwd(NormFwdArgs a) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
-            if (i < nvec) {
+            if (i < nvec && live) {
                 float f[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) v[k][j] = (v[k][j] - mu) * rstd;
@@ -615,9 +630,9 @@ k_norm_fwd(NormFwdArgs a) {
         }
         if constexpr (!kAligned) {
             norm_copied<kTpr, kAligned>();   // the whole row is staged
-            norm_store_row<T, kTpr>(y, d, t, out);
+            if (live) norm_store_row<T, kTpr>(y, d, t, out);
         }
-        if (t == 0) {
+        if (t == 0 && live) {
             if (kCenter && a.mean) a.mean[r] = mu;
             if (a.rstd) a.rstd[r] = rstd;
         }
@@ -687,7 +702,9 @@ k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
         rstd_next = __ldg(a.rstd + r);
     }
     int stage = 0;
-    for (; r < a.n; r += step) {
+    const int64_t before = kTpr < 32 ? (threadIdx.x & 31) / kTpr : 0;
+    for (; r - before < a.n; r += step) {
+        const bool live = kTpr >= 32 || r < a.n;
         const float mu = mu_next, rstd = rstd_next;
         if (r + step < a.n) {
             mu_next = center ? __ldg(a.mean + r + step) : 0.f;
@@ -709,7 +726,7 @@ k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
-            if (i < nvec) {
+            if (i < nvec && live) {
                 norm_slot<T, V, kTpr, kAligned>(sx, k, t, xh[k]);
                 norm_slot<G, V, kTpr, kAligned>(sg, k, t, g[k]);
                 if constexpr (!kAligned) {
@@ -746,7 +763,7 @@ k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
-            if (i < nvec) {
+            if (i < nvec && live) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) xh[k][j] = (g[k][j] - c1 - xh[k][j] * c2) * rstd;
                 if constexpr (kAligned) norm_stg(dx + i * V, norm_pack<T, V>(xh[k]));
@@ -755,7 +772,7 @@ k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
         }
         if constexpr (!kAligned) {
             norm_copied<kTpr, kAligned>();   // the whole row is staged
-            norm_store_row<T, kTpr>(dx, d, t, out);
+            if (live) norm_store_row<T, kTpr>(dx, d, t, out);
         }
     }
     // the CTA's partial row
@@ -781,10 +798,21 @@ k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
             }
         }
     } else {
-        // the rows' warps one after the other, through shared memory
+        // the rows of a warp by shuffles, then the warps (or pairs of them) one after the
+        // other, through shared memory
         __shared__ float sum[kFull ? 2 : 1][kTpr * kNormElems];
-        for (int q = 0; q < kRows; ++q) {
-            if ((int)threadIdx.x / kTpr == q) {
+        constexpr int kGroup = kTpr < 32 ? 32 : kTpr;
+#pragma unroll
+        for (int o = kTpr; o < 32; o <<= 1)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    dw[k][j] += __shfl_xor_sync(0xffffffffu, dw[k][j], o);
+                    if (kFull) db[k][j] += __shfl_xor_sync(0xffffffffu, db[k][j], o);
+                }
+        for (int q = 0; q < kThreads / kGroup; ++q) {
+            if ((int)threadIdx.x / kGroup == q && (int)threadIdx.x % kGroup < kTpr) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     const int i = k * kTpr + t;

@@ -108,6 +108,23 @@ def test_forward_and_backward(n, d, dtype, center):
     _check(x, w, b, 1e-5, center, dy, _run(x, w, b, 1e-5, center, dy))
 
 
+@pytest.mark.parametrize("n,d", [(1000, 128), (1001, 65), (30011, 64), (40000, 100), (6007, 16), (20003, 129), (9001, 256),
+                                 (2050, 200), (77, 513), (5003, 768), (6001, 1024), (4001, 1001)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("center", [True, False])
+def test_many_narrow_rows(n, d, dtype, center):
+    """Rows that share a warp or a CTA, more of them than run at once."""
+    gen = torch.Generator(device=DEV).manual_seed(n * 65537 + d)
+    x = _rows(n, d, dtype, gen, offset=0.3)
+    w = (1 + 0.3 * torch.randn(d, generator=gen, device=DEV)).to(dtype)
+    b = (0.3 * torch.randn(d, generator=gen, device=DEV)).to(dtype) if center else None
+    dy = _rows(n, d, dtype, gen)
+    got = _run(x, w, b, 1e-5, center, dy)
+    _check(x, w, b, 1e-5, center, dy, got)
+    for p, q in zip(got, _run(x, w, b, 1e-5, center, dy)):
+        assert p is None and q is None or torch.equal(p, q)
+
+
 @pytest.mark.parametrize("d", [64, 250, 1024, 1031, 4096])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("wide_dy,wide_w", [(True, True), (True, False), (False, True)])

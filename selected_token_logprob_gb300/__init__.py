@@ -16,6 +16,10 @@ Entry points (same names as the C ABI):
                         part_max, part_sum, sel)
     logp_merge_partials(part_max, part_sum, sel, targets, v_total,
                         ignore_index) -> (logp, lse)
+    fused_layer_norm_forward / fused_layer_norm_backward (norm.py; autograd:
+        fused_layer_norm), logp_preference_loss (preference.py), orthogonalize
+        (newton_schulz.py): the norm in front of the LM head, the loss on
+        pairs of packed sequences, the orthogonalised update of a weight
 ``FusedLogp``, an autograd function that saves only the O(N) LSE (and its
 residual), and ``flp_device_error`` / ``flp_selftest_wait_timeout`` for the
 device-side health word.

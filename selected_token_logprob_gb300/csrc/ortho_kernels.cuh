@@ -35,7 +35,7 @@
 // CTA's abort flag, the copies and MMAs in flight are waited for, TMEM is freed and
 // the kernel returns.
 //
-// What bounds it (4096 x 4096, 1025 us): the tensor cores and the copies that feed
+// What bounds it (4096 x 4096, 1.07 ms): the tensor cores and the copies that feed
 // them, 585 cycles a K block of a 256 x 256 tile (512 being the MMAs' own), in 2, 2
 // and 4 waves a step where 1.8, 1.8 and 3.4 would hold the work.  Cutting the K
 // blocks of all tiles into equal runs, one a pair, did not pay: the same 1046 us,
@@ -162,10 +162,10 @@ __device__ __forceinline__ OrthUnit orth_unit(int64_t u, const OrthArgs& p) {
 }
 
 // Shared memory of a CTA: the stages (128 rows of A and its rows or columns of
-// B per K block), a block of barriers, and two 4 KB boxes per epilogue warp.  A
-// TMA copy takes 2000 (idle) to 3100 (loaded) cycles to arrive, so nearly all
-// of shared memory goes to the stages: with 4 of them (and 64 KB of boxes) a
-// K block of a 256 x 256 pair tile took 776 cycles, 512 being the MMAs' own.
+// B per K block), a block of barriers, and two boxes of 32 x 32 per epilogue warp and
+// matrix.  A TMA copy takes 2000 (idle) to 3100 (loaded) cycles to arrive, so nearly
+// all of shared memory goes to the stages (a 256 x 256 pair tile: 6 for Gram and Poly,
+// 5 for Apply): with 4 a K block took 776 cycles, 512 being the MMAs' own.
 constexpr uint32_t kOrthABytes = 128 * kOrthBK * 2;
 template <int kBN, bool kPair>
 constexpr uint32_t kOrthBBytes = (kPair ? kBN / 2 : kBN) * kOrthBK * 2;

@@ -10,7 +10,8 @@
 // token) divided by their number D.  The gradient of token t of sequence s is
 // +-(dl/dh) / D, divided by n_s when averaging.
 //
-// One cooperative launch, three phases with a barrier of the grid between them.
+// One cooperative launch (all CTAs are resident, so every barrier ends), three phases
+// with a barrier of the grid between them.
 // Sums: the batch is cut into fixed chunks of 512 tokens; a warp takes a run of
 // consecutive chunks and writes, for every sequence that a chunk meets, the sum and
 // the active count into slot (chunk + sequence).  Along the packed batch each next

@@ -718,6 +718,17 @@ flp_status flp_selftest_wait_timeout(int device, int64_t limit_cycles, int* time
  */
 flp_status flp_selftest_ex2_bias(int device, double* mean_rel_err, double* compensation);
 
+/*
+ * Self-test of the norm's backward where the rows' CTAs are fewer than those that
+ * can be resident (as on a part with more SMs than the rows' grid is sized for, 152):
+ * fused_layer_norm_backward with that grid sized for `sms` (1 to 152) of them.
+ */
+flp_status flp_selftest_norm_backward(int sms, const void* dy, int dy_dtype, int64_t ld_dy, const void* x, int dtype,
+                                      int64_t n, int64_t d, int64_t ld_x, const void* weight, int weight_dtype,
+                                      const float* mean, const float* rstd, int center, void* workspace,
+                                      int64_t workspace_bytes, void* dx, int64_t ld_dx, float* dweight, float* dbias,
+                                      int accumulate, flp_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -78,6 +78,9 @@ SIGNATURES = {
     "fused_layer_norm_backward": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, ctypes.c_int, _I64, _I64, _I64, _P,
                                                  ctypes.c_int, _P, _P, ctypes.c_int, _P, _I64, _P, _I64, _P, _P,
                                                  ctypes.c_int, _P]),
+    "flp_selftest_norm_backward": (ctypes.c_int, [ctypes.c_int, _P, ctypes.c_int, _I64, _P, ctypes.c_int, _I64, _I64,
+                                                  _I64, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _I64, _P, _I64,
+                                                  _P, _P, ctypes.c_int, _P]),
     "logp_preference_loss_workspace_size": (ctypes.c_int, [_I64, _I64, ctypes.POINTER(_I64)]),
     "logp_preference_loss": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                             ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float, _P, _I64,

@@ -8,9 +8,17 @@ using namespace flp_host;
 
 namespace {
 
+// Where a call's launches go: `sms` sizes the grid of the rows (kNormSms but in the
+// self-test).
+struct NormTo {
+    int dev, sms;
+    cudaStream_t s;
+};
+
 template <class T, class G, bool kCenter>
-flp_status launch_bwd_any(const flp::NormBwdArgs& a, cudaStream_t s, int* parts) {
-    flp::k_norm_dx_any<T, G, kCenter><<<row_ctas(a.n, 1, kNormSms * 8), flp::kNormAnyThreads, 0, s>>>(a);
+flp_status launch_bwd_any(const flp::NormBwdArgs& a, const NormTo& to, int* parts) {
+    const cudaStream_t s = to.s;
+    flp::k_norm_dx_any<T, G, kCenter><<<row_ctas(a.n, 1, to.sms * 8), flp::kNormAnyThreads, 0, s>>>(a);
     if (a.part_w || a.part_b) {
         const dim3 grid((unsigned)ceil_div(a.d, flp::kNormAnyThreads), flp::kNormAnyParts);
         flp::k_norm_dw_any<T, G, kCenter><<<grid, flp::kNormAnyThreads, 0, s>>>(a);
@@ -22,7 +30,8 @@ flp_status launch_bwd_any(const flp::NormBwdArgs& a, cudaStream_t s, int* parts)
 // Launches the row kernel.  *parts = its CTAs, one partial row each, that are left
 // to fold; 0 where the kernel folds them itself.
 template <class T, class G, int kTpr, bool kFull, bool kAligned>
-flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
+flp_status launch_bwd_rows(const flp::NormBwdArgs& a, const NormTo& to, int* parts) {
+    const int dev = to.dev;
     static std::atomic<bool> ready[kMaxDevices];
     static std::atomic<int> fits[kMaxDevices];   // CTAs that can be resident at once + 1, with the most shared memory
     constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr;
@@ -35,10 +44,10 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
     };
     const size_t smem = bytes(a.d);
     if (smem > kNormMaxSmem)
-        return a.mean ? launch_bwd_any<T, G, true>(a, s, parts) : launch_bwd_any<T, G, false>(a, s, parts);
+        return a.mean ? launch_bwd_any<T, G, true>(a, to, parts) : launch_bwd_any<T, G, false>(a, to, parts);
     flp_status st;
     if ((st = norm_setup(kern, dev, ready)) != FLP_OK) return st;
-    const int rows = row_ctas(a.n, kRows, kNormSms * flp::kNormBwdCtas<kTpr>);
+    const int rows = row_ctas(a.n, kRows, to.sms * flp::kNormBwdCtas<kTpr>);
     int fit = fits[dev].load(std::memory_order_acquire);
     if (fit == 0) {
         // for the widest row of this kernel, so that one number serves all its calls
@@ -54,7 +63,7 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
         fits[dev].store(fit, std::memory_order_release);
     }
     const bool sums = a.part_w != nullptr || a.part_b != nullptr, grid_fold = sums && rows < fit;
-    // with a few rows more CTAs, so that the fold takes one turn
+    // with a few rows more CTAs than take any, so that the fold takes one turn
     int grid = rows;
     if (grid_fold) {
         const int teams = kThreads / 32 / flp::norm_fold_team(rows, kThreads / 32);
@@ -65,7 +74,7 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
+    cfg.stream = to.s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
@@ -78,27 +87,27 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, int dev, cudaStream_t s, i
 }
 
 template <class T, class G, bool kFull, bool kAligned>
-flp_status launch_bwd_v(const flp::NormBwdArgs& a, int dev, cudaStream_t s, int* parts) {
+flp_status launch_bwd_v(const flp::NormBwdArgs& a, const NormTo& to, int* parts) {
     // As in the forward, the fewest threads that hold a row (2 M rows of 64 BF16: by a warp
     // each 515 us, 160 here; 65536 x 512 with 128 threads 69, 42 here; 32768 x 2048 with 256
     // 83, 69 here), but for two warps a row (131072 x 1024: 168 us, with four 153).
     constexpr int E = flp::kNormElems;
-    if (a.d <= 8 * E) return launch_bwd_rows<T, G, 8, kFull, kAligned>(a, dev, s, parts);
-    if (a.d <= 16 * E) return launch_bwd_rows<T, G, 16, kFull, kAligned>(a, dev, s, parts);
-    if (a.d <= 32 * E) return launch_bwd_rows<T, G, 32, kFull, kAligned>(a, dev, s, parts);
-    if (a.d <= 128 * E) return launch_bwd_rows<T, G, 128, kFull, kAligned>(a, dev, s, parts);
-    if (a.d <= 256 * E) return launch_bwd_rows<T, G, 256, kFull, kAligned>(a, dev, s, parts);
-    return launch_bwd_rows<T, G, 512, kFull, kAligned>(a, dev, s, parts);
+    if (a.d <= 8 * E) return launch_bwd_rows<T, G, 8, kFull, kAligned>(a, to, parts);
+    if (a.d <= 16 * E) return launch_bwd_rows<T, G, 16, kFull, kAligned>(a, to, parts);
+    if (a.d <= 32 * E) return launch_bwd_rows<T, G, 32, kFull, kAligned>(a, to, parts);
+    if (a.d <= 128 * E) return launch_bwd_rows<T, G, 128, kFull, kAligned>(a, to, parts);
+    if (a.d <= 256 * E) return launch_bwd_rows<T, G, 256, kFull, kAligned>(a, to, parts);
+    return launch_bwd_rows<T, G, 512, kFull, kAligned>(a, to, parts);
 }
 
 template <class T, class G>
-flp_status launch_norm_bwd(const flp::NormBwdArgs& a, bool vec, int dev, cudaStream_t s, int* parts) {
+flp_status launch_norm_bwd(const flp::NormBwdArgs& a, bool vec, const NormTo& to, int* parts) {
     const bool center = a.mean != nullptr, full = center || a.part_b != nullptr;
     if (a.d > 512 * flp::kNormElems)
-        return center ? launch_bwd_any<T, G, true>(a, s, parts) : launch_bwd_any<T, G, false>(a, s, parts);
+        return center ? launch_bwd_any<T, G, true>(a, to, parts) : launch_bwd_any<T, G, false>(a, to, parts);
     if (vec)
-        return full ? launch_bwd_v<T, G, true, true>(a, dev, s, parts) : launch_bwd_v<T, G, false, true>(a, dev, s, parts);
-    return full ? launch_bwd_v<T, G, true, false>(a, dev, s, parts) : launch_bwd_v<T, G, false, false>(a, dev, s, parts);
+        return full ? launch_bwd_v<T, G, true, true>(a, to, parts) : launch_bwd_v<T, G, false, true>(a, to, parts);
+    return full ? launch_bwd_v<T, G, true, false>(a, to, parts) : launch_bwd_v<T, G, false, false>(a, to, parts);
 }
 
 bool norm_workspace_bytes(int64_t d, int64_t* out) {
@@ -108,22 +117,10 @@ bool norm_workspace_bytes(int64_t d, int64_t* out) {
     return true;
 }
 
-}  // namespace
-
-extern "C" {
-
-flp_status fused_layer_norm_backward_workspace_size(int64_t d, int64_t* bytes) {
-    if (bytes == nullptr) return fail(FLP_EINVAL, "bytes is a null pointer");
-    if (d < 1) return fail(FLP_EINVAL, "d must be >= 1 (got %lld)", (long long)d);
-    if (!norm_workspace_bytes(d, bytes)) return fail(FLP_EINVAL, "workspace size overflows int64");
-    return ok();
-}
-
-flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy, const void* x, int dtype, int64_t n,
-                                     int64_t d, int64_t ld_x, const void* weight, int weight_dtype, const float* mean,
-                                     const float* rstd, int center, void* workspace, int64_t workspace_bytes, void* dx,
-                                     int64_t ld_dx, float* dweight, float* dbias, int accumulate,
-                                     flp_stream_t stream) {
+flp_status norm_backward(int sms, const void* dy, int dy_dtype, int64_t ld_dy, const void* x, int dtype, int64_t n,
+                         int64_t d, int64_t ld_x, const void* weight, int weight_dtype, const float* mean,
+                         const float* rstd, int center, void* workspace, int64_t workspace_bytes, void* dx,
+                         int64_t ld_dx, float* dweight, float* dbias, int accumulate, flp_stream_t stream) {
     flp_status st;
     if ((st = check_norm_shape(n, d, dtype)) != FLP_OK) return st;
     if ((st = check_side_dtype("weight", weight_dtype, dtype)) != FLP_OK) return st;
@@ -179,18 +176,49 @@ flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy
     const bool wide = dy_dtype == FLP_DTYPE_F32;
     const bool vec = (d * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) && rows_aligned16(dx, ld_dx, dtype) &&
                      rows_aligned16(dy, ld_dy, dy_dtype) && aligned16(weight);
+    const NormTo to{dev, sms, s};
     int parts = 0;
     if (dtype == FLP_DTYPE_BF16)
-        st = wide ? launch_norm_bwd<__nv_bfloat16, float>(a, vec, dev, s, &parts)
-                  : launch_norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, vec, dev, s, &parts);
+        st = wide ? launch_norm_bwd<__nv_bfloat16, float>(a, vec, to, &parts)
+                  : launch_norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, vec, to, &parts);
     else if (dtype == FLP_DTYPE_F16)
-        st = wide ? launch_norm_bwd<__half, float>(a, vec, dev, s, &parts)
-                  : launch_norm_bwd<__half, __half>(a, vec, dev, s, &parts);
+        st = wide ? launch_norm_bwd<__half, float>(a, vec, to, &parts)
+                  : launch_norm_bwd<__half, __half>(a, vec, to, &parts);
     else
-        st = launch_norm_bwd<float, float>(a, vec, dev, s, &parts);
+        st = launch_norm_bwd<float, float>(a, vec, to, &parts);
     if (st != FLP_OK || parts == 0) return st;
     return launch_dependent("norm fold", flp::k_norm_fold<flp::kNormFoldThreads>, dim3((unsigned)(2 * ceil_div(d, 8))), flp::kNormFoldThreads,
                             (size_t)0, s, a, parts);
+}
+
+}  // namespace
+
+extern "C" {
+
+flp_status fused_layer_norm_backward_workspace_size(int64_t d, int64_t* bytes) {
+    if (bytes == nullptr) return fail(FLP_EINVAL, "bytes is a null pointer");
+    if (d < 1) return fail(FLP_EINVAL, "d must be >= 1 (got %lld)", (long long)d);
+    if (!norm_workspace_bytes(d, bytes)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    return ok();
+}
+
+flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy, const void* x, int dtype, int64_t n,
+                                     int64_t d, int64_t ld_x, const void* weight, int weight_dtype, const float* mean,
+                                     const float* rstd, int center, void* workspace, int64_t workspace_bytes, void* dx,
+                                     int64_t ld_dx, float* dweight, float* dbias, int accumulate,
+                                     flp_stream_t stream) {
+    return norm_backward(kNormSms, dy, dy_dtype, ld_dy, x, dtype, n, d, ld_x, weight, weight_dtype, mean, rstd, center,
+                         workspace, workspace_bytes, dx, ld_dx, dweight, dbias, accumulate, stream);
+}
+
+flp_status flp_selftest_norm_backward(int sms, const void* dy, int dy_dtype, int64_t ld_dy, const void* x, int dtype,
+                                      int64_t n, int64_t d, int64_t ld_x, const void* weight, int weight_dtype,
+                                      const float* mean, const float* rstd, int center, void* workspace,
+                                      int64_t workspace_bytes, void* dx, int64_t ld_dx, float* dweight, float* dbias,
+                                      int accumulate, flp_stream_t stream) {
+    if (sms < 1 || sms > kNormSms) return fail(FLP_EINVAL, "sms must be in [1, %d] (got %d)", kNormSms, sms);
+    return norm_backward(sms, dy, dy_dtype, ld_dy, x, dtype, n, d, ld_x, weight, weight_dtype, mean, rstd, center,
+                         workspace, workspace_bytes, dx, ld_dx, dweight, dbias, accumulate, stream);
 }
 
 }  // extern "C"

@@ -639,9 +639,10 @@ k_norm_fwd(NormFwdArgs a) {
     }
 }
 
-// dx and this CTA's partial row of dw (and db): `parts` CTAs have rows.  They are
-// folded after a barrier of the grid (a cooperative launch; `grid_fold`), saving the
-// launch of k_norm_fold: it costs a caller as much as the kernel on small batches.
+// dx and this CTA's partial row of dw (and db): the first `parts` CTAs step through the
+// rows.  The partial rows are folded after a barrier of the grid (a cooperative launch;
+// `grid_fold`), saving the launch of k_norm_fold: it costs a caller as much as the kernel
+// on small batches.
 // kFull: with centring (unless a.mean is null) and db; else RMS norm without db.
 template <class T, class G, int kTpr, bool kFull, bool kAligned>
 __global__ void __launch_bounds__(kNormThreads<kTpr>, kNormBwdCtas<kTpr>)
@@ -652,8 +653,9 @@ k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
     __shared__ float red[2 * 64];
     int turn = 0;
     const int t = threadIdx.x % kTpr, d = (int)a.d, nvec = (d + V - 1) / V;
-    const int64_t step = (int64_t)gridDim.x * kRows;
-    int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / kTpr;
+    // the CTAs from `parts` on are here for the fold alone: no row of theirs has a partial row
+    const int64_t step = (int64_t)parts * kRows;
+    int64_t r = ((int)blockIdx.x < parts ? (int64_t)blockIdx.x * kRows : a.n) + threadIdx.x / kTpr;
     // kAligned: the thread's places; else the rows' slots, and after the ring the staged dx
     const uint32_t xpitch = kAligned ? kThreads * kNormElems * (uint32_t)sizeof(T) : norm_pitch<T>(d) * kRows;
     const uint32_t pitch = xpitch + (kAligned ? kThreads * kNormElems * (uint32_t)sizeof(G) : norm_pitch<G>(d) * kRows);

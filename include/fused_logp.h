@@ -674,9 +674,9 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
  * The products run on FP16 operands with FP32 accumulators; X is carried as
  * two FP16 numbers (22 bits) and the diagonals of A and b A + c A^2 in FP32, so
  * that out is within about 1e-3 (of its norm) of the result in 64 bits also
- * where G has few large singular values over a small floor.  The sum of squares
- * is FP32 (entries between about 1e-19 and 1e17 in size).  A zero
- * matrix gives zeros; an infinity or NaN makes its matrix NaN.  Deterministic:
+ * where G has few large singular values over a small floor.  The squares are
+ * scaled where FP32 would not hold their sum, so that every finite G counts.  A zero
+ * matrix gives zeros (with eps == 0 too); an infinity or NaN makes its matrix NaN.  Deterministic:
  * equal calls give equal bits (the order of the sums over K depends on the
  * sizes and the batch).
  * Errors: FLP_EINVAL for a bad dtype, extent, stride, steps, coefficient, eps,

@@ -93,7 +93,7 @@ k_orth_cluster(const __grid_constant__ OrthCluArgs p) {
     const uint32_t base = (raw + 1023u) & ~1023u;   // the same offset in every CTA
     const uint32_t sx = base + kOrthCluX, sa = base + kOrthCluA, sp = base + kOrthCluP, sd = base + kOrthCluD,
                    se = base + kOrthCluE, sums = base + kOrthCluMisc, bar = sums + 64, slot = sums + 80,
-                   red = sums + 96;
+                   red = sums + 96, sums_top = sums + 128, sums_again = sums + 192;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3, half = warp >> 2;
     const int row = quarter * 32 + lane;
@@ -190,22 +190,52 @@ k_orth_cluster(const __grid_constant__ OrthCluArgs p) {
         }
     }
     tmem_st_wait();
-    float s = (sq[0] + sq[1]) + (sq[2] + sq[3]);
+    // Sum (or largest) of t over the cluster, the same in every thread; by way of `to`,
+    // a float for every CTA that no other call uses.
+    auto over_cluster = [&](float t, uint32_t to, auto join) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) sts_f32(red + 4 * warp, s);
-    __syncthreads();
-    if (threadIdx.x < ctas) {   // this CTA's sum into every CTA
-        float t = 0.f;
-        for (int w = 0; w < kOrthCluThreads / 32; ++w) t += lds_f32(red + 4 * w);
-        dsm_st(map_to_rank(sums + 4 * rank, threadIdx.x), t);
+        for (int o = 16; o >= 1; o >>= 1) t = join(t, __shfl_xor_sync(0xffffffffu, t, o));
+        if (lane == 0) sts_f32(red + 4 * warp, t);
+        __syncthreads();
+        if (threadIdx.x < ctas) {   // this CTA's into every CTA
+            t = 0.f;
+            for (int w = 0; w < kOrthCluThreads / 32; ++w) t = join(t, lds_f32(red + 4 * w));
+            dsm_st(map_to_rank(to + 4 * rank, threadIdx.x), t);
+        }
+        __syncwarp();
+        cluster_sync_all();
+        t = 0.f;
+        for (uint32_t k = 0; k < ctas; ++k) t = join(t, lds_f32(to + 4 * k));
+        return t;
+    };
+    auto add = [](float a, float b) { return a + b; };
+    OrthSum total{over_cluster((sq[0] + sq[1]) + (sq[2] + sq[3]), sums, add), 0};
+    if (!orth_sum_plain(total.s)) {   // alike in the whole cluster: as in the partial sums
+        auto each = [&](auto take) {
+            for (int c = half; rows_here && c < chunks; c += 2) {
+                uint32_t r[32];
+                __syncwarp();
+                tmem_ld32(lanes + 32 * c, r);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) take(j, __uint_as_float(r[j]));
+            }
+        };
+        float top = 0.f;
+        each([&](int, float v) { top = fmaxf(top, fabsf(v)); });
+        top = over_cluster(top, sums_top, [](float a, float b) { return fmaxf(a, b); });
+        if (top > 0.f && isfinite(top)) {
+            total.e = ilogbf(top);
+            const float2 by = orth_scale_of(total.e);
+            float again[4] = {0.f, 0.f, 0.f, 0.f};   // in the first sum's order
+            each([&](int j, float v) {
+                v = v * by.x * by.y;
+                again[j & 3] += v * v;
+            });
+            total.s = over_cluster((again[0] + again[1]) + (again[2] + again[3]), sums_again, add);
+        }
     }
-    __syncwarp();
-    cluster_sync_all();
-    float total = 0.f;
-    for (uint32_t k = 0; k < ctas; ++k) total += lds_f32(sums + 4 * k);
-    // tensor memory holds kOrthScale^2 X; an infinite sum of squares makes X NaN
-    float mult = isfinite(total) ? kOrthScale * kOrthScale / (__fsqrt_rn(total) + p.eps) : __int_as_float(0x7fc00000);
+    // tensor memory holds kOrthScale^2 X
+    float2 mult = orth_inverse(total, p.eps, kOrthScale * kOrthScale);
 
     constexpr float kInv = 1.f / kOrthScale;
     for (int step = 0;; ++step) {
@@ -217,7 +247,7 @@ k_orth_cluster(const __grid_constant__ OrthCluArgs p) {
                 tmem_ld32(lanes + 32 * c, r);
                 float v[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * mult;
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * mult.x * mult.y;
                 if (step == 0) tmem_st32(lanes + 32 * c, v);
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -229,7 +259,7 @@ k_orth_cluster(const __grid_constant__ OrthCluArgs p) {
             }
             if (step == 0) tmem_st_wait();
         }
-        mult = 1.f;
+        mult = {1.f, 1.f};
         fence_proxy_async_smem();
         tc_fence_before();
         __syncthreads();

@@ -43,6 +43,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <limits.h>
 
 #include "tc_prims.cuh"
 
@@ -985,6 +986,21 @@ k_orth_split(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 
 // ---------------------------------------------------------------- the input
 
+// A sum of squares, s 4^e.  e is 0 unless the FP32 sum of the squares themselves
+// would overflow or lose what underflows.
+struct OrthSum {
+    float s;
+    int e;
+};
+constexpr float kOrthSumLow = 0x1p-60f, kOrthSumHigh = 0x1p100f;   // between them it is taken as it is
+// 2^-e as two factors (2^-e itself may be out of range): values below 2^(e + 1) take the
+// first, then the second, without overflow.
+__device__ __forceinline__ float2 orth_scale_of(int e) {
+    const int h = e / 2;
+    return make_float2(__int_as_float((127 - h) << 23), __int_as_float((127 - (e - h)) << 23));
+}
+__device__ __forceinline__ bool orth_sum_plain(float s) { return s >= kOrthSumLow && s <= kOrthSumHigh; }
+
 struct OrthInput {
     const void* x;            // [rows, ld] of T, matrices `stride` elements apart
     int64_t rows, cols, ld, stride;
@@ -994,7 +1010,7 @@ struct OrthInput {
     int vec;                  // rows of x are whole, aligned 16-byte vectors
     int parts;                // partial sums of a matrix, at most 256
     float eps;
-    float* sums;              // [batch, parts]
+    OrthSum* sums;            // [batch, parts]
     __half *hi, *lo;          // [batch mp, np]
     int64_t mp, np;
 };
@@ -1015,17 +1031,22 @@ __device__ __forceinline__ void orth_vec(const T* p, float (&v)[16 / sizeof(T)])
 // a run of a row at a time (whole rows left most warps without one where a part
 // has few: a call on 8 x 1024 x 4096 took 679 us, now 672).
 constexpr int kOrthSumThreads = 512;
-template <class T>
-__global__ void __launch_bounds__(kOrthSumThreads)
-k_orth_sumsq(OrthInput p) {
+// A thread's share of it (kOrthSquares), of the scaled values' (kOrthScaled), or its largest |x|.
+enum OrthSumKind { kOrthSquares = 0, kOrthScaled = 1, kOrthLargest = 2 };
+template <class T, int kKind>
+__device__ __forceinline__ float orth_part(const OrthInput& p, const T* x, int q, float2 by = {1.f, 1.f}) {
     constexpr int V = 16 / sizeof(T);
-    __shared__ float red[kOrthSumThreads / 32];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t b = blockIdx.x / p.parts;
-    const int q = (int)(blockIdx.x - b * p.parts), lane = threadIdx.x & 31;
-    const T* x = static_cast<const T*>(p.x) + b * p.stride;
+    const int lane = threadIdx.x & 31;
     const int64_t rows = (p.rows - q + p.parts - 1) / p.parts;
     float s[4] = {0.f, 0.f, 0.f, 0.f};   // four chains: the adds of one would wait on each other
+    auto take = [&](float& t, float v) {
+        if (kKind == kOrthLargest) {
+            t = fmaxf(t, fabsf(v));
+        } else {
+            if (kKind == kOrthScaled) v = v * by.x * by.y;
+            t += v * v;
+        }
+    };
     // a run: four vectors a lane, or 16 values of unaligned rows
     const int64_t have = p.vec ? p.cols / V : p.cols, runs = (have + (p.vec ? 127 : 511)) / (p.vec ? 128 : 512);
     for (int64_t u = threadIdx.x >> 5; u < rows * runs; u += kOrthSumThreads / 32) {
@@ -1041,27 +1062,58 @@ k_orth_sumsq(OrthInput p) {
             for (int k = 0; k < 4; ++k)
                 if (c + 32 * k < have)
 #pragma unroll
-                    for (int j = 0; j < V; ++j) s[k] += v[k][j] * v[k][j];
+                    for (int j = 0; j < V; ++j) take(s[k], v[k][j]);
         } else {
             const int64_t c = (u - r * runs) * 512 + lane;
             float v[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = c + 32 * k < have ? orth_f32(row[c + 32 * k]) : 0.f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) s[k & 3] += v[k] * v[k];
+            for (int k = 0; k < 16; ++k) take(s[k & 3], v[k]);
         }
     }
-    float t = (s[0] + s[1]) + (s[2] + s[3]);
+    if (kKind == kOrthLargest) return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+// Its sum (or largest) over the CTA, the same in every thread.
+template <bool kLargest>
+__device__ __forceinline__ float orth_cta(float t, float* red) {
+    auto join = [](float a, float b) { return kLargest ? fmaxf(a, b) : a + b; };
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    for (int o = 16; o >= 1; o >>= 1) t = join(t, __shfl_xor_sync(0xffffffffu, t, o));
+    __syncthreads();   // the last one's readers
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        t = threadIdx.x < kOrthSumThreads / 32 ? red[threadIdx.x] : 0.f;
+    t = (threadIdx.x & 31) < kOrthSumThreads / 32 ? red[threadIdx.x & 31] : 0.f;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (threadIdx.x == 0) p.sums[blockIdx.x] = t;
+    for (int o = 16; o >= 1; o >>= 1) t = join(t, __shfl_xor_sync(0xffffffffu, t, o));
+    return t;
+}
+template <class T>
+__global__ void __launch_bounds__(kOrthSumThreads, 2)
+k_orth_sumsq(OrthInput p) {
+    __shared__ float red[kOrthSumThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t b = blockIdx.x / p.parts;
+    const int q = (int)(blockIdx.x - b * p.parts);
+    const T* x = static_cast<const T*>(p.x) + b * p.stride;
+    OrthSum t{orth_cta<false>(orth_part<T, kOrthSquares>(p, x, q), red), 0};
+    if (!orth_sum_plain(t.s)) {   // again, with the largest scaled to between 1 and 2
+        const float top = orth_cta<true>(orth_part<T, kOrthLargest>(p, x, q), red);
+        if (top > 0.f && isfinite(top)) {   // else zeros, or nothing that a scale would mend
+            t.e = ilogbf(top);
+            t.s = orth_cta<false>(orth_part<T, kOrthScaled>(p, x, q, orth_scale_of(t.e)), red);
+        }
     }
+    if (threadIdx.x == 0) p.sums[blockIdx.x] = t;
+}
+
+// `by` / (|x| + eps) as two factors, for a matrix of the sum of squares t: 0 for a matrix of
+// zeros, NaN where the sum is not finite.
+__device__ __forceinline__ float2 orth_inverse(OrthSum t, float eps, float by) {
+    if (!isfinite(t.s)) return make_float2(1.f, __int_as_float(0x7fc00000));
+    const float2 f = orth_scale_of(t.e);
+    return make_float2(f.x, t.s > 0.f ? by / (__fsqrt_rn(t.s) + eps * f.x * f.y) * f.y : 0.f);
 }
 
 // X (hi, lo) = x / (|x| + eps), zero in the padding: a 64 x 64 tile of X a turn,
@@ -1069,28 +1121,36 @@ k_orth_sumsq(OrthInput p) {
 // are aligned vectors already in X's order.
 constexpr int kOrthLoadThreads = 256;
 template <class T>
-__global__ void __launch_bounds__(kOrthLoadThreads)
+__global__ void __launch_bounds__(kOrthLoadThreads, 5)
 k_orth_load(OrthInput p) {
     constexpr int V = 16 / sizeof(T);
     __shared__ float tile[64][65];
-    __shared__ float s_inv;
+    __shared__ float2 s_inv;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     orth_dep_wait();   // the partial sums
     int64_t have = -1;
-    float inv = 0.f;
+    float2 inv = {0.f, 0.f};
     for (int64_t u = blockIdx.x; u < p.all_tiles; u += gridDim.x) {
         const int64_t b = u / p.tiles, t = u - b * p.tiles;
         const int64_t j0 = t / p.tiles_m * 64, i0 = t % p.tiles_m * 64;
         if (b != have) {   // the matrix's scale
             __syncthreads();
             if (threadIdx.x < 32) {
-                float s = 0.f;
-                for (int k = threadIdx.x; k < p.parts; k += 32) s += __ldcg(p.sums + b * p.parts + k);
+                const int2* sums = reinterpret_cast<const int2*>(p.sums + b * p.parts);
+                OrthSum w{0.f, INT_MIN};   // the largest exponent of a part that is not 0
+                for (int k = threadIdx.x; k < p.parts; k += 32) {
+                    const int2 q = __ldcg(sums + k);
+                    if (__int_as_float(q.x) != 0.f) w.e = max(w.e, q.y);
+                }
+                w.e = __reduce_max_sync(0xffffffffu, w.e);
+                if (w.e == INT_MIN) w.e = 0;
+                for (int k = threadIdx.x; k < p.parts; k += 32) {
+                    const int2 q = __ldcg(sums + k);
+                    w.s += q.y == w.e ? __int_as_float(q.x) : ldexpf(__int_as_float(q.x), 2 * (q.y - w.e));
+                }
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                // an infinite sum of squares (FP32 overflow) makes X NaN, not 0
-                if (threadIdx.x == 0)
-                    s_inv = isfinite(s) ? kOrthScale / (__fsqrt_rn(s) + p.eps) : __int_as_float(0x7fc00000);
+                for (int o = 16; o >= 1; o >>= 1) w.s += __shfl_xor_sync(0xffffffffu, w.s, o);
+                if (threadIdx.x == 0) s_inv = orth_inverse(w, p.eps, kOrthScale);
             }
             __syncthreads();
             inv = s_inv;
@@ -1134,7 +1194,7 @@ k_orth_load(OrthInput p) {
             uint32_t hw[4], lw[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float x0 = v[2 * q] * inv, x1 = v[2 * q + 1] * inv;
+                const float x0 = v[2 * q] * inv.x * inv.y, x1 = v[2 * q + 1] * inv.x * inv.y;
                 hw[q] = orth_pack(x0, x1);
                 lw[q] = orth_pack((x0 - h_lo(hw[q])) * kOrthLoScale, (x1 - h_hi(hw[q])) * kOrthLoScale);
             }

@@ -27,7 +27,7 @@ bool orth_layout(int64_t batch, int64_t rows, int64_t cols, OrthLayout* l) {
     if (x > INT64_MAX / 16 || a > INT64_MAX / 16) return false;
     auto up = [](int64_t v) { return ceil_div(v, 1024) * 1024; };
     l->parts = 0;
-    l->d = up(batch * flp::kOrthParts * 4);
+    l->d = up(batch * flp::kOrthParts * (int64_t)sizeof(flp::OrthSum));
     l->e = l->d + up(all_rows * 4);
     l->hi0 = l->e + up(all_rows * 4);
     l->hi1 = l->hi0 + up(x);
@@ -429,7 +429,7 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     parts = parts < rows ? parts : rows;
     in.parts = (int)(parts < flp::kOrthParts ? parts : flp::kOrthParts);
     in.eps = eps;
-    in.sums = reinterpret_cast<float*>(ws + l.parts);
+    in.sums = reinterpret_cast<flp::OrthSum*>(ws + l.parts);
     in.hi = hi[0];
     in.lo = lo;
     in.mp = l.mp;

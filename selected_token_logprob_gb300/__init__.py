@@ -38,7 +38,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._args import _cuda, _dtype, _mask, _opt_ptr, _rows, _stream, _vec
+from ._args import _cuda, _dtype, _mask, _opt_ptr, _rows, _stream, _vec, _workspace
 from ._lib import FusedLogpError
 from .norm import (FusedLayerNorm, fused_layer_norm, fused_layer_norm_backward,
                    fused_layer_norm_backward_workspace_size, fused_layer_norm_forward)
@@ -385,13 +385,12 @@ def logp_grpo_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch
         if counted:
             raise ValueError("counted=True needs the workspace that holds the counts")
         workspace = torch.empty(logp_grpo_loss_workspace_size(n, nseq), dtype=torch.uint8, device=dev)
-    _cuda(workspace)
+    wptr, wbytes = _workspace(workspace)
     fn = "logp_grpo_loss_counted" if counted else "logp_grpo_loss"
     st = getattr(_lib.load(), fn)(logp.data_ptr(), old_logp.data_ptr(), _opt_ptr(ref_logp),
                                   advantages.data_ptr(), mp, _opt_ptr(cu_seqlens), nseq, n,
                                   GRPO_MODES[mode], float(eps_lo), float(eps_hi), float(beta),
-                                  float(normalizer), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), loss.data_ptr(),
+                                  float(normalizer), wptr, wbytes, loss.data_ptr(),
                                   grad.data_ptr(), _opt_ptr(tl), _stream(logp))
     _lib.check(fn, st)
     return (loss, grad, tl) if token_loss else (loss, grad)
@@ -416,11 +415,10 @@ def logp_grpo_loss_counts(n: int, active_mask: torch.Tensor | None = None,
         if ref is None:
             raise ValueError("give the workspace when there is neither a mask nor cu_seqlens")
         workspace = torch.empty(logp_grpo_loss_workspace_size(n, nseq), dtype=torch.uint8, device=ref.device)
-    _cuda(workspace)
+    wptr, wbytes = _workspace(workspace)
     s = stream if stream is not None else torch.cuda.current_stream(workspace.device)
     st = _lib.load().logp_grpo_loss_counts(mp, _opt_ptr(cu_seqlens), nseq, n, GRPO_MODES[mode],
-                                           float(normalizer), workspace.data_ptr(),
-                                           workspace.numel() * workspace.element_size(), s.cuda_stream)
+                                           float(normalizer), wptr, wbytes, s.cuda_stream)
     _lib.check("logp_grpo_loss_counts", st)
     return workspace
 
@@ -483,11 +481,10 @@ def fused_linear_logp_forward(hidden: torch.Tensor, weight: torch.Tensor, target
         need = fused_linear_logp_workspace_size(n, v)
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _cuda(workspace)
-        wbytes = workspace.numel() * workspace.element_size()
+        wptr, wbytes = _workspace(workspace)
         st = _lib.load().fused_linear_logp_forward(
             hidden.data_ptr(), n, d, ld_h, weight.data_ptr(), v, ld_w, targets.data_ptr(),
-            int(ignore_index), mp, inv_t, workspace.data_ptr(), wbytes, logp.data_ptr(),
+            int(ignore_index), mp, inv_t, wptr, wbytes, logp.data_ptr(),
             lse.data_ptr(), _opt_ptr(lse_lo), _stream(hidden))
         _lib.check("fused_linear_logp_forward", st)
     return (logp, lse, lse_lo) if want_lo else (logp, lse)
@@ -547,8 +544,7 @@ def fused_linear_logp_backward(hidden: torch.Tensor, weight: torch.Tensor, targe
     if workspace is None:
         wptr, wbytes = None, 0
     else:
-        _cuda(workspace)
-        wptr, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        wptr, wbytes = _workspace(workspace)
     st = _lib.load().fused_linear_logp_backward(
         hidden.data_ptr(), n, d, ld_h, weight.data_ptr(), v, ld_w, targets.data_ptr(), int(ignore_index), mp,
         inv_t, lse.data_ptr(), _opt_ptr(lse_lo), grad.data_ptr(), wptr, wbytes, dhidden.data_ptr(), ld_dh,
@@ -631,11 +627,11 @@ def fused_linear_logp_shard_partials(hidden: torch.Tensor, weight_shard: torch.T
     if d_w != d:
         raise ValueError(f"hidden has {d} columns but weight_shard has {d_w}")
     _vec(targets, "targets", n, torch.int64)
-    _cuda(hidden, weight_shard, targets, workspace)
+    _cuda(hidden, weight_shard, targets)
+    wptr, wbytes = _workspace(workspace)
     st = _lib.load().fused_linear_logp_shard_partials(
         hidden.data_ptr(), n, d, ld_h, weight_shard.data_ptr(), w, ld_w, int(vocab_start), int(v_total),
-        targets.data_ptr(), _inv_temperature(temperature), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(hidden))
+        targets.data_ptr(), _inv_temperature(temperature), wptr, wbytes, _stream(hidden))
     _lib.check("fused_linear_logp_shard_partials", st)
 
 
@@ -649,10 +645,11 @@ def fused_linear_logp_merge(workspace: torch.Tensor, v_total: int, targets: torc
     logp = torch.empty(n, dtype=torch.float32, device=dev)
     lse = torch.empty(n, dtype=torch.float32, device=dev)
     lse_lo = torch.empty(n, dtype=torch.float32, device=dev) if with_lse_lo else None
-    _cuda(workspace, targets)
+    _cuda(targets)
+    wptr, wbytes = _workspace(workspace)
     mp = _mask(active_mask, n)
     st = _lib.load().fused_linear_logp_merge(
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), n, int(v_total), targets.data_ptr(),
+        wptr, wbytes, n, int(v_total), targets.data_ptr(),
         int(ignore_index), mp, _inv_temperature(temperature), logp.data_ptr(), lse.data_ptr(), _opt_ptr(lse_lo),
         _stream(targets))
     _lib.check("fused_linear_logp_merge", st)
@@ -742,8 +739,7 @@ def fused_linear_logp_shard_backward(hidden: torch.Tensor, weight_shard: torch.T
     mp = _mask(active_mask, n)
     if workspace is None and n > 0:
         workspace = torch.empty(fused_linear_logp_backward_workspace_size(d, w), dtype=torch.uint8, device=dev)
-    wptr, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                        workspace.numel() * workspace.element_size())
+    wptr, wbytes = (None, 0) if workspace is None else _workspace(workspace)
     st = _lib.load().fused_linear_logp_shard_backward(
         hidden.data_ptr(), n, d, ld_h, weight_shard.data_ptr(), w, ld_w, int(vocab_start), int(v_total),
         targets.data_ptr(), int(ignore_index), mp, _inv_temperature(temperature), lse.data_ptr(), _opt_ptr(lse_lo),

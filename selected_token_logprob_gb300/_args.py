@@ -47,6 +47,15 @@ def _cuda(*ts) -> None:
             raise ValueError("all tensors must be CUDA tensors")
 
 
+def _workspace(t: torch.Tensor):
+    """(pointer, bytes) of a scratch tensor.  A strided or expanded one would not own
+    the bytes that its element count gives, and the kernels would write past it."""
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _cuda(t)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _opt_ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 

@@ -8,7 +8,7 @@ import functools
 import torch
 
 from . import _lib
-from ._args import _DTYPES, _cuda, _dtype, _stream
+from ._args import _DTYPES, _cuda, _dtype, _stream, _workspace
 
 #: (a, b, c) of the usual quintic step X <- a X + (b A + c A^2) X, A = X X^T.
 ORTHOGONALIZE_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
@@ -61,11 +61,11 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=ORTHOGONALIZE_CO
         return out
     if workspace is None:
         workspace = torch.empty(orthogonalize_workspace_size(batch, rows, cols), dtype=torch.uint8, device=x.device)
-    _cuda(workspace)
+    wptr, wbytes = _workspace(workspace)
     coef = (ctypes.c_float * (3 * steps))(*[float(v) for t in flat for v in t])
     st = _lib.load().flp_orthogonalize(
-        x.data_ptr(), dt, batch, rows, cols, ld, stride, steps, coef, float(eps), float(scale), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), out.data_ptr(), _DTYPES[out.dtype], ld_out, stride_out,
+        x.data_ptr(), dt, batch, rows, cols, ld, stride, steps, coef, float(eps), float(scale), wptr, wbytes,
+        out.data_ptr(), _DTYPES[out.dtype], ld_out, stride_out,
         _stream(x))
     _lib.check("flp_orthogonalize", st)
     return out

@@ -9,7 +9,7 @@ import functools
 import torch
 
 from . import _lib
-from ._args import _DTYPES, _cuda, _dtype, _opt_ptr, _rows, _stream, _vec
+from ._args import _DTYPES, _cuda, _dtype, _opt_ptr, _rows, _stream, _vec, _workspace
 
 
 def _affine(weight, bias, x, d: int) -> int:
@@ -134,8 +134,7 @@ def fused_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.T
     dbias = _sum_output("dbias", dbias, with_dbias, accumulate, d, dev)
     wptr, wbytes = None, 0
     if workspace is not None:
-        _cuda(workspace)
-        wptr, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        wptr, wbytes = _workspace(workspace)
     elif n > 0 and (with_dweight or with_dbias):
         wbytes = fused_layer_norm_backward_workspace_size(d)
         workspace = torch.empty(wbytes, dtype=torch.uint8, device=dev)

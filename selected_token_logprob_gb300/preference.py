@@ -8,7 +8,7 @@ import functools
 import torch
 
 from . import _lib
-from ._args import _cuda, _mask, _opt_ptr, _stream, _vec
+from ._args import _cuda, _mask, _opt_ptr, _stream, _vec, _workspace
 
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 PREFERENCE_LAYOUTS = {"interleaved": 0, "halves": 1}
@@ -53,15 +53,12 @@ def logp_preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, ref_logp:
     grad = torch.empty(n, dtype=torch.float32, device=dev)
     rewards = torch.empty((nseq // 2, 2), dtype=torch.float32, device=dev)
     if workspace is None:
-        wbytes = logp_preference_loss_workspace_size(n, nseq)
-        workspace = torch.empty(wbytes, dtype=torch.uint8, device=dev)
-    else:
-        _cuda(workspace)
-        wbytes = workspace.numel() * workspace.element_size()
+        workspace = torch.empty(logp_preference_loss_workspace_size(n, nseq), dtype=torch.uint8, device=dev)
+    wptr, wbytes = _workspace(workspace)
     st = _lib.load().logp_preference_loss(
         logp.data_ptr(), _opt_ptr(ref_logp), mp, cu_seqlens.data_ptr(), nseq, n, PREFERENCE_KINDS[kind],
         PREFERENCE_LAYOUTS[layout], 1 if average else 0, beta, label_smoothing, margin, normalizer,
-        workspace.data_ptr(), wbytes, loss.data_ptr(), grad.data_ptr(), rewards.data_ptr(), _stream(logp))
+        wptr, wbytes, loss.data_ptr(), grad.data_ptr(), rewards.data_ptr(), _stream(logp))
     _lib.check("logp_preference_loss", st)
     return loss, grad, rewards
 

@@ -10,6 +10,7 @@ import torch
 
 from . import _lib
 from ._args import _DTYPES, _cuda, _dtype, _opt_ptr, _rows, _stream, _vec, _workspace
+from ._autograd import once
 
 
 def _affine(weight, bias, x, d: int) -> int:
@@ -171,7 +172,7 @@ class FusedLayerNorm(torch.autograd.Function):
             with_dbias=ctx.bias_dtype is not None and ctx.needs_input_grad[2])
         dw = dw if dw is None else dw.to(weight.dtype)
         db = db if db is None else db.to(ctx.bias_dtype)
-        return dx, dw, db, None, None
+        return *once((dx, dw, db), dy, x, weight), None, None
 
 
 def fused_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,

@@ -582,7 +582,8 @@ flp_status logp_grpo_loss_counted(const float* logp, const float* old_logp, cons
  *   dx     [n, ld_dx] of x's dtype, not overlapping x or dy
  *   dweight, dbias  [d] FP32 out, or NULL when not wanted; with `accumulate`
  *          they are added to (gradient accumulation over micro-batches)
- *   workspace  fused_layer_norm_backward_workspace_size(d) bytes, 16-byte
+ *   workspace  fused_layer_norm_backward_rows_workspace_size(n, d) bytes, or
+ *          fused_layer_norm_backward_workspace_size(d) whatever n is; 16-byte
  *          aligned, caller-owned, no initial contents needed (the partial
  *          sums of dweight and dbias); may be NULL without both
  * A row's y, mean, rstd and dx depend on that row (and the vectors) only;
@@ -596,6 +597,7 @@ flp_status fused_layer_norm_forward(const void* x, int dtype, int64_t n, int64_t
                                     const void* weight, const void* bias, int weight_dtype, float eps, int center,
                                     void* y, int64_t ld_y, float* mean, float* rstd, flp_stream_t stream);
 flp_status fused_layer_norm_backward_workspace_size(int64_t d, int64_t* bytes);
+flp_status fused_layer_norm_backward_rows_workspace_size(int64_t n, int64_t d, int64_t* bytes);
 flp_status fused_layer_norm_backward(const void* dy, int dy_dtype, int64_t ld_dy, const void* x, int dtype, int64_t n,
                                      int64_t d, int64_t ld_x, const void* weight, int weight_dtype, const float* mean,
                                      const float* rstd, int center, void* workspace, int64_t workspace_bytes, void* dx,

@@ -75,6 +75,7 @@ SIGNATURES = {
     "fused_layer_norm_forward": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int,
                                                 ctypes.c_float, ctypes.c_int, _P, _I64, _P, _P, _P]),
     "fused_layer_norm_backward_workspace_size": (ctypes.c_int, [_I64, ctypes.POINTER(_I64)]),
+    "fused_layer_norm_backward_rows_workspace_size": (ctypes.c_int, [_I64, _I64, ctypes.POINTER(_I64)]),
     "fused_layer_norm_backward": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, ctypes.c_int, _I64, _I64, _I64, _P,
                                                  ctypes.c_int, _P, _P, ctypes.c_int, _P, _I64, _P, _I64, _P, _P,
                                                  ctypes.c_int, _P]),

@@ -20,9 +20,9 @@ flp_status launch_bwd_any(const flp::NormBwdArgs& a, const NormTo& to, int* part
     const cudaStream_t s = to.s;
     flp::k_norm_dx_any<T, G, kCenter><<<row_ctas(a.n, 1, to.sms * 8), flp::kNormAnyThreads, 0, s>>>(a);
     if (a.part_w || a.part_b) {
-        const dim3 grid((unsigned)ceil_div(a.d, flp::kNormAnyThreads), flp::kNormAnyParts);
+        *parts = row_ctas(a.n, 1, flp::kNormAnyParts);
+        const dim3 grid((unsigned)ceil_div(a.d, flp::kNormAnyThreads), (unsigned)*parts);
         flp::k_norm_dw_any<T, G, kCenter><<<grid, flp::kNormAnyThreads, 0, s>>>(a);
-        *parts = flp::kNormAnyParts;
     }
     return check_launch("norm backward");
 }
@@ -110,9 +110,13 @@ flp_status launch_norm_bwd(const flp::NormBwdArgs& a, bool vec, const NormTo& to
     return full ? launch_bwd_v<T, G, true, false>(a, to, parts) : launch_bwd_v<T, G, false, false>(a, to, parts);
 }
 
-bool norm_workspace_bytes(int64_t d, int64_t* out) {
+// Most partial rows of n rows: a CTA that has one has a row.
+int64_t norm_parts(int64_t n) { return n < flp::kNormParts ? n : flp::kNormParts; }
+
+bool norm_workspace_bytes(int64_t n, int64_t d, int64_t* out) {
     int64_t b;
-    if (d > INT64_MAX - 4 || __builtin_mul_overflow((d + 3) / 4 * 4, (int64_t)(2 * flp::kNormParts * 4), &b)) return false;
+    if (d > INT64_MAX - 4 || __builtin_mul_overflow((d + 3) / 4 * 4, 8 * norm_parts(n), &b) || b > INT64_MAX - 256)
+        return false;
     *out = ceil_div(b, 256) * 256;
     return true;
 }
@@ -131,7 +135,7 @@ flp_status norm_backward(int sms, const void* dy, int dy_dtype, int64_t ld_dy, c
     const bool sums = dweight != nullptr || dbias != nullptr;
     if (n == 0 && !sums) return ok();
     int64_t need = 0;
-    if (!norm_workspace_bytes(d, &need)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    if (!norm_workspace_bytes(n, d, &need)) return fail(FLP_EINVAL, "workspace size overflows int64");
     if (sums && n > 0) {
         if (workspace_bytes < need)
             return fail(FLP_EINVAL, "workspace_bytes (%lld) is below the %lld bytes needed",
@@ -172,7 +176,7 @@ flp_status norm_backward(int sms, const void* dy, int dy_dtype, int64_t ld_dy, c
     const int64_t dp = ceil_div(d, 4) * 4;
     const flp::NormBwdArgs a{dy, ld_dy, x, n, d, ld_x, {weight, weight_dtype}, center ? mean : nullptr, rstd,
                              1.f / (float)d, dx, ld_dx, dp, dweight ? ws : nullptr,
-                             dbias ? ws + (int64_t)flp::kNormParts * dp : nullptr, dweight, dbias, accumulate != 0};
+                             dbias ? ws + norm_parts(n) * dp : nullptr, dweight, dbias, accumulate != 0};
     const bool wide = dy_dtype == FLP_DTYPE_F32;
     const bool vec = (d * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) && rows_aligned16(dx, ld_dx, dtype) &&
                      rows_aligned16(dy, ld_dy, dy_dtype) && aligned16(weight);
@@ -198,7 +202,15 @@ extern "C" {
 flp_status fused_layer_norm_backward_workspace_size(int64_t d, int64_t* bytes) {
     if (bytes == nullptr) return fail(FLP_EINVAL, "bytes is a null pointer");
     if (d < 1) return fail(FLP_EINVAL, "d must be >= 1 (got %lld)", (long long)d);
-    if (!norm_workspace_bytes(d, bytes)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    if (!norm_workspace_bytes(flp::kNormParts, d, bytes)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    return ok();
+}
+
+flp_status fused_layer_norm_backward_rows_workspace_size(int64_t n, int64_t d, int64_t* bytes) {
+    if (bytes == nullptr) return fail(FLP_EINVAL, "bytes is a null pointer");
+    if (n < 0) return fail(FLP_EINVAL, "n must be >= 0 (got %lld)", (long long)n);
+    if (d < 1) return fail(FLP_EINVAL, "d must be >= 1 (got %lld)", (long long)d);
+    if (!norm_workspace_bytes(n, d, bytes)) return fail(FLP_EINVAL, "workspace size overflows int64");
     return ok();
 }
 

@@ -63,13 +63,13 @@ struct NormBwdArgs {
     void* dx;
     int64_t ld_dx;
     int64_t dp;      // d rounded up to 4: a partial row
-    float* part_w;   // [kNormParts, dp] partial sums of dy xh, or null
-    float* part_b;   // [kNormParts, dp] partial sums of dy, or null
+    float* part_w;   // [min(n, kNormParts), dp] partial sums of dy xh, or null
+    float* part_b;   // [min(n, kNormParts), dp] partial sums of dy, or null
     float *dweight, *dbias;   // what the partial rows are folded into
     int accumulate;
 };
 
-// Rows of partial weight gradients: a constant, so that the order of the sum
+// Most rows of partial weight gradients: a constant, so that the order of the sum
 // over the batch depends on the problem alone.
 constexpr int kNormParts = 608;
 constexpr int kNormAnyThreads = 256;
@@ -146,7 +146,7 @@ k_norm_dx_any(NormBwdArgs a) {
     }
 }
 
-// Partial sums over the rows p, p + kNormAnyParts, ... of one column per thread.
+// Partial sums over the rows p, p + kNormAnyParts, ... of one column per thread, p < n.
 template <class T, class G, bool kCenter>
 __global__ void __launch_bounds__(kNormAnyThreads)
 k_norm_dw_any(NormBwdArgs a) {

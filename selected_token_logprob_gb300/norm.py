@@ -73,12 +73,17 @@ def fused_layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None
 
 
 @functools.lru_cache(maxsize=256)
-def fused_layer_norm_backward_workspace_size(d: int) -> int:
+def fused_layer_norm_backward_workspace_size(d: int, n: int | None = None) -> int:
     """Bytes of device scratch that fused_layer_norm_backward needs for the
-    partial sums of the weight's and bias's gradients."""
+    partial sums of the weight's and bias's gradients: for ``n`` rows, or for
+    any number of them."""
     b = ctypes.c_int64(0)
-    _lib.check("fused_layer_norm_backward_workspace_size",
-               _lib.load().fused_layer_norm_backward_workspace_size(int(d), ctypes.byref(b)))
+    if n is None:
+        _lib.check("fused_layer_norm_backward_workspace_size",
+                   _lib.load().fused_layer_norm_backward_workspace_size(int(d), ctypes.byref(b)))
+    else:
+        _lib.check("fused_layer_norm_backward_rows_workspace_size",
+                   _lib.load().fused_layer_norm_backward_rows_workspace_size(int(n), int(d), ctypes.byref(b)))
     return int(b.value)
 
 
@@ -137,7 +142,7 @@ def fused_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.T
     if workspace is not None:
         wptr, wbytes = _workspace(workspace)
     elif n > 0 and (with_dweight or with_dbias):
-        wbytes = fused_layer_norm_backward_workspace_size(d)
+        wbytes = fused_layer_norm_backward_workspace_size(d, n)
         workspace = torch.empty(wbytes, dtype=torch.uint8, device=dev)
         wptr = workspace.data_ptr()
     st = _lib.load().fused_layer_norm_backward(

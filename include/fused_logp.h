@@ -721,6 +721,16 @@ flp_status flp_selftest_wait_timeout(int device, int64_t limit_cycles, int* time
 flp_status flp_selftest_ex2_bias(int device, double* mean_rel_err, double* compensation);
 
 /*
+ * Self-test of the orthogonalised update's choice of kernels, on the host: *form is the
+ * form of a product of `batch` matrices with a side above 128 on `sms` SMs that hold
+ * `pairs` CTA pairs: 0 = a cluster a tile, 1 = persistent CTAs on 128 x 128 tiles, 2 =
+ * persistent pairs on 256 x 256 tiles.  product 0: the symmetric ones (X X^T, A^2),
+ * 1: those with X.
+ */
+flp_status flp_selftest_orthogonalize_form(int product, int64_t batch, int64_t rows, int64_t cols, int sms, int pairs,
+                                           int* form);
+
+/*
  * Self-test of the norm's backward where the rows' CTAs are fewer than those that
  * can be resident (as on a part with more SMs than the rows' grid is sized for, 152):
  * fused_layer_norm_backward with that grid sized for `sms` (1 to 152) of them.

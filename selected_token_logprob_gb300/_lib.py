@@ -79,6 +79,8 @@ SIGNATURES = {
     "fused_layer_norm_backward": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, ctypes.c_int, _I64, _I64, _I64, _P,
                                                  ctypes.c_int, _P, _P, ctypes.c_int, _P, _I64, _P, _I64, _P, _P,
                                                  ctypes.c_int, _P]),
+    "flp_selftest_orthogonalize_form": (ctypes.c_int, [ctypes.c_int, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int,
+                                                       ctypes.POINTER(ctypes.c_int)]),
     "flp_selftest_norm_backward": (ctypes.c_int, [ctypes.c_int, _P, ctypes.c_int, _I64, _P, ctypes.c_int, _I64, _I64,
                                                   _I64, _P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _I64, _P, _I64,
                                                   _P, _P, ctypes.c_int, _P]),

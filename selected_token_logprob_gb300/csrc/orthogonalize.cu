@@ -177,33 +177,42 @@ int orth_pairs(int dev) {
     return c;
 }
 
+// The form of a product of matrices of mp x np (both padded) on `sms` SMs that hold
+// `pairs` CTA pairs at once.
+enum OrthFormKind { kOrthFormSplit = 0, kOrthFormCta = 1, kOrthFormPair = 2 };
+OrthFormKind orth_form(bool sym, int64_t batch, int64_t mp, int64_t np, int sms, int pairs) {
+    const int64_t cols = sym ? mp : np, units = batch * orth_tiles(sym, mp, cols, 128, 128);
+    // Fewer 128 x 128 tiles than SMs: a tile a cluster, its K loop and its epilogue
+    // split over up to 4 CTAs (a call on 1024 x 1024: 135 us with the tiles below, 152
+    // unsplit, 117 split; 200 x 400: 90, 117, 89; 512 x 4096: 188, 193, 128).
+    if (units <= sms) return kOrthFormSplit;
+    // Else by the waves: 256 x 256 tiles a pair or 128 x 128 a CTA, a K block taking
+    // about 540 and 420 cycles (8 x 1024 x 4096: Gram's 80 pair tiles 68 us, its 288
+    // small ones 43; 4096 x 4096 in all 1064 and 1482 us).
+    const int64_t small = ceil_div(units, sms) * 420;
+    const int64_t wide = batch * orth_tiles(sym, mp, cols, 256, 256);
+    return pairs <= 0 || small <= ceil_div(wide, pairs) * 540 ? kOrthFormCta : kOrthFormPair;
+}
+
 template <int kMode>
 flp_status orth_product(int dev, int sms, int pairs, int64_t batch, const OrthMaps& t, flp::OrthArgs p, cudaStream_t s) {
     constexpr bool kSym = kMode == flp::kOrthGram || kMode == flp::kOrthPoly;
     const int64_t cols = kSym ? p.mp : p.np;
     p.nkb = (int)((kMode == flp::kOrthGram ? p.np : p.mp) / flp::kOrthBK);
+    const OrthFormKind form = orth_form(kSym, batch, p.mp, p.np, sms, pairs);
     auto shape = [&](int bm, int bn) {
         p.tiles_m = (int)ceil_div(p.mp, bm);
         p.tiles_n = (int)ceil_div(cols, bn);
         p.per = orth_tiles(kSym, p.mp, cols, bm, bn);
         p.units = batch * p.per;
     };
-    // Fewer 128 x 128 tiles than SMs: a tile a cluster, its K loop and its epilogue
-    // split over up to 4 CTAs (a call on 1024 x 1024: 135 us with the tiles below, 152
-    // unsplit, 117 split; 200 x 400: 90, 117, 89; 512 x 4096: 188, 193, 128).
     shape(128, 128);
-    if (p.units <= sms) {
+    if (form == kOrthFormSplit) {
         int split = 1;
         while (split < 4 && p.units * split * 2 <= sms && p.nkb >= 4) split *= 2;
         return orth_split_launch<kMode>(dev, split, t, p, s);
     }
-    // Else by the waves: 256 x 256 tiles a pair or 128 x 128 a CTA, a K block taking
-    // about 540 and 420 cycles (8 x 1024 x 4096: Gram's 80 pair tiles 68 us, its 288
-    // small ones 43; 4096 x 4096 in all 1064 and 1482 us).
-    const int64_t small = ceil_div(p.units, sms) * 420;
-    const int64_t wide = batch * orth_tiles(kSym, p.mp, cols, 256, 256);
-    if (pairs <= 0 || small <= ceil_div(wide, pairs) * 540)
-        return orth_launch<kMode, 128, false>(dev, sms, t, p, s);
+    if (form == kOrthFormCta) return orth_launch<kMode, 128, false>(dev, sms, t, p, s);
     shape(256, 256);
     return orth_launch<kMode, 256, true>(dev, pairs, t, p, s);
 }
@@ -311,6 +320,19 @@ flp_status flp_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t
     OrthLayout l;
     if (!orth_layout(batch, rows, cols, &l)) return fail(FLP_EINVAL, "workspace size overflows int64");
     *bytes = l.total;
+    return ok();
+}
+
+flp_status flp_selftest_orthogonalize_form(int product, int64_t batch, int64_t rows, int64_t cols, int sms, int pairs,
+                                           int* form) {
+    if (form == nullptr) return fail(FLP_EINVAL, "form is a null pointer");
+    if (product != 0 && product != 1) return fail(FLP_EINVAL, "product must be 0 or 1 (got %d)", product);
+    if (sms < 1) return fail(FLP_EINVAL, "sms must be >= 1 (got %d)", sms);
+    flp_status st;
+    if ((st = check_orth_shape(batch, rows, cols)) != FLP_OK) return st;
+    OrthLayout l;
+    if (!orth_layout(batch, rows, cols, &l)) return fail(FLP_EINVAL, "workspace size overflows int64");
+    *form = (int)orth_form(product == 0, batch, l.mp, l.np, sms, pairs);
     return ok();
 }
 

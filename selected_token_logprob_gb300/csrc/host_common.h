@@ -68,6 +68,8 @@ inline flp_status common_device(int count, const void* const* ptrs, const char* 
                          const bool* optional, int* dev) {
     int d0 = -1;
     const char* first = nullptr;
+    for (int i = 0; i < count; ++i)   // before the first CUDA call
+        if (ptrs[i] == nullptr && !(optional && optional[i])) return fail(FLP_EINVAL, "%s is a null pointer", names[i]);
     for (int i = 0; i < count; ++i) {
         if (optional && optional[i] && ptrs[i] == nullptr) continue;
         int d;

@@ -674,9 +674,15 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
  *   workspace  flp_orthogonalize_workspace_size(batch, rows, cols) bytes,
  *            128-byte aligned, caller-owned, no initial contents needed
  * The products run on FP16 operands with FP32 accumulators; X is carried as
- * two FP16 numbers (22 bits) and the diagonals of A and b A + c A^2 in FP32, so
- * that out is within about 1e-3 (of its norm) of the result in 64 bits also
- * where G has few large singular values over a small floor.  The squares are
+ * two FP16 numbers (22 bits) and the diagonals of A and b A + c A^2 in FP32.
+ * With the usual coefficients and 5 steps out is within 3e-4 to 2e-3 (of its
+ * norm, before the rounding to out_dtype) of the result in 64 bits, 4e-3 at
+ * most, for spectra from alike singular values to rank 1 over any floor.  More
+ * steps multiply, by a each, what rounding puts beside singular values near
+ * zero: 6 steps are within 4.5e-3, 8 within 1.5e-2, 10 within 8e-2 (in plain
+ * FP32 up to 4e-2 there); where no singular value is near zero, 10 steps are
+ * within 4e-3.  Coefficients that settle at 1 (such as (1.5, -0.5, 0)) multiply
+ * nothing.  The squares are
  * scaled where FP32 would not hold their sum, so that every finite G counts.  A zero
  * matrix gives zeros (with eps == 0 too); an infinity or NaN makes its matrix NaN.  Deterministic:
  * equal calls give equal bits (the order of the sums over K depends on the

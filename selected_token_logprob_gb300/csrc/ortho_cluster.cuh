@@ -9,7 +9,11 @@
 //          writing the FP16 A0 and the FP32 diagonal into every CTA;
 //   Poly   every CTA forms B0 and e for itself (128 x 128 products);
 //   Apply  X, in tensor memory, is scaled by a + e_i row by row and the tensor
-//          cores add B0 X_hi onto it; its FP16 rounding becomes the next X_hi.
+//          cores add B0 X_hi onto it; its FP16 rounding becomes the next X_hi.  But for
+//          the last steps, whose noise is hardly multiplied any more, they add B0 X_lo,
+//          too, X_lo = X - X_hi in FP16, so that no row has to leave it out (f in
+//          ortho_kernels.cuh; with f five steps were off by 2e-3 on a 5 x 5 matrix where
+//          e had 8e-4.  64 x 1024: 27.4 us without X_lo, now 28.8).
 // X_hi lies in shared memory as blocks of 64 columns whose 128-byte rows are
 // K-major for Gram (K = columns) and MN-major for Apply (K = rows): one copy
 // serves both.  What bounds it is the chain of latencies of a step (two cluster
@@ -29,8 +33,8 @@ constexpr uint32_t kOrthBlockBytes = 128 * 128;   // 128 rows of 64 FP16
 constexpr uint32_t kOrthGramCol = 384;            // tensor-memory column of Gram's and Poly's result
 constexpr uint32_t kOrthCluX = 0;
 constexpr uint32_t kOrthCluA = kOrthCluX + kOrthCluMaxBlocks * kOrthBlockBytes;   // A0, then B0 in its place
-constexpr uint32_t kOrthCluP = kOrthCluA + 2 * kOrthBlockBytes;                   // FP32 partials, or staged columns
-constexpr uint32_t kOrthCluD = kOrthCluP + 128 * 128 * 4;
+constexpr uint32_t kOrthCluP = kOrthCluA + 2 * kOrthBlockBytes;   // FP32 partials, X_lo, or staged columns
+constexpr uint32_t kOrthCluD = kOrthCluP + kOrthCluMaxBlocks * kOrthBlockBytes;
 constexpr uint32_t kOrthCluE = kOrthCluD + 512;
 constexpr uint32_t kOrthCluMisc = kOrthCluE + 512;   // sums of the CTAs, barrier, TMEM address, scale
 constexpr size_t kOrthCluSmem = 1024 + kOrthCluMisc + 256;
@@ -49,6 +53,7 @@ struct OrthCluArgs {
     int out_dtype, vec_out;
     int64_t ld_out, stride_out;
     float coef[3 * kOrthMaxSteps];
+    float stray[kOrthMaxSteps];
 };
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
@@ -375,6 +380,7 @@ k_orth_cluster(const __grid_constant__ OrthCluArgs p) {
         const float ka = p.coef[3 * step], kb = p.coef[3 * step + 1], kc = p.coef[3 * step + 2];
         if (rows_here) {
             const float di = lds_f32(sd + 4 * row), k0 = kb + kc * di;
+            float sq_ii = 0.f;
             for (int c = from; c < from + width; c += 32) {
                 uint32_t r[32];
                 __syncwarp();
@@ -398,7 +404,7 @@ k_orth_cluster(const __grid_constant__ OrthCluArgs p) {
                             const float sqr = __uint_as_float(r[j]) * kInv;   // scaled A0^2
                             v[k] = (k0 + kc * __uint_as_float(ds[k])) * a + kc * sqr;
                             if (c + j == row) {
-                                sts_f32(se + 4 * row, kb * di + kc * (di * di) + kc * (sqr * kInv));
+                                sq_ii = sqr * kInv;
                                 v[k] = 0.f;
                             }
                         }
@@ -408,9 +414,11 @@ k_orth_cluster(const __grid_constant__ OrthCluArgs p) {
                     sts_v4(at, w[0], w[1], w[2], w[3]);
                 }
             }
+            if (row >= from && row < from + width) sts_f32(se + 4 * row, kb * di + kc * (di * di) + kc * sq_ii);
         }
         __syncthreads();   // e
         // ---------------- Apply
+        const bool with_lo = p.stray[step] < 1.f;
         if (rows_here) {
             const float ai = ka + lds_f32(se + 4 * row);
             for (int c = half; c < chunks; c += 2) {
@@ -421,10 +429,24 @@ k_orth_cluster(const __grid_constant__ OrthCluArgs p) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * ai;
                 tmem_st32(lanes + 32 * c, v);
+                if (with_lo) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float x0 = __uint_as_float(r[8 * q + 2 * k]) * kInv,
+                                        x1 = __uint_as_float(r[8 * q + 2 * k + 1]) * kInv;
+                            const uint32_t h = orth_pack(x0, x1);
+                            w[k] = orth_pack(x0 - h_lo(h), x1 - h_hi(h));
+                        }
+                        sts_v4(orth_block_piece(sp + (c >> 1) * kOrthBlockBytes, row, (c & 1) * 4 + q), w[0], w[1], w[2], w[3]);
+                    }
+                }
             }
             tmem_st_wait();
         }
-        fence_proxy_async_smem();   // B0
+        fence_proxy_async_smem();   // B0, X_lo
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
@@ -432,9 +454,12 @@ k_orth_cluster(const __grid_constant__ OrthCluArgs p) {
             for (int b = 0; b < nblk; b += 4) {
                 const int cols = nblk - b < 4 ? (nblk - b) * 64 : 256;
                 const uint32_t idesc = orth_idesc_n(cols, true);
-                for (int k = 0; k < p.mp / 16; ++k)
-                    umma_bf16(tmem + b * 64, orth_desc_k(sa + (k >> 2) * kOrthBlockBytes) + 2 * (k & 3),
-                              orth_desc_mn_block(sx + b * kOrthBlockBytes) + (2048 >> 4) * k, idesc, 1u);
+                for (uint32_t x = sx;; x = sp) {   // X_hi, then X_lo
+                    for (int k = 0; k < p.mp / 16; ++k)
+                        umma_bf16(tmem + b * 64, orth_desc_k(sa + (k >> 2) * kOrthBlockBytes) + 2 * (k & 3),
+                                  orth_desc_mn_block(x + b * kOrthBlockBytes) + (2048 >> 4) * k, idesc, 1u);
+                    if (!with_lo || x == sp) break;
+                }
             }
             umma_commit(bar);
         }

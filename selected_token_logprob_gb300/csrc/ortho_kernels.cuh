@@ -15,9 +15,22 @@
 //     rest: with A = D + A0,
 //       B_ij = (b + c (d_i + d_j)) A0_ij + c (A0^2)_ij   (i != j)
 //       e_i  = b d_i + c d_i^2 + c (A0^2)_ii
-//       X'   = (a + e_i) X_i. + B0 X.
-// Against 64 bits the result is off by 3e-4 to 1e-3 of its norm (plain FP16: up
-// to 5e-2 where the spectrum has a low rank over a floor; BF16: 0.2).
+//       X'   = (a + e_i) hi_i. + (a + f_i) lo_i. + B0 hi.
+//   - f_i is e_i or 0.  With e_i the row of B X takes lo as far as B is diagonal, which
+//     is nearly all of it once the singular values are alike.  But B0 lo is missing: in
+//     the directions that X does not have it would cancel diag(e) lo, which alone is noise
+//     there, and the steps to come multiply it by their a.  Its part outside of the row's
+//     own direction is sqrt(1 - rho_i), rho_i = d_i^2 / (A^2)_ii (r / m for a projection
+//     of rank r of m, 1 for a row orthogonal to all others), with (A^2)_ii = d_i^2 +
+//     (A0^2)_ii.  So f_i = e_i where (1 - rho_i) G <= 35, G the product of a^2 over the
+//     steps to come: always in the last two usual steps, at rho >= 0.75 in the third
+//     last, 0.98 before that.
+// Against 64 bits the result of five usual steps is off by 3e-4 to 2e-3 of its norm on
+// spectra from alike to rank 1, with any floor, by 4e-3 at most (matrices of a few rows,
+// or a row that holds most of a low rank); f = e throughout: 1e-2 at a rank of m / 2,
+// 4e-2 at rank 1; plain FP16: 5e-2 and more; BF16: 0.2.  What is left are the roundings
+// of hi, A0 and B0 to 11 bits: a choice of one FP16 product where operands of hi and lo
+// would take three.
 //
 // A and B are symmetric: only tiles on and above the diagonal are computed, and
 // each is written to both places.
@@ -72,11 +85,12 @@ struct OrthArgs {
     int64_t units;            // over the batch
     int nkb;                  // K blocks of 64
     float a, b, c;            // this step's coefficients
+    float stray;              // f_i = e_i where (A0^2)_ii <= stray (A^2)_ii
     __half* mat_out;          // Gram: A0, Poly: B0
     const __half* mat_in;     // A0
     const __half* x_hi;       // X; its next hi, and lo (in place)
     __half *x_out, *x_lo;
-    float *d, *e;             // [batch mp] diagonals
+    float *d, *e, *f;         // [batch mp]: the diagonals, and of e what lo takes
     void* out;                // Final
     int out_dtype, transposed, vec_out;
     int64_t ld_out, stride_out;
@@ -197,6 +211,13 @@ __device__ __forceinline__ uint32_t orth_piece64(uint32_t box, int r, int j) {
     return box + (uint32_t)r * 64 + (uint32_t)((j ^ ((r >> 1) & 3)) * 16);
 }
 
+// Whether a row's diagonal of B takes lo: d its diagonal of A, sq of A0^2.  The 35 over
+// G in `stray` is a middle: with 20 five steps are off by 1.6e-3 at a rank of m / 2 and
+// 1.7e-3 on a square Gaussian matrix, with 35 by 1.9e-3 and 1.4e-3, with 70 by 2.4e-3 and
+// 1.3e-3 (the largest over eleven shapes from 4 x 9 to 256 x 1024).
+constexpr float kOrthStray = 35.f;
+__device__ __forceinline__ bool orth_keeps(float d, float sq, float stray) { return sq <= stray * (d * d + sq); }
+
 // Where a warp's 32 rows of a tile lie.
 struct OrthRows {
     int64_t row;      // this thread's row of the batch's padded rows
@@ -247,7 +268,9 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
                 }
             }
             if (diag && w.i >= c0 && w.i < c0 + 32) {
-                p.e[w.row] = p.b * di + p.c * (di * di) + p.c * (sq * kInv);
+                const float ei = p.b * di + p.c * (di * di) + p.c * (sq * kInv);
+                p.e[w.row] = ei;
+                p.f[w.row] = orth_keeps(di, sq * kInv, p.stray) ? ei : 0.f;
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     if (c0 + j == w.i) v[j] = 0.f;
@@ -264,7 +287,7 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
             for (int j = 0; j < 32; ++j) o[j * p.mp] = __float2half_rn(v[j]);
         }
     } else {
-        const float ai = p.a + p.e[w.row];
+        const float ah = p.a + p.e[w.row], al = (p.a + p.f[w.row]) * (1.f / kOrthLoScale);
         const uint32_t lo_box = box + kOrthSquareBytes;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -274,7 +297,7 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, const OrthRows&
             for (int k = 0; k < 8; ++k) {
                 const float xh = (k & 1) ? h_hi(hs[k >> 1]) : h_lo(hs[k >> 1]);
                 const float xl = (k & 1) ? h_hi(ls[k >> 1]) : h_lo(ls[k >> 1]);
-                v[8 * q + k] = ai * (xh + xl * (1.f / kOrthLoScale)) + __uint_as_float(r[8 * q + k]) * kInv;
+                v[8 * q + k] = ah * xh + (al * xl + __uint_as_float(r[8 * q + k]) * kInv);
             }
         }
         if constexpr (kMode == kOrthApply) {
@@ -707,9 +730,10 @@ __device__ __forceinline__ float orth_half_f(const uint4& v, int k) {
 // Columns c0 .. c0 + 31 of row `row` (i of its matrix): the accumulators v to the result.
 template <int kMode>
 __device__ __forceinline__ void orth_finish(const OrthArgs& p, int64_t batch, int64_t row, int64_t i, int64_t c0,
-                                            bool mirror, float side, const OrthInputs& in, float (&v)[32]) {
+                                            bool mirror, float2 side, const OrthInputs& in, float (&v)[32]) {
     constexpr float kInv = 1.f / kOrthScale;
     if constexpr (kMode == kOrthGram || kMode == kOrthPoly) {
+        float sq = 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const float s = v[j] * kInv;
@@ -719,14 +743,19 @@ __device__ __forceinline__ void orth_finish(const OrthArgs& p, int64_t batch, in
                     p.d[row] = s * kInv;
                     v[j] = 0.f;
                 }
-            } else {   // side = d_i
+            } else {   // side.x = d_i
                 const float dj = orth_word_f(j < 16 ? in.b[j >> 2] : in.d[(j >> 2) - 4], j & 3);
-                v[j] = (p.b + p.c * (side + dj)) * orth_half_f(in.a[j >> 3], j & 7) + p.c * s;
+                v[j] = (p.b + p.c * (side.x + dj)) * orth_half_f(in.a[j >> 3], j & 7) + p.c * s;
                 if (c0 + j == i) {
-                    p.e[row] = p.b * side + p.c * (side * side) + p.c * (s * kInv);
+                    sq = s * kInv;
                     v[j] = 0.f;
                 }
             }
+        }
+        if (kMode == kOrthPoly && i >= c0 && i < c0 + 32) {
+            const float ei = p.b * side.x + p.c * (side.x * side.x) + p.c * sq;
+            p.e[row] = ei;
+            p.f[row] = orth_keeps(side.x, sq, p.stray) ? ei : 0.f;
         }
         uint4* o = reinterpret_cast<uint4*>(p.mat_out + row * p.mp + c0);
 #pragma unroll
@@ -738,11 +767,10 @@ __device__ __forceinline__ void orth_finish(const OrthArgs& p, int64_t batch, in
 #pragma unroll
             for (int j = 0; j < 32; ++j) t[j * p.mp] = __float2half_rn(v[j]);
         }
-    } else {   // side = a + e_i
+    } else {   // side = a + e_i, and a + f_i over lo's scale
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            v[j] = side * (orth_half_f(in.a[j >> 3], j & 7) + orth_half_f(in.b[j >> 3], j & 7) * (1.f / kOrthLoScale)) +
-                   v[j] * kInv;
+            v[j] = side.x * orth_half_f(in.a[j >> 3], j & 7) + (side.y * orth_half_f(in.b[j >> 3], j & 7) + v[j] * kInv);
         if constexpr (kMode == kOrthApply) {
             uint4* oh = reinterpret_cast<uint4*>(p.x_out + row * p.np + c0);
             uint4* ol = reinterpret_cast<uint4*>(p.x_lo + row * p.np + c0);
@@ -847,7 +875,7 @@ k_orth_split(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     int chunks = epilogue && i_warp < p.mp ? width / 32 : 0;
     while (chunks > 0 && n0 + from + 32 * (chunks - 1) >= cols) --chunks;
     OrthInputs in;
-    float side = 0.f;
+    float2 side = {0.f, 0.f};
     if (warp == 0) {
         if (lane == 0) {
             const int row0 = (int)(w.batch * p.mp), m0 = row0 + w.mb * 128;
@@ -905,8 +933,8 @@ k_orth_split(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             umma_commit(tfull);   // also after a wait that ran out: what was issued drains
         }
     } else if (chunks > 0) {
-        if constexpr (kMode == kOrthPoly) side = p.d[row];
-        else if constexpr (!kSym) side = p.a + p.e[row];
+        if constexpr (kMode == kOrthPoly) side.x = p.d[row];
+        else if constexpr (!kSym) side = make_float2(p.a + p.e[row], (p.a + p.f[row]) * (1.f / kOrthLoScale));
         orth_inputs<kMode>(p, w.batch, row, n0 + from, in);
     }
     __syncwarp();

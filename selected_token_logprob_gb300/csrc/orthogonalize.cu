@@ -12,7 +12,7 @@ namespace {
 
 struct OrthLayout {
     int64_t m, n, mp, np;              // of X: the matrix or its transpose, m <= n
-    int64_t parts, d, e, hi0, hi1, lo, a0, b0, total;   // byte offsets
+    int64_t parts, d, e, f, hi0, hi1, lo, a0, b0, total;   // byte offsets
 };
 
 bool orth_layout(int64_t batch, int64_t rows, int64_t cols, OrthLayout* l) {
@@ -29,7 +29,8 @@ bool orth_layout(int64_t batch, int64_t rows, int64_t cols, OrthLayout* l) {
     l->parts = 0;
     l->d = up(batch * flp::kOrthParts * (int64_t)sizeof(flp::OrthSum));
     l->e = l->d + up(all_rows * 4);
-    l->hi0 = l->e + up(all_rows * 4);
+    l->f = l->e + up(all_rows * 4);
+    l->hi0 = l->f + up(all_rows * 4);
     l->hi1 = l->hi0 + up(x);
     l->lo = l->hi1 + up(x);
     l->a0 = l->lo + up(x);
@@ -345,7 +346,8 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     if (out_dtype != FLP_DTYPE_BF16 && out_dtype != FLP_DTYPE_F32)
         return fail(FLP_EINVAL, "out_dtype must be FLP_DTYPE_BF16 or FLP_DTYPE_F32 (got %d)", out_dtype);
     if ((st = check_orth_shape(batch, rows, cols)) != FLP_OK) return st;
-    if (steps < 1 || steps > 64) return fail(FLP_EINVAL, "steps must be in [1, 64] (got %d)", steps);
+    if (steps < 1 || steps > flp::kOrthMaxSteps)
+        return fail(FLP_EINVAL, "steps must be in [1, %d] (got %d)", flp::kOrthMaxSteps, steps);
     if (coefficients == nullptr) return fail(FLP_EINVAL, "coefficients is a null pointer");
     for (int k = 0; k < 3 * steps; ++k)
         if (!isfinite(coefficients[k])) return fail(FLP_EINVAL, "coefficients must be finite");
@@ -390,6 +392,13 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     const bool vec_in = (cols * eb) % 16 == 0 && rows_aligned16(x, ld_x, dtype) &&
                         (batch == 1 || (stride_x * eb) % 16 == 0);
     const bool vec_out = aligned16(out) && (ld_out * ob) % 16 == 0 && (batch == 1 || (stride_out * ob) % 16 == 0);
+    // by what the steps after it multiply a step's noise
+    float stray[flp::kOrthMaxSteps];
+    double grow = 1.0;
+    for (int k = steps - 1; k >= 0; --k) {
+        stray[k] = (float)(flp::kOrthStray / grow);
+        grow *= (double)coefficients[3 * k] * (double)coefficients[3 * k];
+    }
     if (l.m <= 128) {
         flp::OrthCluArgs c{};
         c.x = x;
@@ -410,6 +419,7 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
         c.ld_out = ld_out;
         c.stride_out = stride_out;
         for (int k = 0; k < 3 * steps; ++k) c.coef[k] = coefficients[k];
+        for (int k = 0; k < steps; ++k) c.stray[k] = stray[k];
         bool done = false;
         st = dtype == FLP_DTYPE_BF16 ? orth_cluster_launch<__nv_bfloat16>(dev, batch, c, s, &done)
              : dtype == FLP_DTYPE_F16 ? orth_cluster_launch<__half>(dev, batch, c, s, &done)
@@ -477,6 +487,7 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
     p.np = l.np;
     p.d = reinterpret_cast<float*>(ws + l.d);
     p.e = reinterpret_cast<float*>(ws + l.e);
+    p.f = reinterpret_cast<float*>(ws + l.f);
     p.mat_in = reinterpret_cast<const __half*>(ws + l.a0);
     p.x_lo = lo;
     p.out = out;
@@ -491,6 +502,7 @@ flp_status flp_orthogonalize(const void* x, int dtype, int64_t batch, int64_t ro
         p.a = coefficients[3 * k];
         p.b = coefficients[3 * k + 1];
         p.c = coefficients[3 * k + 2];
+        p.stray = stray[k];
         p.x_hi = hi[cur];
         p.x_out = hi[cur ^ 1];
         p.mat_out = reinterpret_cast<__half*>(ws + l.a0);

@@ -92,7 +92,8 @@ __device__ __forceinline__ float norm_block_sum(float v, float* red) {
 // ---------------------------------------------------------------- any width
 
 // One CTA per row, the row read once per sum: for widths that no register
-// tile holds.
+// tile holds.  Bound by its element-wise reads (4096 x 20480 BF16, RMS norm: forward 157 us,
+// 2.1 TB/s; the backward, from 8193 columns on, at 8192 x 12288 425 us, 1.4 TB/s).
 template <class T, bool kCenter>
 __global__ void __launch_bounds__(kNormAnyThreads)
 k_norm_fwd_any(NormFwdArgs a) {
@@ -249,7 +250,8 @@ k_norm_fold(NormBwdArgs a, int rows) {
 //
 // What bounds it: memory (32768 x 4096 BF16: forward 88 us, 6.1 TB/s, backward with FP32
 // dy 150 us, 7.1 TB/s; 2 M rows of 64: 5.2 and 5.0 TB/s), but for the instructions of the
-// shifted rows (130182 x 1031: 2.3 and 2.1 TB/s).
+// shifted rows and their latencies (130182 x 1031: 2.3 and 2.1 TB/s; 68% of the issue slots
+// in the forward, 46% at 24% occupancy in the backward).
 constexpr int kNormElems = 16;
 template <int kTpr>
 constexpr int kNormThreads = kTpr < 128 ? 128 : kTpr;

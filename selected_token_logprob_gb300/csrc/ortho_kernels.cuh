@@ -48,9 +48,10 @@
 // CTA's abort flag, the copies and MMAs in flight are waited for, TMEM is freed and
 // the kernel returns.
 //
-// What bounds it (4096 x 4096, 1.07 ms): the tensor cores and the copies that feed
-// them, 585 cycles a K block of a 256 x 256 tile (512 being the MMAs' own), in 2, 2
-// and 4 waves a step where 1.8, 1.8 and 3.4 would hold the work.  Cutting the K
+// What bounds it (4096 x 4096, 1.08 ms at 1860 MHz, the power cap's): the tensor cores and
+// the copies that feed them, 585 cycles a K block of a 256 x 256 tile (512 being the MMAs'
+// own), in 2, 2 and 4 waves a step where 1.8, 1.8 and 3.4 would hold the work: 805 us; the
+// input passes 38; start, first copies and last epilogue of 15 launches the rest.  Cutting the K
 // blocks of all tiles into equal runs, one a pair, did not pay: the same 1046 us,
 // and 644 instead of 617 at 4 x 2048 x 2048.
 #pragma once

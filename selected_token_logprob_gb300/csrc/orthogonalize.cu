@@ -187,9 +187,12 @@ OrthFormKind orth_form(bool sym, int64_t batch, int64_t mp, int64_t np, int sms,
     // split over up to 4 CTAs (a call on 1024 x 1024: 135 us with the tiles below, 152
     // unsplit, 117 split; 200 x 400: 90, 117, 89; 512 x 4096: 188, 193, 128).
     if (units <= sms) return kOrthFormSplit;
-    // Else by the waves: 256 x 256 tiles a pair or 128 x 128 a CTA, a K block taking
-    // about 540 and 420 cycles (8 x 1024 x 4096: Gram's 80 pair tiles 68 us, its 288
-    // small ones 43; 4096 x 4096 in all 1064 and 1482 us).
+    // Else by the waves: 256 x 256 tiles a pair or 128 x 128 a CTA.  A wave of pairs weighs
+    // 540 : 420 of one of CTAs: fitted to whole calls, with what a wave costs beside its K
+    // blocks (which alone take 585 and 490 cycles).  Symmetric products by CTAs and by pairs:
+    // 3008 x 3104 616 and 657 us in all, 8 x 1024 x 4096 687 and 745, 5 x 1000 x 1100 271 and
+    // 250, 4096 x 4096 1312 and 1025; those with X: 20 x 300 x 310 134 and 164, 3008 x 3104
+    // 648 and 616, 4096 x 4096 1218 and 1025.
     const int64_t small = ceil_div(units, sms) * 420;
     const int64_t wide = batch * orth_tiles(sym, mp, cols, 256, 256);
     return pairs <= 0 || small <= ceil_div(wide, pairs) * 540 ? kOrthFormCta : kOrthFormPair;
@@ -268,11 +271,13 @@ int orth_cluster_ctas(int dev, int64_t batch, int64_t m, int64_t blocks) {
             if (ceil_div(blocks, c) <= per) return c;
         return 0;
     };
-    // Few columns: one CTA, without exchanges (64 x 256: 22.7 us; in 4 CTAs 23.3, in 2 26.4).
+    // Few columns: one CTA, without exchanges (64 x 128: 19.6 us, in 2 CTAs 25.0; 128 x 256:
+    // 37.6, in 4 41.6; 76 x 64 x 256: 26.9, in 4 70.0; a few of 64 x 256 alone the other
+    // way round, 26.6 and 24.2).
     if (blocks <= 4) return orth_cluster_fit<T>(dev, 1) > 0 ? 1 : 0;
-    // Two blocks a CTA while all clusters run at once (64 x 512: 25.8 us, four blocks
-    // 31.2; 128 x 512: 43, 55; 64 x 1024: 27.9, 30.6), else four, or six with the most
-    // CTAs (16 x 128 x 1024: two 90.7, four 50.8).
+    // Two blocks a CTA while all clusters run at once (64 x 512: 27.3 us, four blocks
+    // 35.1; 128 x 512: 45.8, 61.1; 64 x 1024: 29.0, 34.3), else four, or six with the most
+    // CTAs (16 x 128 x 1024: two 93.7, four 56.0).
     int c = fewest(2);
     if (c == 0 || batch > orth_cluster_fit<T>(dev, c)) {
         c = fewest(4);
@@ -282,9 +287,9 @@ int orth_cluster_ctas(int dev, int64_t batch, int64_t m, int64_t blocks) {
     const int fit = orth_cluster_fit<T>(dev, c);
     if (fit <= 0) return 0;
     // Large clusters leave SMs idle: over 64 rows the tiled kernels win from the third
-    // wave on (128 x 4096, 16 CTAs: a batch of 12 121 against 142 us, of 16 181 against
-    // 164; 128 x 2048, 8 CTAs: of 24 109 against 133, of 32 163 against 151); smaller
-    // clusters and fewer rows stay ahead (200 x 64 x 1024: 191 against 275).
+    // wave on (128 x 4096, 16 CTAs: a batch of 12 128 against 139 us, of 16 190 against
+    // 158; 128 x 2048, 8 CTAs: of 24 115 against 132, of 32 171 against 151); smaller
+    // clusters and fewer rows stay ahead (200 x 64 x 1024: 206 against 279).
     if (m > 64 && c >= 8 && batch > 2 * (int64_t)fit) return 0;
     return c;
 }

@@ -37,24 +37,24 @@ flp_status launch_bwd_rows(const flp::NormBwdArgs& a, const NormTo& to, int* par
     constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr;
     static_assert(kNormSms * flp::kNormBwdCtas<kTpr> <= flp::kNormParts, "a partial row per CTA");
     const auto kern = flp::k_norm_bwd<T, G, kTpr, kFull, kAligned>;
-    auto bytes = [](int64_t d) {
-        return kAligned ? (size_t)kThreads * flp::kNormElems * (sizeof(T) + sizeof(G)) * flp::kNormBwdStages<T, G>
-                        : ((size_t)(flp::norm_pitch<T>(d) + flp::norm_pitch<G>(d)) * flp::kNormBwdStages<T, G> +
-                           flp::norm_pitch<T>(d)) * kRows;
+    constexpr int kStages = flp::kNormBwdStages<T, G>;
+    constexpr auto bytes = [](int64_t d) {
+        return kAligned ? (size_t)kThreads * flp::kNormElems * (sizeof(T) + sizeof(G)) * kStages
+                        : ((size_t)(flp::norm_pitch<T>(d) + flp::norm_pitch<G>(d)) * kStages + flp::norm_pitch<T>(d)) *
+                              kRows;
     };
+    // for the widest row of this kernel, so that one number serves all its calls
+    constexpr size_t top = bytes((int64_t)kTpr * flp::kNormElems);
+    static_assert(top <= kNormMaxSmem, "the widest row of this kernel fits");
     const size_t smem = bytes(a.d);
-    if (smem > kNormMaxSmem)
-        return a.mean ? launch_bwd_any<T, G, true>(a, to, parts) : launch_bwd_any<T, G, false>(a, to, parts);
     flp_status st;
     if ((st = norm_setup(kern, dev, ready)) != FLP_OK) return st;
     const int rows = row_ctas(a.n, kRows, to.sms * flp::kNormBwdCtas<kTpr>);
     int fit = fits[dev].load(std::memory_order_acquire);
     if (fit == 0) {
-        // for the widest row of this kernel, so that one number serves all its calls
-        const size_t top = bytes((int64_t)kTpr * flp::kNormElems);
         int per_sm = 0;
         const int sms = sm_count(dev);
-        if (top > kNormMaxSmem || sms <= 0 ||
+        if (sms <= 0 ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, top) != cudaSuccess) {
             (void)cudaGetLastError();
             per_sm = 0;

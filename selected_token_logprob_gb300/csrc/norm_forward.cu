@@ -17,11 +17,13 @@ flp_status launch_fwd_any(const flp::NormFwdArgs& a, cudaStream_t s) {
 template <class T, class W, int kTpr, bool kCenter, bool kAligned>
 flp_status launch_fwd_rows(const flp::NormFwdArgs& a, int dev, cudaStream_t s) {
     static std::atomic<bool> ready[kMaxDevices];
-    constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = flp::kNormFwdStages<T>;
+    constexpr int kThreads = flp::kNormThreads<kTpr>, kRows = kThreads / kTpr;
+    constexpr int kStages = flp::kNormFwdStages<T, kTpr, kAligned>;
+    static_assert((size_t)flp::norm_pitch<T>(kTpr * flp::kNormElems) * kRows * (kStages + 1) <= kNormMaxSmem || kAligned,
+                  "the widest row of this kernel fits");
     const auto kern = flp::k_norm_fwd<T, W, kTpr, kCenter, kAligned>;
     const size_t smem = kAligned ? (size_t)kThreads * flp::kNormElems * sizeof(T) * kStages
                                  : (size_t)flp::norm_pitch<T>(a.d) * kRows * (kStages + 1);
-    if (smem > kNormMaxSmem) return launch_fwd_any<T, kCenter>(a, s);
     flp_status st;
     if ((st = norm_setup(kern, dev, ready)) != FLP_OK) return st;
     kern<<<row_ctas(a.n, kRows, kNormSms * flp::kNormFwdCtas<kTpr>), kThreads, smem, s>>>(a);

@@ -62,6 +62,6 @@ inline int row_ctas(int64_t n, int rows, int most) {
     return (int)(c < most ? c : most);
 }
 
-constexpr size_t kNormMaxSmem = 232448 - 8192;   // of a CTA, beside the static arrays
+constexpr size_t kNormMaxSmem = 232448 - 2048;   // of a CTA with a row, beside the static arrays
 
 }  // namespace flp_host

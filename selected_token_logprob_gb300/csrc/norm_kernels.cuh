@@ -260,9 +260,11 @@ template <int kTpr>
 constexpr int kNormFwdCtas = 1024 / kNormThreads<kTpr>;
 template <int kTpr>
 constexpr int kNormBwdCtas = 512 / kNormThreads<kTpr>;
-// rows of the ring: 160 .. 192 KB per SM
-template <class T>
-constexpr int kNormFwdStages = sizeof(T) == 2 ? 5 : 3;
+// rows of the ring: 160 .. 192 KB per SM; in the forward one less where an unaligned row's
+// staged result would not fit beside it (rows of FP32 by the most threads), so that every
+// width is summed in one order, wherever its rows lie
+template <class T, int kTpr, bool kAligned>
+constexpr int kNormFwdStages = sizeof(T) == 2 ? 5 : kAligned || kTpr < 1024 ? 3 : 2;
 template <class T, class G>
 constexpr int kNormBwdStages = 24 / (int)(sizeof(T) + sizeof(G));
 
@@ -405,7 +407,7 @@ __device__ __forceinline__ void norm_row_sum(float (&v)[kCount], float* red, int
 // Bytes of a ring slot of one unaligned row: its 16-byte blocks, one more than
 // aligned ones would take.
 template <class T>
-__host__ __device__ __forceinline__ uint32_t norm_pitch(int64_t d) {
+__host__ __device__ constexpr uint32_t norm_pitch(int64_t d) {
     return (uint32_t)((d * (int64_t)sizeof(T) + 15) / 16 + 1) * 16;
 }
 template <class T>
@@ -533,7 +535,7 @@ template <class T, class W, int kTpr, bool kCenter, bool kAligned>
 __global__ void __launch_bounds__(kNormThreads<kTpr>, kNormFwdCtas<kTpr>)
 k_norm_fwd(NormFwdArgs a) {
     constexpr int V = 16 / (int)sizeof(T), NV = kNormElems / V;
-    constexpr int kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = kNormFwdStages<T>;
+    constexpr int kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = kNormFwdStages<T, kTpr, kAligned>;
     extern __shared__ __align__(16) unsigned char norm_smem[];
     __shared__ float red[2 * 64];
     int turn = 0;
@@ -650,7 +652,8 @@ template <class T, class G, int kTpr, bool kFull, bool kAligned>
 __global__ void __launch_bounds__(kNormThreads<kTpr>, kNormBwdCtas<kTpr>)
 k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
     constexpr int V = 16 / (int)sizeof(G), NV = kNormElems / V;
-    constexpr int kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr, kStages = kNormBwdStages<T, G>;
+    constexpr int kThreads = kNormThreads<kTpr>, kRows = kThreads / kTpr;
+    constexpr int kStages = kNormBwdStages<T, G>;
     extern __shared__ __align__(16) unsigned char norm_smem[];
     __shared__ float red[2 * 64];
     int turn = 0;

@@ -677,7 +677,9 @@ flp_status logp_preference_loss(const float* logp, const float* ref_logp, const 
  * two FP16 numbers (22 bits) and the diagonals of A and b A + c A^2 in FP32.
  * With the usual coefficients and 5 steps out is within 3e-4 to 2e-3 (of its
  * norm, before the rounding to out_dtype) of the result in 64 bits, 4e-3 at
- * most, for spectra from alike singular values to rank 1 over any floor.  More
+ * most, for spectra from alike singular values to rank 1 over any floor (where
+ * a side is below 8, a handful of roundings do not average: 1e-2, and 3e-2
+ * after 8 steps).  More
  * steps multiply, by a each, what rounding puts beside singular values near
  * zero: 6 steps are within 4.5e-3, 8 within 1.5e-2, 10 within 8e-2 (in plain
  * FP32 up to 4e-2 there); where no singular value is near zero, 10 steps are

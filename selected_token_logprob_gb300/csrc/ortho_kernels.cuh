@@ -26,8 +26,8 @@
 //     steps to come: always in the last two usual steps, at rho >= 0.75 in the third
 //     last, 0.98 before that.
 // Against 64 bits the result of five usual steps is off by 3e-4 to 2e-3 of its norm on
-// spectra from alike to rank 1, with any floor, by 4e-3 at most (matrices of a few rows,
-// or a row that holds most of a low rank); f = e throughout: 1e-2 at a rank of m / 2,
+// spectra from alike to rank 1, with any floor, by 4e-3 at most (few rows, or a row that
+// holds most of a low rank; 1e-2 where a side is below 8); f = e throughout: 1e-2 at a rank of m / 2,
 // 4e-2 at rank 1; plain FP16: 5e-2 and more; BF16: 0.2.  What is left are the roundings
 // of hi, A0 and B0 to 11 bits: a choice of one FP16 product where operands of hi and lo
 // would take three.

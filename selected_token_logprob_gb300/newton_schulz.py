@@ -39,7 +39,7 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=ORTHOGONALIZE_CO
     ``out`` (BF16, the default ``out_dtype``, or FP32), which may be x.  The
     products run on FP16 operands with compensated carries: five of the usual
     steps are within 3e-4 to 2e-3 of the result's norm of the exact one (4e-3 at
-    most), six within 4.5e-3; more steps lose more where singular values are near
+    most, 1e-2 where a side is below 8), six within 4.5e-3; more steps lose more where singular values are near
     zero (eight 1.5e-2, ten 8e-2).  ``workspace`` (a CUDA byte
     tensor of orthogonalize_workspace_size(B, M, N) bytes) is allocated when
     not given."""

@@ -133,6 +133,23 @@ def test_coefficients_that_converge():
             assert err <= 1.5 * _rel(_rounded(x, coefs), want) + 2e-4 + 2.0 ** -20, (a, shape, err)
 
 
+@pytest.mark.parametrize("m,n", [(2, 2), (2, 5), (5, 3), (4, 9), (7, 7), (8, 8), (40, 8), (16, 16), (32, 32), (64, 80)])
+@pytest.mark.parametrize("kind", ["gauss", "rank 1", "rank 1 over 1e-3", "half rank", "rows of unlike size"])
+def test_many_small_matrices(m, n, kind):
+    """The header's ceilings on every matrix of a stack of hundreds."""
+    g = torch.Generator(device=DEV).manual_seed(35)
+    rand = lambda *s: torch.randn(500, *s, generator=g, device=DEV)   # noqa: E731
+    r = max(1, min(m, n) // 2)
+    x = {"gauss": lambda: rand(m, n), "rank 1": lambda: rand(m, 1) @ rand(1, n),
+         "rank 1 over 1e-3": lambda: rand(m, 1) @ rand(1, n) + 1e-3 * rand(m, n),
+         "half rank": lambda: rand(m, r) @ rand(r, n),
+         "rows of unlike size": lambda: rand(m, n) * torch.exp(2 * rand(m, 1))}[kind]()
+    tiny = min(m, n) < 8
+    for steps, ceiling in ((5, 1e-2 if tiny else 4e-3), (8, 3e-2 if tiny else 1.5e-2)):
+        want = _exact(x, [ABC] * steps)
+        assert _rel(flp.orthogonalize(x, steps=steps, out_dtype=torch.float32), want) <= ceiling, steps
+
+
 def test_a_stack_decides_row_by_row():
     """Matrices of unlike spectra in one stack keep their own bits."""
     x = torch.stack([_spectrum(k, (300, 500), 34) for k in ("gauss", "rank 0.01", "rank 0.5")])

@@ -238,7 +238,12 @@ __device__ __forceinline__ void fp8_put_rows(const Fp8Args& p, const CUtensorMap
         const int64_t n0 = n + part * 32;
         if (n0 >= p.N || m >= p.M) break;   // the same for the warp
         const uint32_t box = boxes + (wide ? part & 1 : (part >> 1) & 1) * kFp8Box;
-        if (lane == 0) bulk_wait_read<1>();   // the copy that last used this box has read it
+        // the copy that last used this box has read it; at a tile's start both boxes', of which a ragged
+        // tile before may have left the first one last
+        if (lane == 0) {
+            if (part == 0) bulk_wait_read<0>();
+            else bulk_wait_read<1>();
+        }
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

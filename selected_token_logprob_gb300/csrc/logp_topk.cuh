@@ -128,19 +128,17 @@ __device__ __forceinline__ float topk_value(uint32_t key) {
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 
-// The unit's words raised to a floor (a packed word, or FP32), at least the type's lowest number: -inf
-// becomes a number, so that 0 times it is 0; terms that far below the maximum are 0 either way.
+// The unit's words raised to a floor (a packed word, or FP32) that lies at the type's lowest number or
+// above it: -inf becomes a number, so that 0 times it is 0; terms that far below the maximum are 0
+// either way.
+template <Dt D>
+constexpr float kTopkLowest = D == Dt::F16 ? -65504.f : D == Dt::BF16 ? -0x1.fep127f : -0x1.fffffep127f;
 template <Dt D>
 __device__ __forceinline__ uint32_t topk_floor(float fl) {
-    if constexpr (D == Dt::F32) return __float_as_uint(fmaxf(fl, __uint_as_float(0xff7fffffu)));
-    else if constexpr (D == Dt::BF16) {
-        const uint32_t b =
-            (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(fmaxf(fl, __uint_as_float(0xff7f0000u))));
-        return b | (b << 16);
-    } else {
-        const uint32_t b = (uint32_t)__half_as_ushort(__float2half_rd(fmaxf(fl, -65504.f)));
-        return b | (b << 16);
-    }
+    if constexpr (D == Dt::F32) return __float_as_uint(fl);
+    const uint32_t b = D == Dt::BF16 ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(fl))
+                                     : (uint32_t)__half_as_ushort(__float2half_rd(fl));
+    return b | (b << 16);
 }
 template <Dt D>
 __device__ __forceinline__ void topk_raise(Unit<D>& u, uint32_t fl) {
@@ -160,7 +158,9 @@ __device__ __forceinline__ u64 topk_pair(const Unit<D>& u, int k) {
     else return f2(h_lo(u.w[k]), h_hi(u.w[k]));
 }
 
-// Sums of a group's terms 2^e and of 2^e e.  e = x c + g (kDiff: (x - gm) c).
+// Sums of a group's terms 2^e and of 2^e e.  e = x c + g, of values raised to the floor; kDiff: (x - gm) c of
+// the values themselves, then not below kTopkLeast, where a term is 0 (-inf must not meet it).
+constexpr float kTopkLeast = -300.f;
 template <Dt D, bool kFull, bool kDiff>
 __device__ __forceinline__ void topk_sums(const Unit<D> (&q)[kTopkGroup<D>], int nvalid, float gm, float g, const Scale& sc,
                                           float& gs, float& gt) {
@@ -173,9 +173,14 @@ __device__ __forceinline__ void topk_sums(const Unit<D> (&q)[kTopkGroup<D>], int
             u64 p[4], tt = 0ull;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const u64 e = kDiff ? to_log2<true>(pair_sub<D>(q[u], k, gm), sc) : f2_fma(topk_pair<D>(q[u], k), c2, g2);
+                u64 e = kDiff ? to_log2<true>(pair_sub<D>(q[u], k, gm), sc) : f2_fma(topk_pair<D>(q[u], k), c2, g2);
                 float a0, a1;
                 f2_split(e, a0, a1);
+                if constexpr (kDiff) {
+                    a0 = f_max_nan(a0, kTopkLeast);
+                    a1 = f_max_nan(a1, kTopkLeast);
+                    e = f2(a0, a1);
+                }
                 p[k] = f2(ex2_ftz(a0), ex2_ftz(a1));
                 tt = k == 0 ? f2_mul(p[k], e) : f2_fma(p[k], e, tt);
             }
@@ -204,7 +209,9 @@ __device__ __forceinline__ void topk_sums(const Unit<D> (&q)[kTopkGroup<D>], int
 //
 // Terms are 2^(x c + g) with g = -(gm c) rounded; r, what the rounding lost, is the same for all of
 // them: the group's sum is 2^r = 1 + r ln 2 of that (|r| <= 2^-12: the next term is below 2^-25), its
-// T is moved by r.  Where |gm c| is larger the difference is taken first.
+// T is moved by r.  Where |gm c| is larger, or the floor below the type's lowest number, the difference is
+// taken first: next to a large maximum a floor would be the maximum itself, at the lowest number -inf
+// would count as it does.
 template <Dt D, bool kFull>
 __device__ __forceinline__ uint32_t topk_update(Unit<D> (&q)[kTopkGroup<D>], int nvalid, MST& a, const Scale& sc, float far) {
     uint32_t w = q[0].w[0];
@@ -215,13 +222,13 @@ __device__ __forceinline__ uint32_t topk_update(Unit<D> (&q)[kTopkGroup<D>], int
             if (u + k > 0) w = word_max<D>(w, q[u].w[k]);
     const float gm = f_max_nan(a.m, word_value<D>(w));
     if (gm == -INFINITY) return w;   // nothing finite seen yet: (m, s, t) stays (-inf, 0, 0)
-    const uint32_t fl = topk_floor<D>(__fsub_rn(gm, far));
-#pragma unroll
-    for (int u = 0; u < kTopkGroup<D>; ++u)
-        if (kFull || u < nvalid) topk_raise<D>(q[u], fl);
-    const float g = __fmul_rn(-gm, sc.hi);
+    const float g = __fmul_rn(-gm, sc.hi), fl = __fsub_rn(gm, far);
     float gs, gt;
-    if (fabsf(g) < 4096.f) {
+    if (fabsf(g) < 4096.f && fl >= kTopkLowest<D>) {
+        const uint32_t raise = topk_floor<D>(fl);
+#pragma unroll
+        for (int u = 0; u < kTopkGroup<D>; ++u)
+            if (kFull || u < nvalid) topk_raise<D>(q[u], raise);
         topk_sums<D, kFull, false>(q, nvalid, gm, g, sc, gs, gt);
         const float r = __fmaf_rn(-gm, sc.hi, -g), more = __fmul_rn(r, (float)kLn2);
         gt = __fmaf_rn(r, gs, gt);

@@ -1,0 +1,80 @@
+"""Log-probabilities with entropy and alternatives where a logit's distance from the maximum is
+lost beside the logit itself: large logits, small temperatures, closed columns of the type's
+lowest number or -inf; against the definition in 64 bits, which takes the maximum off first.
+Tolerances are those of test_logp_topk_gpu: they hold for a row's distances from its maximum,
+whatever the maximum is."""
+
+import math
+
+import pytest
+import torch
+
+import selected_token_logprob_gb300 as flp
+from test_logp_topk_gpu import close, exact
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def build(kind, v, dtype, g):
+    """24 rows: the open columns' values, the rest."""
+    n, low = 24, torch.finfo(dtype).min
+    x = torch.full((n, v), -math.inf, device="cuda", dtype=dtype)
+    few = torch.rand((n, v), generator=g, device="cuda") < 0.02
+    few[:, torch.randint(0, v, (1,), generator=g, device="cuda")] = True
+    r = torch.randn((n, v), generator=g, device="cuda")
+    if kind == "neighbours":         # one maximum of +-1e10 or so, half of it and less elsewhere
+        top = 1e10 if dtype != torch.float16 else 6e4
+        x = (r * 1e9 / 1e10 * top).clamp(-0.5 * top, 0.5 * top).to(dtype)
+        x[:, v // 3] = top
+        x[1::2] = -x[1::2].abs() - (top * 0.01 if dtype == torch.float16 else top)
+    elif kind == "lowest and inf":   # few columns at the lowest number, the rest closed
+        x[few] = low
+    elif kind == "large and inf":    # few columns at one large value, the rest closed
+        x[few] = -6e4 if dtype == torch.float16 else -1e10
+    elif kind == "halves":           # two large values mixed
+        x[:] = low / -4
+        x[few] = low / -8
+        x[::3] = -x[::3]
+    elif kind == "filled":           # closed by a finite fill, all of a row or all but a few
+        fill = [-1e4 if dtype == torch.float16 else -1e9, -6e4 if dtype == torch.float16 else -1e10, low]
+        for i in range(n):
+            x[i] = fill[i % 3]
+        x[12:][few[12:]] = r[12:][few[12:]].to(dtype)
+    else:                            # ordinary ones
+        x = (r * 3).to(dtype)
+        x[::4, ::2] = -math.inf
+    return x
+
+
+CASES = [(kind, 1.0) for kind in ("neighbours", "lowest and inf", "large and inf", "halves", "filled")] + \
+    [("lowest and inf", 0.7), ("halves", 0.7), ("filled", 0.7), ("neighbours", 1.3),
+     ("ordinary", 1e-9), ("ordinary", 3e-7), ("ordinary", 2e-5), ("ordinary", 1e-3), ("ordinary", 1e4), ("ordinary", 1e30)]
+
+
+def case(kind, temperature, v, dtype):
+    g = torch.Generator(device="cuda").manual_seed(v + len(kind))
+    x = build(kind, v, dtype, g)
+    k = min(v, 12)
+    y = x.float().argmax(1)
+    y[::5] = torch.randint(0, v, (len(y[::5]),), generator=g, device="cuda")
+    y[3] = -100
+    r = flp.fused_logp_topk_forward(x, y, k, temperature=temperature)
+    torch.cuda.synchronize()
+    assert flp.flp_device_error(0) == 0
+    return x, y, r, exact(x, y, k, temperature), g
+
+
+def held(got, want):
+    """Log-probabilities, which are -inf where FP32 has no number for them (below -3.4028235e38)."""
+    close(got, want.float().double(), 1.2e-5 * (1 + want.abs()))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v", [40, 5000, 151936])
+@pytest.mark.parametrize("kind,temperature", CASES)
+def test_entropy_and_alternatives(kind, temperature, v, dtype):
+    x, y, r, e, _ = case(kind, temperature, v, dtype)
+    close(r.entropy, e["h"], 2e-5 * (1 + e["h"].abs()))
+    assert torch.equal(r.top_ids, e["ids"])
+    held(r.top_logp, e["top"])

@@ -541,7 +541,6 @@ struct TopkRow {
     int k;
     __device__ __forceinline__ void put(int rank, uint32_t key, uint32_t col) const {
         ids[rank] = (int64_t)col;
-        // around the maximum: next to a large one LSE has no digits left for log S
         top[rank] = __double2float_rn(s * ((double)topk_value(key) - m) - *log_s);
     }
 };
@@ -717,7 +716,8 @@ k_logp_topk_finish(TopkArgs a, TopkOut o) {
                 row_log[lane] = log_s;
                 l = __double2float_rn(lse);
                 lo = isfinite(l) ? __double2float_rn(lse - (double)l) : 0.f;
-                lp = __double2float_rn((double)a.sc.s * (double)row_x[lane] - lse);
+                // around the maximum, as the alternatives: next to a large one LSE has no digits left for log S
+                lp = __double2float_rn((double)a.sc.s * ((double)row_x[lane] - (double)m) - log_s);
                 h = __fmaf_rn(-(float)kLn2, __fdiv_rn(row_t[lane], sum), logf(sum));
                 h = h < 0.f ? 0.f : h;   // of one value: log S is the rounding of S alone
             }

@@ -14,6 +14,7 @@ from test_logp_topk_gpu import close, exact
 
 pytestmark = pytest.mark.gpu
 TYPES = [torch.bfloat16, torch.float16, torch.float32]
+U = 2.0 ** -24
 
 
 def build(kind, v, dtype, g):
@@ -78,3 +79,15 @@ def test_entropy_and_alternatives(kind, temperature, v, dtype):
     close(r.entropy, e["h"], 2e-5 * (1 + e["h"].abs()))
     assert torch.equal(r.top_ids, e["ids"])
     held(r.top_logp, e["top"])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v", [40, 5000, 151936])
+@pytest.mark.parametrize("kind,temperature", CASES)
+def test_logp_and_lse(kind, temperature, v, dtype):
+    x, y, r, e, _ = case(kind, temperature, v, dtype)
+    held(r.logp, e["logp"])
+    z = x.double() * float(torch.tensor(1 / temperature, dtype=torch.float32))
+    lse = torch.where(e["active"], torch.logsumexp(z, 1), 0)
+    in_range = lse.float().isfinite()
+    close(r.lse[in_range], lse[in_range], (1.2e-5 + U * lse.abs())[in_range])

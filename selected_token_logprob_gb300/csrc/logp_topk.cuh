@@ -249,9 +249,9 @@ __device__ __forceinline__ uint32_t topk_update(Unit<D> (&q)[kTopkGroup<D>], int
     return w;
 }
 
-// As ms_merge, with T.
+// As ms_merge, with T; a NaN is the larger one, whatever it meets.
 __device__ __forceinline__ MST mst_merge(MST a, MST b, const Scale& sc) {
-    const bool a_big = a.m >= b.m;
+    const bool a_big = a.m >= b.m || a.m != a.m;
     const MST big = a_big ? a : b, small = a_big ? b : a;
     float r, d = 0.f;
     if (small.m == -INFINITY) r = 0.f;
@@ -712,7 +712,8 @@ k_logp_topk_finish(TopkArgs a, TopkOut o) {
             float l = 0.f, lo = 0.f, lp = 0.f, h = 0.f;
             if (on) {
                 const double log_s = log((double)sum);
-                const double lse = m == -INFINITY ? -(double)INFINITY : (double)a.sc.s * (double)m + log_s;
+                // -inf for a row of -inf alone; beside a NaN m is -inf too, but the sum is NaN
+                const double lse = m == -INFINITY && sum == 0.f ? -(double)INFINITY : (double)a.sc.s * (double)m + log_s;
                 row_log[lane] = log_s;
                 l = __double2float_rn(lse);
                 lo = isfinite(l) ? __double2float_rn(lse - (double)l) : 0.f;

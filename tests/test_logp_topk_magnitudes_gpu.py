@@ -91,3 +91,23 @@ def test_logp_and_lse(kind, temperature, v, dtype):
     lse = torch.where(e["active"], torch.logsumexp(z, 1), 0)
     in_range = lse.float().isfinite()
     close(r.lse[in_range], lse[in_range], (1.2e-5 + U * lse.abs())[in_range])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v", [4000, 151936])
+def test_a_nan_in_a_closed_tile(v, dtype):
+    """A row's NaN makes its results NaN wherever it lies: 8 columns a lane of a warp and step,
+    beside closed columns alone, with open ones in another place of the row or nowhere."""
+    lanes = [0, 5, 16, 31]
+    x = torch.full((2 * len(lanes) + 1, v), -math.inf, device="cuda", dtype=dtype)
+    for i, lane in enumerate(lanes):
+        x[2 * i, v // 2 // 256 * 256 + 8 * lane + i] = math.nan
+        x[2 * i + 1] = x[2 * i]
+        x[2 * i + 1, 3:9] = 1.0      # open
+    x[-1, 3:9] = 1.0
+    y = torch.full((x.shape[0],), 4, device="cuda")
+    r = flp.fused_logp_topk_forward(x, y, 3)
+    for t in (r.logp, r.lse, r.entropy, r.top_logp[:, 0]):
+        assert bool(t[:-1].isnan().all()), t
+    assert bool(x.float().isnan().gather(1, r.top_ids[:, :1])[:-1].all())
+    assert abs(r.logp[-1].item() + math.log(6)) <= 2e-5 and abs(r.entropy[-1].item() - math.log(6)) <= 6e-5

@@ -594,7 +594,9 @@ flp_status logp_grpo_loss_counted(const float* logp, const float* old_logp, cons
  *   lse, lse_lo, entropy, top_ids  the forward's (entropy is not read without
  *             grad_entropy, top_ids not without grad_top); columns in top_ids
  *             that are outside [0, v) count nowhere, the same column twice counts
- *             with the sum of both gradients
+ *             with the sum of both gradients.  Where |lse| is 2^18 or more, lse and
+ *             lse_lo do not hold log S well enough: the row's maximum and sum are
+ *             taken from its logits again
  *   dlogits   `dtype` [n, ld_out], may be logits itself (ld_out == ld); inactive
  *             rows are zeros
  * Deterministic, and a row's results depend on that row only.

@@ -887,7 +887,8 @@ struct TopkBwdArgs {
 
 // The 8 values from p on, at any address: the aligned 16-byte pieces that hold them (up to 15 bytes
 // beyond, inside the piece of one of them), shifted together.  The shift is the same for a row.
-template <Dt D, bool kInPlace>
+// kPlain: of memory that this kernel writes; kWhole: the values are whole pieces.
+template <Dt D, bool kPlain, bool kWhole>
 __device__ __forceinline__ void topk_load_any(const char* p, Unit<D>& u) {
     constexpr int N = Unit<D>::kWords;
     const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
@@ -896,11 +897,11 @@ __device__ __forceinline__ void topk_load_any(const char* p, Unit<D>& u) {
 #pragma unroll
     for (int k = 0; k < N / 4 + 1; ++k) {
         uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (k < N / 4 || (!kInPlace && off != 0))
-            q = kInPlace ? ld_v4(base + 16 * k) : __ldg(reinterpret_cast<const uint4*>(base) + k);
+        if (k < N / 4 || (!kWhole && off != 0))
+            q = kPlain ? ld_v4(base + 16 * k) : __ldg(reinterpret_cast<const uint4*>(base) + k);
         w[4 * k] = q.x; w[4 * k + 1] = q.y; w[4 * k + 2] = q.z; w[4 * k + 3] = q.w;
     }
-    if constexpr (!kInPlace) {   // in place the units lie on the pieces
+    if constexpr (!kWhole) {
 #pragma unroll
         for (int s = 2; s >= 1; s >>= 1) {
             if ((off >> 2) & s) {
@@ -911,30 +912,181 @@ __device__ __forceinline__ void topk_load_any(const char* p, Unit<D>& u) {
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        if constexpr (D == Dt::F32 || kInPlace) u.w[k] = w[k];
+        if constexpr (D == Dt::F32 || kWhole) u.w[k] = w[k];
         else u.w[k] = __funnelshift_r(w[k], w[k + 1], (off & 2u) * 8);
     }
+}
+
+// The columns with a one-hot term, number 0 the target, then the alternatives: this thread's (-1:
+// none), and all in shared memory, which a barrier of the CTA makes readable.
+__device__ __forceinline__ int64_t topk_bwd_columns(const TopkBwdArgs& a, int64_t t, int64_t yt, int64_t* sh_col,
+                                                    float* sh_w) {
+    const int tid = threadIdx.x;
+    int64_t col = -1;
+    float wt = 0.f;
+    if (tid == 0) {
+        col = a.g ? yt : -1;
+        wt = col >= 0 ? __ldg(a.g + t) : 0.f;
+    } else if (a.gt != nullptr && tid <= a.k) {
+        col = __ldg(a.ids + t * a.k + tid - 1);
+        if (col < 0 || col >= a.v) col = -1;
+        wt = col >= 0 ? __ldg(a.gt + t * a.k + tid - 1) : 0.f;
+    }
+    if (tid <= kTopkMax) {
+        sh_col[tid] = col;
+        sh_w[tid] = wt;
+    }
+    return col;
+}
+// G: three of the places a lane, then the butterfly.
+__device__ __forceinline__ float topk_bwd_total(const float* sh_w, int lane) {
+    float G = __fadd_rn(sh_w[lane], sh_w[lane + 32]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) G = __fadd_rn(G, __shfl_xor_sync(0xffffffffu, G, off));
+    return __fadd_rn(G, sh_w[kTopkMax]);
+}
+// s ((w - G) - G expm1(lp) - gh p (lp + H)), w the sum of the gradients of that column.
+template <bool kEntropy>
+__device__ __forceinline__ float topk_bwd_special(const TopkBwdArgs& a, int64_t col, const int64_t* sh_col,
+                                                  const float* sh_w, float lp, float G, float gh, float H) {
+    float sum = 0.f;
+    for (int j = 0; j <= a.k; ++j) sum += sh_col[j] == col ? sh_w[j] : 0.f;
+    float ds = __fsub_rn(__fsub_rn(sum, G), __fmul_rn(G, expm1f(lp)));
+    if (kEntropy) ds = __fmaf_rn(-gh, __fmul_rn(expf(lp), __fadd_rn(lp, H)), ds);
+    return __fmul_rn(a.s, ds);
+}
+template <Dt D>
+__device__ __forceinline__ void topk_bwd_put(char* dr, int64_t col, float d) {
+    if constexpr (D == Dt::F32) reinterpret_cast<float*>(dr)[col] = d;
+    else if constexpr (D == Dt::BF16)
+        reinterpret_cast<uint16_t*>(dr)[col] = (uint16_t)(pack_bf16x2(d, d) & 0xffffu);
+    else reinterpret_cast<uint16_t*>(dr)[col] = (uint16_t)(pack_f16x2(d, d) & 0xffffu);
+}
+
+// Rows of a large |LSE| (and of one without a number): beside it neither LSE nor its rounding residual
+// holds log S, and a floor below it may be LSE itself.  One CTA takes the row, finds its
+// maximum M and sum again and forms lp = s (x - M) - log S of each column.  Two passes more
+// over rows that are rare: closed by a finite fill throughout, or of a temperature below
+// 1e-5 or so.  One of 151936 BF16 takes 260 us, 256 of them 427 (ordinary rows 3.5 and 27).
+constexpr float kTopkFarLse = 262144.f;
+// Below the floor p is 0.
+__device__ __forceinline__ float topk_bwd_floor(const TopkBwdArgs& a, float l) {
+    return __fmul_rn(__fsub_rn(l, 200.f), a.inv_s);
+}
+__device__ __forceinline__ bool topk_bwd_far(float l, float fl) { return !(fabsf(l) < kTopkFarLse && fl > -3e38f); }
+// An active row's target, -1 without targets; -2: not active.
+__device__ __forceinline__ int64_t topk_bwd_target(const TopkBwdArgs& a, int64_t t) {
+    if (a.mask != nullptr && __ldg(a.mask + t) == 0) return -2;
+    if (a.y == nullptr) return -1;
+    const int64_t y = __ldg(a.y + t);
+    return y >= 0 && y < a.v && y != a.ignore_index ? y : -2;
+}
+template <Dt D, bool kEntropy>
+__device__ __noinline__ void topk_bwd_far_row(const TopkBwdArgs& a, int64_t t, int64_t* sh_col, float* sh_w) {
+    const int64_t yt = topk_bwd_target(a, t);
+    const float l = __ldg(a.lse + t);
+    if (yt == -2 || !topk_bwd_far(l, topk_bwd_floor(a, l))) return;   // the same for the whole CTA
+    constexpr int EB = Unit<D>::kElemBytes, NW = Unit<D>::kWords, kWarps = kBwdThreads / kWarp, kB = D == Dt::F32 ? 1 : 2;
+    __shared__ float sh_max[kWarps];
+    __shared__ double sh_sum[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const char* xr = static_cast<const char*>(a.x) + t * a.ld * EB;   // dx may be x: plain loads
+    char* dr = static_cast<char*>(a.dx) + t * a.ld_out * EB;
+    const bool vec_out = (reinterpret_cast<uintptr_t>(dr) & 15u) == 0;
+    // f(c, u) for the units of this thread, kB loaded together: the same wherever the row lies
+    auto each = [&](auto&& f) {
+#pragma unroll 1
+        for (int64_t c0 = 8 * tid; c0 < a.v; c0 += kB * 8 * kBwdThreads) {
+            Unit<D> u[kB];
+#pragma unroll
+            for (int b = 0; b < kB; ++b) {
+                const int64_t c = c0 + b * 8 * kBwdThreads;
+                if (c + 8 <= a.v) topk_load_any<D, true, false>(xr + c * EB, u[b]);
+                else if (c < a.v) bwd_load<D, false, true>(xr, c, a.v, u[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < kB; ++b) {
+                const int64_t c = c0 + b * 8 * kBwdThreads;
+                if (c < a.v) f(c, u[b]);
+            }
+        }
+    };
+    const int64_t col = topk_bwd_columns(a, t, yt, sh_col, sh_w);
+    float M = -INFINITY;
+    each([&](int64_t c, const Unit<D>& u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < a.v) M = f_max_nan(M, topk_element<D>(u.w, e));
+    });
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) M = f_max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (lane == 0) sh_max[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = f_max_nan(M, sh_max[w]);
+    double S = 0.0;
+    each([&](int64_t c, const Unit<D>& u) {
+        float p = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < a.v) p += expf(__fmul_rn(a.s, __fsub_rn(topk_element<D>(u.w, e), M)));
+        S += (double)p;
+    });
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) S += __shfl_xor_sync(0xffffffffu, S, off);
+    if (lane == 0) sh_sum[warp] = S;
+    __syncthreads();
+    S = 0.0;
+    for (int w = 0; w < kWarps; ++w) S += sh_sum[w];
+    const float log_s = (float)log(S), G = topk_bwd_total(sh_w, lane);
+    const float gh = kEntropy ? __ldg(a.gh + t) : 0.f, H = kEntropy ? __ldg(a.entropy + t) : 0.f;
+    auto logp = [&](float x) {   // at -200 p is 0, and times a number
+        return f_max_nan(__fsub_rn(__fmul_rn(a.s, __fsub_rn(x, M)), log_s), -200.f);
+    };
+    float ds = 0.f;
+    if (col >= 0) {
+        const float lp = logp(bits_value<D>(elem_bits_plain<D>(xr, col)));
+        ds = topk_bwd_special<kEntropy>(a, col, sh_col, sh_w, lp, G, gh, H);
+    }
+    __syncthreads();   // the logits of the columns apart are read
+    each([&](int64_t c, const Unit<D>& u) {
+        uint32_t out[NW];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float d[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float lp = logp(topk_element<D>(u.w, 2 * k + e));
+                const float q = kEntropy ? __fmaf_rn(gh, __fadd_rn(lp, H), G) : G;
+                d[e] = __fmul_rn(-a.s, __fmul_rn(expf(lp), q));
+            }
+            put_pair<D>(out, k, d[0], d[1]);
+        }
+        if (vec_out) bwd_store<D, true>(dr, c, a.v, out);
+        else bwd_store<D, false>(dr, c, a.v, out);
+    });
+    __syncthreads();   // the row is stored; sh_col and sh_w are read
+    if (col >= 0) topk_bwd_put<D>(dr, col, ds);
 }
 
 // One CTA per (segment of kBwdSegCols columns, row), elementwise; exp as in k_logp_bwd.
 // The columns with a one-hot term (target and alternatives, at most 65) that lie in the
 // segment are computed apart by a thread each, from logits read before any store (dx may be
-// x), and stored after the segment:
-//   s ((w - G) - G expm1(lp) - gh p (lp + H)), w the sum of the gradients of that column:
-// for the target alone w = G and nothing cancels.
+// x), and stored after the segment: for the target alone w = G and nothing cancels.
 //
 // kShift: rows of any alignment.  A thread's units then lie on the 16-byte pieces of dx's row (the
 // first starts up to 7 columns before it), x's are shifted out of two pieces.  (By elements, 2048 x
 // 151936 BF16 in rows 151937 apart took 709 us, 275 so; aligned rows 179.)
 template <Dt D, bool kShift, bool kInPlace, bool kEntropy>
 __global__ void __launch_bounds__(kBwdThreads, kBwdMinBlocks<D>)
-k_logp_topk_bwd(TopkBwdArgs a) {
+k_logp_topk_bwd(const __grid_constant__ TopkBwdArgs a) {
     constexpr int EB = Unit<D>::kElemBytes, NW = Unit<D>::kWords;
     constexpr int kBatch = kShift ? kBwdUnitsPerThread / 2 : kBwdUnitsPerThread;   // units loaded together
     __shared__ int64_t sh_col[kTopkMax + 1];
     __shared__ float sh_w[kTopkMax + 1];
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t cs = (int64_t)kBwdThreads * 8;
+    bool far = false;   // one of the rows is left to topk_bwd_far_row
 #pragma unroll 1
     for (int64_t t = blockIdx.y; t < a.n; t += gridDim.y) {
         const char* xr = static_cast<const char*>(a.x) + t * a.ld * EB;
@@ -947,7 +1099,7 @@ k_logp_topk_bwd(TopkBwdArgs a) {
             if constexpr (!kShift) {
                 bwd_load<D, true, kInPlace>(xr, c, a.v, u);
             } else if (c >= 0 && c + 8 <= a.v) {
-                topk_load_any<D, kInPlace>(xr + c * EB, u);
+                topk_load_any<D, kInPlace, kInPlace>(xr + c * EB, u);   // in place the units are whole pieces
             } else {
 #pragma unroll
                 for (int k = 0; k < NW; ++k) u.w[k] = 0u;
@@ -973,13 +1125,9 @@ k_logp_topk_bwd(TopkBwdArgs a) {
                     }
             }
         };
-        bool act = a.mask == nullptr || __ldg(a.mask + t) != 0;
-        int64_t yt = -1;
-        if (a.y != nullptr) {
-            yt = __ldg(a.y + t);
-            act = act && yt >= 0 && yt < a.v && yt != a.ignore_index;
-        }
-        if (!act) {   // the same for the whole CTA
+        const float l = __ldg(a.lse + t);
+        const int64_t yt = topk_bwd_target(a, t);
+        if (yt == -2) {   // the same for the whole CTA
             uint32_t z[NW];
 #pragma unroll
             for (int j = 0; j < NW; ++j) z[j] = 0u;
@@ -988,44 +1136,30 @@ k_logp_topk_bwd(TopkBwdArgs a) {
                 if (col0 + u * cs < a.v) store(col0 + u * cs, z);
             continue;
         }
+        const float fl = topk_bwd_floor(a, l);
+        if (topk_bwd_far(l, fl)) {   // the same for the whole CTA, and the row
+            far = true;
+            continue;
+        }
         Unit<D> w[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
             if (col0 + u * cs < a.v) load(col0 + u * cs, w[u]);
 
-        // the one-hot columns: number 0 the target, then the alternatives
-        int64_t col = -1;
-        float wt = 0.f;
-        if (tid == 0) {
-            col = a.g ? yt : -1;
-            wt = col >= 0 ? __ldg(a.g + t) : 0.f;
-        } else if (a.gt != nullptr && tid <= a.k) {
-            col = __ldg(a.ids + t * a.k + tid - 1);
-            if (col < 0 || col >= a.v) col = -1;
-            wt = col >= 0 ? __ldg(a.gt + t * a.k + tid - 1) : 0.f;
-        }
-        if (tid <= kTopkMax) {
-            sh_col[tid] = col;
-            sh_w[tid] = wt;
-        }
+        const int64_t col = topk_bwd_columns(a, t, yt, sh_col, sh_w);
         const bool special = col >= 0 && col >= seg0 && col < seg0 + kBwdSegCols;   // (seg0 may lie before the row)
         float xs = 0.f;
         if (special) xs = bits_value<D>(kInPlace ? elem_bits_plain<D>(xr, col) : elem_bits<D>(xr, col));
         const bool any = __syncthreads_or(special);   // also: the logits of the columns apart are read
-        // G: three of the places a lane, then the butterfly
-        float G = __fadd_rn(sh_w[lane], sh_w[lane + 32]);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) G = __fadd_rn(G, __shfl_xor_sync(0xffffffffu, G, off));
-        G = __fadd_rn(G, sh_w[kTopkMax]);
+        const float G = topk_bwd_total(sh_w, lane);
 
-        const float l = __ldg(a.lse + t), l_lo = a.lse_lo ? __ldg(a.lse_lo + t) : 0.f;
+        const float l_lo = a.lse_lo ? __ldg(a.lse_lo + t) : 0.f;
         const float gh = kEntropy ? __ldg(a.gh + t) : 0.f, H = kEntropy ? __ldg(a.entropy + t) : 0.f;
         BwdRow r;
         r.s = a.s;
         r.gs = __fmul_rn(a.s, G);
         r.lr = (fabsf(l) < 8388608.f) ? __fmul_rn(rintf(__fmul_rn(l, 65536.f)), 1.f / 65536.f) : l;
         r.delta = __fadd_rn(__fsub_rn(l, r.lr), l_lo);   // l - lr is exact
-        const float fl = __fmul_rn(__fsub_rn(l, 200.f), a.inv_s);
         r.floor_f = fl;
         r.floor_w = 0xff80ff80u;
         if constexpr (D == Dt::BF16) {
@@ -1034,9 +1168,9 @@ k_logp_topk_bwd(TopkBwdArgs a) {
         }
         r.neg_lr = f2(-r.lr, -r.lr);
         r.s2 = f2(a.s, a.s);
-        // -s (1 - delta + b), with b for the bias of ex2; times G, or times G + gh (lp + H)
+        // -s (e^-delta + b), with b for the bias of ex2; times G, or times G + gh (lp + H)
         const float base = kEntropy ? a.s : r.gs;
-        const float coef = __fmaf_rn(base, __fsub_rn(r.delta, kEx2BiasComp), -base);
+        const float coef = __fmaf_rn(base, __fsub_rn(bwd_rest(r.delta), kEx2BiasComp), -base);
         r.coef2 = f2(coef, coef);
         const float g0 = __fmaf_rn(gh, __fsub_rn(H, r.delta), G);
         const u64 g02 = f2(g0, g0), gh2 = f2(gh, gh), l2e = f2(kLog2e, kLog2e);
@@ -1044,12 +1178,8 @@ k_logp_topk_bwd(TopkBwdArgs a) {
 
         float ds = 0.f;
         if (special) {
-            float sum = 0.f;
-            for (int j = 0; j <= a.k; ++j) sum += sh_col[j] == col ? sh_w[j] : 0.f;
             const float lp = __fsub_rn(__fmaf_rn(a.s, fmaxf(xs, fl), -r.lr), r.delta);
-            ds = __fsub_rn(__fsub_rn(sum, G), __fmul_rn(G, expm1f(lp)));
-            if (kEntropy) ds = __fmaf_rn(-gh, __fmul_rn(expf(lp), __fadd_rn(lp, H)), ds);
-            ds = __fmul_rn(a.s, ds);
+            ds = topk_bwd_special<kEntropy>(a, col, sh_col, sh_w, lp, G, gh, H);
         }
 #pragma unroll
         for (int half = 0; half < kBwdUnitsPerThread / kBatch; ++half) {
@@ -1081,12 +1211,11 @@ k_logp_topk_bwd(TopkBwdArgs a) {
             }
         }
         __syncthreads();   // the segment is stored; sh_col and sh_w are read
-        if (any && special) {
-            if constexpr (D == Dt::F32) reinterpret_cast<float*>(dr)[col] = ds;
-            else if constexpr (D == Dt::BF16)
-                reinterpret_cast<uint16_t*>(dr)[col] = (uint16_t)(pack_bf16x2(ds, ds) & 0xffffu);
-            else reinterpret_cast<uint16_t*>(dr)[col] = (uint16_t)(pack_f16x2(ds, ds) & 0xffffu);
-        }
+        if (any && special) topk_bwd_put<D>(dr, col, ds);
+    }
+    if (far && blockIdx.x == 0) {
+#pragma unroll 1
+        for (int64_t t = blockIdx.y; t < a.n; t += gridDim.y) topk_bwd_far_row<D, kEntropy>(a, t, sh_col, sh_w);
     }
 }
 

@@ -333,6 +333,14 @@ struct BwdRow {
     float lr, delta, gs, s;
 };
 
+// 1 - e^-delta for what the rounded LSE leaves (LSE = lr + delta): delta itself, of which the square is
+// below a rounding, up to 2^-11.  From |LSE| = 2^13 on it may be more, 2^-6 at 2^18: three terms of the
+// series (the next is below 2^-28).
+__device__ __forceinline__ float bwd_rest(float delta) {
+    const float more = __fmul_rn(delta, __fmaf_rn(delta, __fmaf_rn(delta, 1.f / 6.f, -0.5f), 1.f));
+    return fabsf(delta) < 0x1p-11f ? delta : more;
+}
+
 // The pair (x_{2k}, x_{2k+1}) of a unit widened to binary32 and raised to the
 // row's floor.
 template <Dt D>

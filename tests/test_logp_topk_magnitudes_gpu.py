@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import selected_token_logprob_gb300 as flp
-from test_logp_topk_gpu import close, exact
+from test_logp_topk_gpu import HALF, TINY, close, exact, exact_grad
 
 pytestmark = pytest.mark.gpu
 TYPES = [torch.bfloat16, torch.float16, torch.float32]
@@ -111,3 +111,36 @@ def test_a_nan_in_a_closed_tile(v, dtype):
         assert bool(t[:-1].isnan().all()), t
     assert bool(x.float().isnan().gather(1, r.top_ids[:, :1])[:-1].all())
     assert abs(r.logp[-1].item() + math.log(6)) <= 2e-5 and abs(r.entropy[-1].item() - math.log(6)) <= 6e-5
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v", [40, 5000, 151936])
+@pytest.mark.parametrize("kind,temperature", CASES)
+def test_backward(kind, temperature, v, dtype):
+    x, y, r, e, g = case(kind, temperature, v, dtype)
+    n, k = r.top_ids.shape
+    s = float(torch.tensor(1 / temperature, dtype=torch.float32))
+    gl = torch.randn(n, generator=g, device="cuda") / s
+    gh = torch.rand(n, generator=g, device="cuda") / s
+    gt = torch.rand((n, k), generator=g, device="cuda") / s
+    for up in ((gl, gh, gt), (gl, None, None), (None, gh, None), (None, None, gt)):
+        want, size = exact_grad(e, y, *up, temperature=temperature)
+        # as there; the factors lp + H count for |lp| <= 88 (p is 0 below)
+        tol = want.abs() * HALF[dtype] + TINY[dtype] + size * 2e-5 * (88 if up[1] is not None else 2)
+        # p below 2^-126 is flushed to 0: off by that times the factor s (G + gh (lp + H)) beside it
+        factor = sum(0 if u is None else (u if u.dim() == 1 else u.sum(1)).abs() for u in (up[0], up[2]))
+        if up[1] is not None:
+            factor = factor + up[1] * (88 + e["h"])
+        tol = tol + 2.0 ** -126 * s * factor.double()[:, None]
+        got = flp.fused_logp_topk_backward(x, y, r, *up, temperature=temperature)
+        close(got, want, tol)
+        own = x.clone()
+        assert flp.fused_logp_topk_backward(own, y, r, *up, temperature=temperature, dlogits=own) is own
+        assert torch.equal(own, got)
+        # rows of another alignment
+        buf = torch.full((n * (v + 3) + 8,), 5.0, dtype=dtype, device="cuda")
+        out = buf[1:1 + n * (v + 3)].view(n, v + 3)[:, :v]
+        flp.fused_logp_topk_backward(x, y, r, *up, temperature=temperature, dlogits=out)
+        assert torch.equal(out, got)
+        out.fill_(5.0)
+        assert bool((buf == 5.0).all())

@@ -95,6 +95,9 @@ int64_t flp_tile_width(int64_t v);
  *            (LSE - lse, |lse_lo| <= half an ulp of lse).  Passing it to the
  *            backward removes the FP32 quantisation of the LSE from the
  *            gradient (an addition of this library; the pages store FP32 only).
+ *            Both together hold LSE to 2^-48 |LSE|, and where M times the inverse
+ *            temperature is a binary32 number (temperature 1) log S to 2^-24
+ *            whatever M is.
  * Any alignment and any ld are accepted.  16-byte aligned rows with ld % 8 == 0
  * (and v < 2^31) stream through per-warp bulk-copy (TMA) rings in shared
  * memory; other layouts take a scalar-load path with the same arithmetic

@@ -100,8 +100,8 @@ struct BwdArgs {
 template <flp::Dt D, bool VI, bool VO, bool IP>
 void launch_bwd(const BwdArgs& a, dim3 grid) {
     flp::k_logp_bwd<D, VI, VO, IP><<<grid, flp::kBwdThreads, 0, a.st>>>(
-        a.x, a.n, a.v, a.ld, a.y, a.ii, a.mask, a.s, a.inv_s, a.lse, a.lse_lo, a.g, a.dx, a.ld_out, a.y_off,
-        a.v_total);
+        flp::LogpBwdArgs{a.x, a.n, a.v, a.ld, a.y, a.ii, a.mask, a.s, a.inv_s, a.lse, a.lse_lo, a.g, a.dx, a.ld_out, a.y_off,
+                         a.v_total});
 }
 
 template <flp::Dt D>

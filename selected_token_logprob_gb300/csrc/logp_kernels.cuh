@@ -305,23 +305,69 @@ k_logp_merge(const float* __restrict__ pm, const float* __restrict__ ps,
 // local column y_t - y_off only when that lies in [0, v).  Every element is
 // computed from the same per-row constants as in the unsharded call, so the
 // shards' outputs side by side are the unsharded gradient bit for bit.
+struct LogpBwdArgs {
+    const void* x;
+    int64_t n, v, ld;
+    const int64_t* y;
+    int64_t ignore_index;
+    const uint8_t* mask;
+    float s, inv_s;
+    const float *lse, *lse_lo, *g;
+    void* dx;
+    int64_t ld_out, y_off, v_total;
+};
+
+// This CTA's segment of a row of a large |LSE| l.
 template <Dt D, bool kVecIn, bool kVecOut, bool kInPlace>
-__global__ void __launch_bounds__(kBwdThreads, kBwdMinBlocks<D>)
-k_logp_bwd(const void* x, int64_t n, int64_t v, int64_t ld, const int64_t* __restrict__ y,
-           int64_t ignore_index, const uint8_t* __restrict__ mask, float s, float inv_s,
-           const float* __restrict__ lse, const float* __restrict__ lse_lo,
-           const float* __restrict__ g, void* dx, int64_t ld_out, int64_t y_off, int64_t v_total) {
+__device__ __forceinline__ void logp_bwd_far_row(const LogpBwdArgs& a, int64_t t, int64_t yt, float l) {
     constexpr int EB = Unit<D>::kElemBytes;
-    constexpr int NW = Unit<D>::kWords;
-    // grid: x = segment of the row, y = row (strided when n > gridDim.y)
+    const float lo = __fadd_rn(__fsub_rn(l, l), a.lse_lo ? __ldg(a.lse_lo + t) : 0.f), gs = __fmul_rn(a.s, __ldg(a.g + t));
+    const char* xr = static_cast<const char*>(a.x) + t * a.ld * EB;
+    char* dr = static_cast<char*>(a.dx) + t * a.ld_out * EB;
     const int64_t col0 = (int64_t)blockIdx.x * kBwdSegCols + (int64_t)threadIdx.x * 8;
 #pragma unroll 1
-    for (int64_t t = blockIdx.y; t < n; t += gridDim.y) {
-        const char* xr = reinterpret_cast<const char*>(x) + t * ld * EB;
-        char* dr = reinterpret_cast<char*>(dx) + t * ld_out * EB;
-        const int64_t yt = __ldg(y + t);
+    for (int u = 0; u < kBwdUnitsPerThread; ++u) {
+        const int64_t c = col0 + (int64_t)u * kBwdThreads * 8;
+        if (c >= a.v) break;
+        Unit<D> w;
+        uint32_t o[Unit<D>::kWords];
+        bwd_load<D, kVecIn, kInPlace>(xr, c, a.v, w);
+        bwd_unit_far<D>(w, a.s, gs, l, lo, yt - a.y_off - c, o);
+        bwd_store<D, kVecOut>(dr, c, a.v, o);
+    }
+}
+// Of all its rows, those of a large |LSE|.
+template <Dt D, bool kVecIn, bool kVecOut, bool kInPlace>
+__device__ __noinline__ void logp_bwd_far_rows(const LogpBwdArgs& a) {
+#pragma unroll 1
+    for (int64_t t = blockIdx.y; t < a.n; t += gridDim.y) {
+        const int64_t yt = __ldg(a.y + t);
+        const float l = __ldg(a.lse + t);
+        if (row_active(a.mask, t, yt, a.v_total, a.ignore_index) && bwd_far(l))
+            logp_bwd_far_row<D, kVecIn, kVecOut, kInPlace>(a, t, yt, l);
+    }
+}
+
+template <Dt D, bool kVecIn, bool kVecOut, bool kInPlace>
+__global__ void __launch_bounds__(kBwdThreads, kBwdMinBlocks<D>)
+k_logp_bwd(const __grid_constant__ LogpBwdArgs a) {
+    constexpr int EB = Unit<D>::kElemBytes;
+    constexpr int NW = Unit<D>::kWords;
+    const int64_t v = a.v;
+    // grid: x = segment of the row, y = row (strided when n > gridDim.y)
+    const int64_t col0 = (int64_t)blockIdx.x * kBwdSegCols + (int64_t)threadIdx.x * 8;
+    // Rows of a large |LSE|: where rows are vectors their code in the loop costs nothing, element by element
+    // it does (2048 x 32003 FP16 in place 172 us, 166 by a call behind the loop; the call costs vectors 1%).
+    constexpr bool kFarInLoop = kVecIn && kVecOut;
+    bool far = false;
+#pragma unroll 1
+    for (int64_t t = blockIdx.y; t < a.n; t += gridDim.y) {
+        const char* xr = static_cast<const char*>(a.x) + t * a.ld * EB;
+        char* dr = static_cast<char*>(a.dx) + t * a.ld_out * EB;
+        const int64_t yt = __ldg(a.y + t);
+        const float l = __ldg(a.lse + t);
         const int64_t cs = (int64_t)kBwdThreads * 8;
-        if (!row_active(mask, t, yt, v_total, ignore_index)) {
+        if (!row_active(a.mask, t, yt, a.v_total, a.ignore_index)) {
             uint32_t z[NW];
 #pragma unroll
             for (int k = 0; k < NW; ++k) z[k] = 0u;
@@ -330,16 +376,20 @@ k_logp_bwd(const void* x, int64_t n, int64_t v, int64_t ld, const int64_t* __res
                 if (col0 + u * cs < v) bwd_store<D, kVecOut>(dr, col0 + u * cs, v, z);
             continue;
         }
+        if (bwd_far(l)) {   // the same for the whole row
+            if constexpr (kFarInLoop) logp_bwd_far_row<D, kVecIn, kVecOut, kInPlace>(a, t, yt, l);
+            else far = true;
+            continue;
+        }
         BwdRow r;
-        const float l = __ldg(lse + t);
-        const float l_lo = lse_lo ? __ldg(lse_lo + t) : 0.f;
-        r.s = s;
-        r.gs = __fmul_rn(s, __ldg(g + t));
-        r.lr = (fabsf(l) < 8388608.f) ? __fmul_rn(rintf(__fmul_rn(l, 65536.f)), 1.f / 65536.f) : l;
+        const float l_lo = a.lse_lo ? __ldg(a.lse_lo + t) : 0.f;
+        r.s = a.s;
+        r.gs = __fmul_rn(a.s, __ldg(a.g + t));
+        r.lr = __fmul_rn(rintf(__fmul_rn(l, 65536.f)), 1.f / 65536.f);
         r.delta = __fadd_rn(__fsub_rn(l, r.lr), l_lo);           // l - lr is exact
-        // -s g (1 - delta), times (1 + b) for the mean bias b of ex2.approx
-        const float coef = __fmaf_rn(r.gs, __fsub_rn(r.delta, kEx2BiasComp), -r.gs);
-        const float fl = __fmul_rn(__fsub_rn(l, 200.f), inv_s);   // ~ (LSE - 200) / s
+        // -s g e^-delta, times (1 + b) for the mean bias b of ex2.approx
+        const float coef = __fmaf_rn(r.gs, __fsub_rn(bwd_rest(r.delta), kEx2BiasComp), -r.gs);
+        const float fl = __fmul_rn(__fsub_rn(l, 200.f), a.inv_s);   // ~ (LSE - 200) / s
         r.floor_f = fl;
         r.floor_w = 0xff80ff80u;
         if constexpr (D == Dt::BF16) {
@@ -347,7 +397,7 @@ k_logp_bwd(const void* x, int64_t n, int64_t v, int64_t ld, const int64_t* __res
             r.floor_w = b | (b << 16);
         }
         r.neg_lr = f2(-r.lr, -r.lr);
-        r.s2 = f2(s, s);
+        r.s2 = f2(a.s, a.s);
         r.coef2 = f2(coef, coef);
 
         Unit<D> w[kBwdUnitsPerThread];
@@ -358,10 +408,13 @@ k_logp_bwd(const void* x, int64_t n, int64_t v, int64_t ld, const int64_t* __res
         for (int u = 0; u < kBwdUnitsPerThread; ++u) {
             if (col0 + u * cs < v) {
                 uint32_t o[NW];
-                bwd_unit<D>(w[u], r, yt - y_off - (col0 + u * cs), o);
+                bwd_unit<D>(w[u], r, yt - a.y_off - (col0 + u * cs), o);
                 bwd_store<D, kVecOut>(dr, col0 + u * cs, v, o);
             }
         }
+    }
+    if constexpr (!kFarInLoop) {
+        if (far) logp_bwd_far_rows<D, kVecIn, kVecOut, kInPlace>(a);
     }
 }
 

@@ -717,6 +717,8 @@ k_logp_topk_finish(TopkArgs a, TopkOut o) {
                 row_log[lane] = log_s;
                 l = __double2float_rn(lse);
                 lo = isfinite(l) ? __double2float_rn(lse - (double)l) : 0.f;
+                if (fabsf(__fmul_rn(a.sc.s, m)) >= kLseFar && isfinite(l))   // as finalize_row
+                    lo = __double2float_rn(((double)a.sc.s * (double)m - (double)l) + log_s);
                 // around the maximum, as the alternatives: next to a large one LSE has no digits left for log S
                 lp = __double2float_rn((double)a.sc.s * ((double)row_x[lane] - (double)m) - log_s);
                 h = __fmaf_rn(-(float)kLn2, __fdiv_rn(row_t[lane], sum), logf(sum));

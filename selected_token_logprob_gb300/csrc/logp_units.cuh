@@ -305,13 +305,21 @@ __device__ __forceinline__ MS tile_fold16(MS p, float s) {
 // are exact there) and each output rounded once to binary32 (the "downcast at
 // final write" of issue #241 Goal).  lse_lo, when given, receives the binary32
 // rounding residual of the LSE (LSE - lse), so that lse + lse_lo carries the
-// LSE to about 2^-48 relative for the backward.
+// LSE to about 2^-48 relative for the backward.  From kLseFar on double has few
+// digits left for log S in s M + log S: there it is added last.
+constexpr float kLseFar = 134217728.f;   // 2^27
 __device__ __forceinline__ void finalize_row(MS f, bool active, float x_y, float s, float* logp_out,
                                              float* lse_out, float* lse_lo_out) {
-    const double l = (f.m == -INFINITY) ? -(double)INFINITY
-                                        : (double)s * (double)f.m + log((double)f.s);
+    const double log_s = log((double)f.s);
+    const double l = (f.m == -INFINITY) ? -(double)INFINITY : (double)s * (double)f.m + log_s;
     const float lf = __double2float_rn(l);
     *lse_out = lf;
+    if (fabsf(__fmul_rn(s, f.m)) >= kLseFar && isfinite(f.m)) {   // known before the FP64 above
+        const double top = (double)s * (double)f.m;
+        if (lse_lo_out) *lse_lo_out = isfinite(lf) ? __double2float_rn((top - (double)lf) + log_s) : 0.f;
+        *logp_out = active ? __double2float_rn(((double)s * (double)x_y - top) - log_s) : 0.f;
+        return;
+    }
     if (lse_lo_out) *lse_lo_out = isfinite(lf) ? __double2float_rn(l - (double)lf) : 0.f;
     *logp_out = active ? __double2float_rn((double)s * (double)x_y - l) : 0.f;
 }
@@ -413,6 +421,34 @@ __device__ __forceinline__ void bwd_unit(const Unit<D>& u, const BwdRow& r, int6
             for (int k = 0; k < 4; ++k)
                 if (k == kt) o[k] = (jt & 1) ? ((o[k] & 0xffffu) | (bt << 16)) : ((o[k] & 0xffff0000u) | bt);
         }
+    }
+}
+
+// A row of a large |LSE|, beside which a floor may be LSE itself (or of one that is not finite).
+constexpr float kBwdFarLse = 262144.f;
+__device__ __forceinline__ bool bwd_far(float l) { return !(fabsf(l) < kBwdFarLse); }
+// Gradient of a unit in such a row: the logits as they are, p = e^lp with lp = (s x - l) - lo, not below
+// -200, where p is 0.  lo: the rounding residual of l = LSE, NaN where that is not finite.
+template <Dt D>
+__device__ __forceinline__ void bwd_unit_far(const Unit<D>& u, float s, float gs, float l, float lo, int64_t jt,
+                                             uint32_t (&o)[Unit<D>::kWords]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float x[2], d[2];
+        if constexpr (D == Dt::F32) {
+            x[0] = __uint_as_float(u.w[2 * k]);
+            x[1] = __uint_as_float(u.w[2 * k + 1]);
+        } else {
+            x[0] = D == Dt::BF16 ? bf_lo(u.w[k]) : h_lo(u.w[k]);
+            x[1] = D == Dt::BF16 ? bf_hi(u.w[k]) : h_hi(u.w[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float lp = __fsub_rn(__fmaf_rn(s, x[e], -l), lo);
+            lp = lp < -200.f ? -200.f : lp;   // a NaN stays
+            d[e] = __fmul_rn(-gs, 2 * k + e == jt ? expm1f(lp) : expf(lp));
+        }
+        put_pair<D>(o, k, d[0], d[1]);
     }
 }
 

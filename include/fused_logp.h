@@ -892,6 +892,15 @@ flp_status flp_selftest_orthogonalize_form(int product, int64_t batch, int64_t r
 flp_status flp_selftest_fp8_form(int64_t m, int64_t n, int64_t k, int b_square, int sms, int* bn, int* split);
 
 /*
+ * Self-test of the bounded waits of flp_fp8_matmul: one warp waits on a signal
+ * that nothing gives.  With `aborted` its CTA's abort flag is set from the start
+ * and every wait has to see it at once; without, the epilogue's wait has to run
+ * out (within about 2 s) and sets the device error word.  *gave_up is 1 when they
+ * did.
+ */
+flp_status flp_selftest_fp8_wait(int device, int aborted, int* gave_up);
+
+/*
  * Self-test of the norm's backward where the rows' CTAs are fewer than those that
  * can be resident (as on a part with more SMs than the rows' grid is sized for, 152):
  * fused_layer_norm_backward with that grid sized for `sms` (1 to 152) of them.

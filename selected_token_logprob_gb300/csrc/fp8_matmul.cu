@@ -253,6 +253,18 @@ flp_status flp_fp8_matmul(const void* a, int64_t m, int64_t k, int64_t ld_a, con
     }
 }
 
+flp_status flp_selftest_fp8_wait(int device, int aborted, int* gave_up) {
+    if (gave_up == nullptr) return fail(FLP_EINVAL, "gave_up is a null pointer");
+    DeviceGuard guard;
+    flp_status st;
+    if ((st = guard.enter(device)) != FLP_OK) return st;
+    flp::k_fp8_wait_selftest<<<1, 32>>>(aborted != 0);
+    if ((st = check_launch("fp8 wait self-test")) != FLP_OK) return st;
+    const cudaError_t e = cudaMemcpyFromSymbol(gave_up, flp::g_fp8_selftest, sizeof *gave_up);
+    if (e != cudaSuccess) return fail(FLP_ECUDA, "fp8 wait self-test: %s", cudaGetErrorString(e));
+    return ok();
+}
+
 flp_status flp_selftest_fp8_form(int64_t m, int64_t n, int64_t k, int b_square, int sms, int* bn, int* split) {
     if (m < 1 || n < 1 || k < 1 || sms < 2 || bn == nullptr || split == nullptr)
         return fail(FLP_EINVAL, "m, n and k must be >= 1, sms >= 2 and the outputs not null");

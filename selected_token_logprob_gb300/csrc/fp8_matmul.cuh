@@ -66,17 +66,26 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, volatile
         }
     }
 }
-// The same with a bound on its probes alone, for the epilogue, where the other's clock and flag cost
-// registers (4096 x 8192 x 4096 114 us, 105 so).  A probe in vain takes 3100 cycles: 2^20 of them 1.7 s.
+// The same for the epilogue, where the other's clock costs registers (4096 x 8192 x 4096 114 us, 102 so):
+// by the clock's upper half alone, of which a tick is 2^32 cycles, about 2 s; it gives up with tick
+// kTicks.
+__device__ __forceinline__ uint32_t fp8_clock_hi() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%clock_hi;" : "=r"(t));
+    return t;
+}
+template <uint32_t kTicks = 2>
 __device__ __forceinline__ bool fp8_wait_short(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    uint32_t probes = 0;
+    const uint32_t t0 = fp8_clock_hi();
 #pragma unroll 1
-    while (!mbar_try(bar, parity))
-        if (++probes == (1u << 20)) {
+    while (!mbar_try(bar, parity)) {
+        const bool late = fp8_clock_hi() - t0 >= kTicks;
+        if (late || *abort_flag != 0) {
             *abort_flag = 1;
-            atomicExch(&g_fp8_error, 1);
+            if (late) atomicExch(&g_fp8_error, 1);
             return false;
         }
+    }
     return true;
 }
 // The signal of a read accumulator to the even CTA: what it orders is tensor memory (the fences
@@ -828,6 +837,25 @@ k_fp8_tokens(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         tc_fence_after();
         tmem_dealloc(tmem, kCols);
     }
+}
+
+// Self-test of the waits: a warp waits for what nothing does, with the CTA's abort flag set from the
+// start or not (then by the short wait alone, until the clock's next tick).
+static __device__ int g_fp8_selftest;
+static __global__ void __launch_bounds__(32) k_fp8_wait_selftest(int aborted) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int flag;
+    const uint32_t b = smem_u32(&bar);
+    if (threadIdx.x == 0) {
+        mbar_init(b, 1);
+        fence_mbar_init();
+        flag = aborted;
+    }
+    __syncwarp();
+    bool done = fp8_wait_short<1>(b, 0, &flag);
+    if (aborted) done = fp8_wait(b, 0, &flag) || fp8_wait_cluster(b, 0, &flag) || done;
+    done = __any_sync(0xffffffffu, done);
+    if (threadIdx.x == 0) g_fp8_selftest = done ? 0 : 1;
 }
 
 }  // namespace flp

@@ -497,7 +497,8 @@ k_fp8_pair(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUt
 #pragma unroll
             for (int j = 0; j < (kColVec ? 64 : 128); ++j) sum.s[j] = 0;
             // the next columns, of this or the next block, are on their way while kFp8Chunk are added
-            // (by 32 columns 114 us where 16 take 105, by 8 111: registers)
+            // (by 32 columns 114 us where 16 take 105, by 8 111: registers).  What a lane's wait gave is
+            // voted on at the block's end: all lanes go on or none (a vote in the wait took 105 us for 102)
             auto ready = [&]() {
                 ok = fp8_wait_short(done0 + 8 * stage, phase, abort_flag);
                 if (++stage == kStages) {
@@ -509,7 +510,7 @@ k_fp8_pair(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUt
                 return ok;
             };
             uint32_t r[2][kFp8Chunk];
-            ready();
+            ok = __all_sync(0xffffffffu, ready());
             tmem_ld_ahead(lane_addr + (uint32_t)acc * 256, r[0]);
 #pragma unroll 1
             for (int kb = 0; ok && kb < p.nkb; ++kb) {
@@ -555,7 +556,7 @@ k_fp8_pair(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUt
                         }
                     }
                 }
-                if (kColVec) __syncwarp();   // this place's scales are read
+                ok = __all_sync(0xffffffffu, ok);   // this place's scales are read, and all lanes go on or none
             }
             tmem_wait_ld();   // the last load, which nothing reads, before its registers serve again
             if (ok) fp8_put_rows(p, &tm_c, mw, n0, sum, box, lane);
@@ -744,12 +745,9 @@ k_fp8_tokens(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 const uint32_t at = (uint32_t)(kb % kFp8TokAhead);
                 const float s = fp8_lds(my_row + at * kRowStep);
                 const u64 s2 = f2(s, s);
-                if (!fp8_wait(tfull0 + 8 * acc, acc_phase, abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, fp8_wait(tfull0 + 8 * acc, acc_phase, abort_flag));
+                if (!ok) break;   // all lanes, or none
                 tc_fence_after();
-                __syncwarp();
                 uint32_t r[2][16];
                 tmem_ld_ahead(lane_addr + (uint32_t)(acc * kBN), r[0]);
 #pragma unroll

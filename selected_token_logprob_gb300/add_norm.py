@@ -154,14 +154,16 @@ class FusedAddRmsNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy, dh):
         h, weight, rstd = ctx.saved_tensors
+        residual = ctx.needs_input_grad[1]
         if dy is None:
-            return *once((dh, dh), dh), None, None
+            (dx,) = once((dh,), dh)
+            return dx, dx if residual else None, None, None
         dx, dw = fused_add_rms_norm_backward(
             _readable(dy), _readable(dh), h, weight, rstd,
             with_dweight=weight is not None and ctx.needs_input_grad[2])
         dw = dw if dw is None else dw.to(weight.dtype)
         dx, dw = once((dx, dw), dy, dh, h, weight)
-        return dx, dx if ctx.needs_input_grad[1] else None, dw, None
+        return dx, dx if residual else None, dw, None
 
 
 def fused_add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor | None = None,

@@ -27,6 +27,8 @@ def once(grads: tuple, *inputs) -> tuple:
     if not torch.is_grad_enabled():
         return grads
     given = [g for g in grads if g is not None]
+    if not given:
+        return grads
     made = _Once.apply(len(given), *given, *[t for t in inputs if t is not None])
     made = iter(made if isinstance(made, tuple) else (made,))
     return tuple(None if g is None else next(made) for g in grads)

@@ -46,3 +46,21 @@ def test_gradients(use, residual, weighted):
     want = torch.autograd.grad(loss(y, h), leaves, allow_unused=True)
     for p, q in zip(got, want):
         assert (p is None) == (q is None) and (p is None or torch.allclose(p, q, rtol=1e-12, atol=1e-14))
+
+
+class _NoGradient(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x):
+        return x * 1
+
+    @staticmethod
+    def backward(ctx, grad):
+        return None
+
+
+@pytest.mark.parametrize("create_graph", [False, True])
+def test_no_gradient_comes_back(create_graph):
+    x, r = (torch.randn((3, 5), dtype=torch.float64).requires_grad_() for _ in range(2))
+    y, h = flp.fused_add_rms_norm(x, r)
+    out = _NoGradient.apply(y).sum() + _NoGradient.apply(h).sum()
+    assert torch.autograd.grad(out, (x, r), create_graph=create_graph, allow_unused=True) == (None, None)

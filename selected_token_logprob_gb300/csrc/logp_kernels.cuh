@@ -376,9 +376,14 @@ k_logp_bwd(const __grid_constant__ LogpBwdArgs a) {
                 if (col0 + u * cs < v) bwd_store<D, kVecOut>(dr, col0 + u * cs, v, z);
             continue;
         }
-        if (bwd_far(l)) {   // the same for the whole row
+        auto leave = [&] {   // a row of a large |LSE|
             if constexpr (kFarInLoop) logp_bwd_far_row<D, kVecIn, kVecOut, kInPlace>(a, t, yt, l);
             else far = true;
+        };
+        // asked behind the loads, which then do not wait for l (8192 x 151936 BF16 735 us, 738 before them); in
+        // place that costs registers (720, 711 before them)
+        if (kInPlace && bwd_far(l)) {
+            leave();
             continue;
         }
         BwdRow r;
@@ -404,6 +409,10 @@ k_logp_bwd(const __grid_constant__ LogpBwdArgs a) {
 #pragma unroll
         for (int u = 0; u < kBwdUnitsPerThread; ++u)
             if (col0 + u * cs < v) bwd_load<D, kVecIn, kInPlace>(xr, col0 + u * cs, v, w[u]);
+        if (!kInPlace && bwd_far(l)) {
+            leave();
+            continue;
+        }
 #pragma unroll
         for (int u = 0; u < kBwdUnitsPerThread; ++u) {
             if (col0 + u * cs < v) {

@@ -14,8 +14,8 @@
 // Eight epilogue warps a CTA: a thread has one row and 128 columns, which is what its registers
 // hold.  The MMAs of a K block alone take 550 cycles; the epilogue bounds it at 750: 360 of 128
 // multiply-adds by two warps a scheduler, the rest the latencies of loads, signals and scales, which
-// two warps cannot hide from each other and more have no registers for.  4096 x 8192 x 4096 105 us, 2.6
-// PFLOP/s; B's scales a row are one more multiply a value and reads of shared memory, 162 us.
+// two warps cannot hide from each other and more have no registers for.  4096 x 8192 x 4096 103 us, 2.7
+// PFLOP/s; B's scales a row are one more multiply a value and reads of shared memory, 160 us.
 //
 // k_fp8_tokens, for a few rows of A (tokens): the operands change places, 128 rows of B a
 // tile and the tokens the MMA's N, so that B is streamed once at the memory's rate; with few
@@ -160,15 +160,8 @@ __device__ __forceinline__ void fp8_commit_both(uint32_t bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-// kN consecutive binary32 columns of this thread's lane, not waited for: the registers hold them
+// 16 consecutive binary32 columns of this thread's lane, not waited for: the registers hold them
 // after tmem_wait_ld alone, and what reads them is volatile too and stands behind it.
-__device__ __forceinline__ void tmem_ld_ahead(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_ld_ahead(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -329,7 +322,7 @@ __device__ __forceinline__ Fp8Tile fp8_tile(int64_t u, const Fp8Args& p) {
 }
 
 // B has a scale per 128 x 128 block (kB 0) or per row (1); per row, on 16-byte boundaries and a multiple
-// of 4 rows (2): a lane then copies four at once (4096 x 8192 x 4096 162 us, by single ones 176; both
+// of 4 rows (2): a lane then copies four at once (4096 x 8192 x 4096 160 us, by single ones 176; both
 // in one kernel 176).
 template <int kB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8PairThreads, 1)

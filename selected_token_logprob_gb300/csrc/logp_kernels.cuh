@@ -291,10 +291,11 @@ k_logp_merge(const float* __restrict__ pm, const float* __restrict__ ps,
 // logits at s = 1 (one rounding otherwise); exp(t) = 2^a (1 + c) with
 // a = t log2 e rounded and c = t - a ln 2 recovered by two fused multiply-adds
 // against a two-float ln 2 (the rounding error of a, carried to first order);
-// coef = -s g (1 - delta) ~ -s g exp(-delta) folds s, g and delta in once per
+// coef = -s g exp(-delta) folds s, g and delta in once per
 // row, with the exp2 bias correction.  Logits below about (LSE - 200) / s are raised to that bound first (their
 // exp is below e^-199, zero in binary32), which also keeps a -inf logit from
-// producing inf - inf.  The target column is s g (1 - p) = -s g expm1(s x - LSE),
+// producing inf - inf.  Rows of |LSE| from kBwdFarLse on, where the bound comes near LSE itself, are
+// computed without it (bwd_unit_far).  The target column is s g (1 - p) = -s g expm1(s x - LSE),
 // without cancellation.  Values below 2^-126 flush to zero.  Each thread loads
 // its eight units before computing any, so eight (FP32: sixteen) 16-byte loads
 // are in flight per thread.

@@ -6,18 +6,18 @@
 //   LSE = M + log S, logp = z_y - LSE, H = log S - T / S
 // (both terms of the entropy H are >= 0: nothing cancels), and the k largest logits,
 // of equal ones the lowest column first.  The tiles, the online sums and their merges are
-// those of the plain forward (logp_kernels.cuh), but a term's exponent is one fused
+// those of the plain forward (logp_kernels.cuh), of 1 to 16 tiles a row, but a term's exponent is one fused
 // multiply-add, x c - m c with c = s log2 e: what rounding m c loses is the same for a lane's
 // group and is given back to the group's sums.  (With the plain forward's difference and
 // two-float product a logit took 12.3 instructions, and the issue slots, not memory, were
-// the bound: 2048 x 151936 136 us, 108 so, of which 93 is memory.)  T is a second sum beside S, in units of
+// the bound: 2048 x 151936 136 us, 107 so, of which 93 is memory.)  T is a second sum beside S, in units of
 // log 2, and moved along when the running maximum grows:
 //   T <- 2^d (T + d S) for a shift of the maximum by d (log2 units).
 //
 // The forward is two kernels.  k_logp_topk_scan reads the logits once: per warp one
 // vocabulary tile of a row, giving the tile's (M, S, T) and, per lane and run of
 // `per` groups, the largest logit (a "slot" of 32 per elements; the group's maximum is
-// taken for the online sum anyway).  k_logp_topk_finish, a warp per row, merges the 16
+// taken for the online sum anyway).  k_logp_topk_finish, a warp per row, merges the
 // tiles and finds the top k: an element of the top k lies in a slot whose maximum is one
 // of the k largest, so that about k slots (a few KB, still in L2) are read again and
 // the rest of the row is not.
@@ -135,10 +135,13 @@ template <Dt D>
 constexpr float kTopkLowest = D == Dt::F16 ? -65504.f : D == Dt::BF16 ? -0x1.fep127f : -0x1.fffffep127f;
 template <Dt D>
 __device__ __forceinline__ uint32_t topk_floor(float fl) {
-    if constexpr (D == Dt::F32) return __float_as_uint(fl);
-    const uint32_t b = D == Dt::BF16 ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(fl))
-                                     : (uint32_t)__half_as_ushort(__float2half_rd(fl));
-    return b | (b << 16);
+    if constexpr (D == Dt::F32) {
+        return __float_as_uint(fl);
+    } else {
+        const uint32_t b = D == Dt::BF16 ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(fl))
+                                         : (uint32_t)__half_as_ushort(__float2half_rd(fl));
+        return b | (b << 16);
+    }
 }
 template <Dt D>
 __device__ __forceinline__ void topk_raise(Unit<D>& u, uint32_t fl) {

@@ -145,7 +145,7 @@ k_norm_dx_any(NormBwdArgs a) {
             const float g = to_f32(dy[i]) * norm_vec_at(a.w, i, 1.f);
             const float xh = (to_f32(x[i]) - mu) * rstd;
             const float r0 = a.add ? to_f32(static_cast<const T*>(a.add)[r * a.ld_add + i]) : 0.f;
-            dx[i] = from_f32<T>(a.add ? (g - c1 - xh * c2) * rstd + r0 : (g - c1 - xh * c2) * rstd);
+            dx[i] = from_f32<T>(a.add ? __fmaf_rn(g - c1 - xh * c2, rstd, r0) : (g - c1 - xh * c2) * rstd);
         }
     }
 }
@@ -793,8 +793,6 @@ k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
         for (int k = 0; k < NV; ++k) {
             const int i = k * kTpr + t;
             if (i < nvec && live) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) xh[k][j] = (g[k][j] - c1 - xh[k][j] * c2) * rstd;
                 if constexpr (kAdd) {
                     float e[V];
                     if constexpr (kAligned) {
@@ -803,8 +801,12 @@ k_norm_bwd(NormBwdArgs a, int parts, int grid_fold) {
 #pragma unroll
                         for (int j = 0; j < V; ++j) e[j] = i * V + j < d ? to_f32(add_row[i * V + j]) : 0.f;
                     }
+                    // fused in either form: the bits of a row do not depend on where it lies
 #pragma unroll
-                    for (int j = 0; j < V; ++j) xh[k][j] += e[j];
+                    for (int j = 0; j < V; ++j) xh[k][j] = __fmaf_rn(g[k][j] - c1 - xh[k][j] * c2, rstd, e[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) xh[k][j] = (g[k][j] - c1 - xh[k][j] * c2) * rstd;
                 }
                 if constexpr (kAligned) norm_stg(dx + i * V, norm_pack<T, V>(xh[k]));
                 else norm_sts(out + i * V * (uint32_t)sizeof(T), norm_pack<T, V>(xh[k]));

@@ -224,8 +224,9 @@ struct Fp8Sums<kN, true> {
 
 // 32 rows of kN sums (a row a lane) to rows [m, m + 32), columns [n, n + kN) of C, by way of boxes
 // of 32 rows x 128 bytes in shared memory: chunk j of 16 bytes of row r at place j ^ (r mod 8), as
-// the tensor map's 128-byte swizzle has it.  With p.vec the boxes (two by turns) go out by TMA,
-// rows and columns past C left out; else a row a turn, by elements.  (Each lane storing its own
+// the tensor map's 128-byte swizzle has it.  With p.vec the boxes (two by turns) go out by TMA, rows
+// past C left out, columns by whole 16 bytes: a box that C's last column cuts inside such a piece would
+// reach behind it, and goes as without p.vec, a row a turn, by elements.  (Each lane storing its own
 // row took 6700 cycles a 128 x 256 tile, 32 lines an instruction; the warps' own stores of
 // whole lines out of the boxes 3500, 16 us of 122 at 4096 x 8192 x 4096; by TMA 13.)
 constexpr uint32_t kFp8Box = 32 * 128;
@@ -263,7 +264,7 @@ __device__ __forceinline__ void fp8_put_rows(const Fp8Args& p, const CUtensorMap
             }
             sts_v4(box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) * 16)), w[0], w[1], w[2], w[3]);
         }
-        if (p.vec) {
+        if (p.vec && (n0 + cols <= p.N || p.N % (wide ? 4 : 8) == 0)) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {

@@ -164,10 +164,11 @@ flp_status make_tmap_bf16(CUtensorMap* m, const void* ptr, int64_t rows, int64_t
 // Tensor map of an FP32 row-major [rows, ld] output matrix whose first `cols`
 // columns are written: boxes of 32 x 32 with 128-byte swizzle (the layout the
 // contraction's epilogue stages).  False when the layout does not allow one
-// (base not 16-byte aligned, row stride not a multiple of 16 bytes).
+// (base not 16-byte aligned, row stride or width not a multiple of 16 bytes: a
+// store leaves columns past the width out by whole 16 bytes).
 bool make_tmap_f32_out(CUtensorMap* m, void* ptr, int64_t rows, int64_t cols, int64_t ld) {
     const EncodeTiledFn fn = encode_tiled();
-    if (!fn || !aligned16(ptr) || (ld * 4) % 16 != 0 || rows < 1 || cols < 1) return false;
+    if (!fn || !aligned16(ptr) || (ld * 4) % 16 != 0 || (cols * 4) % 16 != 0 || rows < 1 || cols < 1) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * 4};
     const cuuint32_t box[2] = {32, 32};
